@@ -60,7 +60,8 @@ extern "C" {
 #endif
 
 /* element types */
-typedef enum pkv_dtype { PKV_F32 = 0, PKV_BF16 = 1 } pkv_dtype;
+/* PKV_Q4: 4-bit rows, for the calls that name it ("4-bit pools" below) */
+typedef enum pkv_dtype { PKV_F32 = 0, PKV_BF16 = 1, PKV_Q4 = 2 } pkv_dtype;
 
 /* status codes */
 #define PKV_OK 0
@@ -471,6 +472,100 @@ int paged_bm_free_blocks(const pkv_block_manager* bm, int32_t* stack_out, int64_
  */
 int paged_copy_blocks(void* k_cache, void* v_cache, const int32_t* src, const int32_t* dst,
                       int32_t n_pairs, const pkv_geom* geom, cudaStream_t stream);
+
+/*
+ * 4-bit pools -- K and V held in 4 bits per value ("Sayfalı dikkat": the cache
+ * is what bounds the batch; here it takes 5 bits per value with its scales
+ * instead of 16).  geom->dtype is PKV_Q4 in every call below, head_dim 64 or 128.
+ * Layout:
+ *   pools  uint8 [num_blocks, num_kv_heads, block_size, R], R = 5 * head_dim / 8
+ *          bytes per (token, KV head) row: the row of (block, token t, head h)
+ *          is at ((block * Hkv + h) * B + t) * R.  Slots, block tables and
+ *          lengths mean what they mean for the other pools (slot = block * B + t).
+ *   row    head_dim / 2 bytes of codes, then for each of the NG = head_dim / 32
+ *          groups of 32 dims a scale s and an offset z, both bf16 (s first).
+ *          The 16-bit unit r * NG + g of the codes (r < 8, little-endian) holds
+ *          the 4-bit codes u of dims 32 g + 4 r .. 32 g + 4 r + 3, lowest bits
+ *          first.  The value of code u in group g is s_g * (u - 8) + z_g.
+ * A page is copied by paged_copy_blocks with a geom whose pages have the same
+ * number of bytes (e.g. one head, block_size 1, head_dim Hkv * B * R / 2, bf16).
+ */
+
+/*
+ * paged_kv_write_q4 -- paged_kv_write into 4-bit pools: for every token n with
+ * slot_mapping[n] >= 0 its rows k[n], v[n] ([num_tokens, Hkv, d] of kv_dtype,
+ * PKV_F32 or PKV_BF16) are stored at that slot.  Per group with minimum lo and
+ * maximum hi:
+ *   s = bf16((hi - lo) / 15)        z = bf16((lo / 2 + hi / 2) + s / 2)
+ *   u = min(max(rint((x - z) * (1 / s)) + 8, 0), 15)
+ * every operation in fp32 with one rounding, so that the stored bytes are the
+ * same on every run.  s below 2^-126 is stored as 0 (every value reads as z).  A
+ * value is off by at most s / 2 plus what the bf16 rounding of s and z leaves
+ * at the ends of the range (2^-8 of |lo| + |hi|).  A group that holds a NaN or
+ * an infinity, or spans more than fp32 holds, reads back as NaN.  Duplicate
+ * slots, negative slots and slots past the pool as in paged_kv_write.  k, v and
+ * the pools 16-byte aligned.
+ */
+int paged_kv_write_q4(const void* k, const void* v, int32_t kv_dtype, const int32_t* slot_mapping,
+                      int64_t num_tokens, void* k_cache, void* v_cache, const pkv_geom* geom,
+                      cudaStream_t stream);
+
+/*
+ * paged_kv_read_q4 -- rows of 4-bit pools as values: row n of k_out and v_out
+ * ([num_tokens, Hkv, d] of kv_dtype, rounded once) holds what slot_mapping[n]
+ * stores; a negative slot gives a row of zeros, and so does a slot past the pool
+ * (PKV_FLAG_BAD_SLOT).  The same slot may appear more than once.  With the slots
+ * of all keys of a step's requests (paged_build_slot_mapping) this yields the
+ * packed K/V that paged_varlen_prefill takes with block_table == NULL: prompts
+ * over a 4-bit cache.  k_out, v_out and the pools 16-byte aligned.
+ */
+int paged_kv_read_q4(const void* k_cache, const void* v_cache, const int32_t* slot_mapping,
+                     int64_t num_tokens, void* k_out, void* v_out, int32_t kv_dtype,
+                     const pkv_geom* geom, cudaStream_t stream);
+
+/*
+ * paged_decode_q4 -- paged_decode over 4-bit pools: one query per sequence (q,
+ * out [batch, Hq, d] of q_dtype, PKV_F32 or PKV_BF16), cache_seqlens[b] keys
+ * each, read through block_table row b; 0 when cache_seqlens[b] == 0.  The
+ * values are used as stored (4-bit codes, bf16 scales); scores, softmax
+ * statistics and sums are fp32.
+ * Supported: any Hq / Hkv; head_dim 64 or 128; any block_size; batch <= 4096.
+ * workspace: paged_decode_q4_workspace_size(batch, q_dtype, geom) bytes, 256-byte
+ * aligned, contents irrelevant on entry, as for paged_decode (may be NULL when
+ * that size is 0).  A length below 0 or past the table counts as the nearest
+ * valid one (PKV_FLAG_BAD_LENGTH); keys of a bad page are skipped
+ * (PKV_FLAG_BAD_BLOCK).
+ */
+size_t paged_decode_q4_workspace_size(int32_t batch, int32_t q_dtype, const pkv_geom* geom);
+int paged_decode_q4(const void* q, int32_t q_dtype, const void* k_cache, const void* v_cache,
+                    const int32_t* block_table, int32_t max_blocks_per_seq,
+                    const int32_t* cache_seqlens, int32_t batch, float scale, void* out,
+                    void* workspace, size_t workspace_bytes, const pkv_geom* geom,
+                    cudaStream_t stream);
+
+/*
+ * paged_kv_compact -- keep selected tokens of each sequence, moved together in
+ * place (token eviction; the accepted path of a draft tree), after which the
+ * pages behind the new length can be released.  Any pool: PKV_F32, PKV_BF16 or
+ * PKV_Q4.  Sequence b keeps its positions below start[b] (start == NULL: 0) as
+ * they are, and of the others those in keep[cu_keep[b] .. cu_keep[b+1]-1]: the
+ * K and V rows of the i-th of them move to position start[b] + i, through
+ * block_table row b ([batch, max_blocks_per_seq]).  The i-th entry of a list
+ * must be >= start[b] + i, which any ascending list is.  cu_keep [batch + 1]
+ * starts at 0 and ends at total_keep, the length of keep.  seqlens_out [batch] (may be
+ * NULL) receives start[b] + (number kept), for the next decode; it may be the
+ * lengths' own array (no lengths are read).
+ * Rows at and behind the new end keep their old contents.  The pages written
+ * must belong to one sequence only (copy shared ones first, paged_copy_blocks).
+ * An entry below start[b] + i or past the table sets PKV_FLAG_BAD_LENGTH, and a
+ * bad table entry PKV_FLAG_BAD_BLOCK; that row is not moved.  A start below 0,
+ * bounds outside keep, or a new length past the table set PKV_FLAG_BAD_LENGTH,
+ * and nothing of that sequence is moved.
+ */
+int paged_kv_compact(void* k_cache, void* v_cache, const int32_t* block_table,
+                     int32_t max_blocks_per_seq, const int32_t* start, const int32_t* keep,
+                     int32_t total_keep, const int32_t* cu_keep, int32_t batch,
+                     int32_t* seqlens_out, const pkv_geom* geom, cudaStream_t stream);
 
 /* paged_status_string -- static text for a PKV_* status code. */
 const char* paged_status_string(int status);

@@ -13,6 +13,7 @@ from ._binding import (  # noqa: F401
     LIB_PATH,
     PKV_BF16,
     PKV_F32,
+    PKV_Q4,
     PKV_FLAG_BAD_BLOCK,
     PKV_FLAG_BAD_LENGTH,
     PKV_FLAG_BAD_SEQ,
@@ -34,4 +35,11 @@ from ._binding import (  # noqa: F401
     paged_kv_write_positions,
     paged_varlen_prefill,
     paged_varlen_prefill_workspace_size,
+    paged_decode_q4,
+    paged_decode_q4_workspace_size,
+    paged_kv_compact,
+    paged_kv_read_q4,
+    paged_kv_write_q4,
+    q4_cache_shape,
+    q4_geom_of,
 )

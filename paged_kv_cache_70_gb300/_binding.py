@@ -18,7 +18,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libpagedkv.so")
 
-PKV_F32, PKV_BF16 = 0, 1
+PKV_F32, PKV_BF16, PKV_Q4 = 0, 1, 2
 PKV_FLAG_BAD_BLOCK = 1 << 0
 PKV_FLAG_BAD_SLOT = 1 << 1
 PKV_FLAG_BAD_LENGTH = 1 << 2
@@ -54,6 +54,11 @@ EXPORTED = (
     "paged_mixed_step_workspace_size",
     "paged_mixed_step",
     "paged_mixed_step_one_launch",
+    "paged_kv_write_q4",
+    "paged_kv_read_q4",
+    "paged_decode_q4_workspace_size",
+    "paged_decode_q4",
+    "paged_kv_compact",
 )
 PKV_ERR_NO_SPACE = -5
 
@@ -168,6 +173,17 @@ def load_library(path: str | None = None):
         lib.paged_mixed_step_one_launch.restype = ctypes.c_int
         lib.paged_copy_blocks.argtypes = [vp, vp, vp, vp, i32, gp, vp]
         lib.paged_copy_blocks.restype = ctypes.c_int
+        lib.paged_kv_write_q4.argtypes = [vp, vp, i32, vp, i64, vp, vp, gp, vp]
+        lib.paged_kv_write_q4.restype = ctypes.c_int
+        lib.paged_kv_read_q4.argtypes = [vp, vp, vp, i64, vp, vp, i32, gp, vp]
+        lib.paged_kv_read_q4.restype = ctypes.c_int
+        lib.paged_decode_q4_workspace_size.argtypes = [i32, i32, gp]
+        lib.paged_decode_q4_workspace_size.restype = sz
+        lib.paged_decode_q4.argtypes = [vp, i32, vp, vp, vp, i32, vp, i32, ctypes.c_float, vp, vp,
+                                        sz, gp, vp]
+        lib.paged_decode_q4.restype = ctypes.c_int
+        lib.paged_kv_compact.argtypes = [vp, vp, vp, i32, vp, vp, i32, vp, i32, vp, gp, vp]
+        lib.paged_kv_compact.restype = ctypes.c_int
         lib.paged_status_string.argtypes = [ctypes.c_int]
         lib.paged_status_string.restype = ctypes.c_char_p
         if path is None:
@@ -563,14 +579,18 @@ class BlockManager:
 def paged_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, src: torch.Tensor,
                       dst: torch.Tensor) -> None:
     """Block dst[i] of both pools becomes a copy of block src[i] (int32 CUDA
-    tensors): the copies a copy-on-write needs."""
+    tensors): the copies a copy-on-write needs.  4-bit pools as well."""
     _cuda_contig("k_cache", k_cache)
     _cuda_contig("v_cache", v_cache, k_cache.dtype)
     _cuda_contig("src", src, torch.int32)
     _cuda_contig("dst", dst, torch.int32)
     if src.numel() != dst.numel() or v_cache.shape != k_cache.shape:
         raise ValueError("shape mismatch")
-    g = geom_of(k_cache, k_cache.shape[2])
+    if k_cache.dtype == torch.uint8:  # a 4-bit page, moved as one row of 16-bit words
+        q4_geom_of(k_cache, k_cache.shape[1])
+        g = Geom(1, 1, k_cache[0].numel() // 2 if len(k_cache) else 1, 1, len(k_cache), PKV_BF16)
+    else:
+        g = geom_of(k_cache, k_cache.shape[2])
     with torch.cuda.device(k_cache.device):
         st = load_library().paged_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(src), _ptr(dst),
                                               src.numel(), ctypes.byref(g), _stream(k_cache))
@@ -647,3 +667,147 @@ def paged_mixed_step(k_cache: torch.Tensor, v_cache: torch.Tensor, scale: float,
                 workspace.numel(), ctypes.byref(g), _stream(k_cache))
     _check("paged_mixed_step_one_launch" if one_launch else "paged_mixed_step", rc)
     return pout, dout
+
+
+# ---- 4-bit pools ---------------------------------------------------------------
+
+def q4_cache_shape(num_blocks: int, block_size: int, num_kv_heads: int,
+                   head_dim: int) -> tuple[int, int, int, int]:
+    """Shape of a 4-bit K or V pool (uint8): [num_blocks, num_kv_heads,
+    block_size, 5 * head_dim / 8]."""
+    if head_dim not in (64, 128):
+        raise ValueError("4-bit pools hold head_dim 64 or 128")
+    return num_blocks, num_kv_heads, block_size, head_dim * 5 // 8
+
+
+def q4_geom_of(k_cache: torch.Tensor, num_heads: int) -> Geom:
+    """pkv_geom of a 4-bit pool [num_blocks, num_kv_heads, block_size, 5 d / 8]."""
+    if k_cache.dtype != torch.uint8 or k_cache.dim() != 4 or k_cache.shape[3] not in (40, 80):
+        raise ValueError("a 4-bit pool is uint8 [num_blocks, Hkv, block_size, 5 * head_dim / 8]")
+    nb, hkv, bs, r = k_cache.shape
+    return Geom(num_heads, hkv, r * 8 // 5, bs, nb, PKV_Q4)
+
+
+def paged_kv_write_q4(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
+                      k_cache: torch.Tensor, v_cache: torch.Tensor) -> None:
+    """In-place write of k/v [N, Hkv, d] rows (fp32 or bf16) into 4-bit pools
+    (q4_cache_shape) at slot_mapping; negative slots are skipped."""
+    _cuda_contig("k", k)
+    _cuda_contig("v", v, k.dtype)
+    _cuda_contig("slot_mapping", slot_mapping, torch.int32)
+    _cuda_contig("k_cache", k_cache)
+    _cuda_contig("v_cache", v_cache, torch.uint8)
+    g = q4_geom_of(k_cache, k_cache.shape[1])
+    n = k.shape[0]
+    if k.shape != v.shape or k.shape[1:] != (g.num_kv_heads, g.head_dim) or \
+            v_cache.shape != k_cache.shape:
+        raise ValueError("shape mismatch between k/v rows and the pools")
+    if slot_mapping.numel() != n:
+        raise ValueError("slot_mapping must have one entry per token row")
+    with torch.cuda.device(k.device):
+        st = load_library().paged_kv_write_q4(
+            _ptr(k), _ptr(v), _dtype_code(k), _ptr(slot_mapping), n, _ptr(k_cache), _ptr(v_cache),
+            ctypes.byref(g), _stream(k))
+    _check("paged_kv_write_q4", st)
+
+
+def paged_kv_read_q4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor,
+                     dtype: torch.dtype = torch.bfloat16, k_out: torch.Tensor | None = None,
+                     v_out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The values [N, Hkv, d] that 4-bit pools hold at slot_mapping [N], in
+    ``dtype`` (fp32 or bf16); rows of zeros at negative slots."""
+    _cuda_contig("slot_mapping", slot_mapping, torch.int32)
+    _cuda_contig("k_cache", k_cache)
+    _cuda_contig("v_cache", v_cache, torch.uint8)
+    g = q4_geom_of(k_cache, k_cache.shape[1])
+    if v_cache.shape != k_cache.shape:
+        raise ValueError("shape mismatch between the pools")
+    n = slot_mapping.numel()
+    shape = (n, g.num_kv_heads, g.head_dim)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=k_out.dtype, device=k_cache.device)
+    _cuda_contig("k_out", k_out)
+    _cuda_contig("v_out", v_out, k_out.dtype)
+    if k_out.shape != shape or v_out.shape != shape:
+        raise ValueError("k_out / v_out must be [N, Hkv, d]")
+    with torch.cuda.device(k_cache.device):
+        st = load_library().paged_kv_read_q4(
+            _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), n, _ptr(k_out), _ptr(v_out),
+            _dtype_code(k_out), ctypes.byref(g), _stream(k_cache))
+    _check("paged_kv_read_q4", st)
+    return k_out, v_out
+
+
+def paged_decode_q4_workspace_size(batch: int, q_heads: int, q_dtype: torch.dtype,
+                                   k_cache: torch.Tensor) -> int:
+    g = q4_geom_of(k_cache, q_heads)
+    code = _dtype_code(torch.empty(0, dtype=q_dtype))
+    with torch.cuda.device(k_cache.device):
+        return int(load_library().paged_decode_q4_workspace_size(batch, code, ctypes.byref(g)))
+
+
+def paged_decode_q4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    block_table: torch.Tensor, cache_seqlens: torch.Tensor,
+                    scale: float | None = None, out: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """One query token per sequence (q [batch, Hq, d], fp32 or bf16) over its
+    cache_seqlens[b] keys in 4-bit pools."""
+    _cuda_contig("q", q)
+    _cuda_contig("k_cache", k_cache)
+    _cuda_contig("v_cache", v_cache, torch.uint8)
+    _cuda_contig("block_table", block_table, torch.int32)
+    _cuda_contig("cache_seqlens", cache_seqlens, torch.int32)
+    batch, hq, d = q.shape
+    g = q4_geom_of(k_cache, hq)
+    if d != g.head_dim or v_cache.shape != k_cache.shape or block_table.shape[0] < batch or \
+            cache_seqlens.numel() < batch:
+        raise ValueError("shape mismatch")
+    if out is None:
+        out = torch.empty_like(q)
+    _cuda_contig("out", out, q.dtype)
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
+    code = _dtype_code(q)
+    lib = load_library()
+    with torch.cuda.device(q.device):
+        need = int(lib.paged_decode_q4_workspace_size(batch, code, ctypes.byref(g)))
+        if workspace is None and need:
+            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+        st = lib.paged_decode_q4(_ptr(q), code, _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
+                                 block_table.shape[1], _ptr(cache_seqlens), batch, scale,
+                                 _ptr(out), _ptr(workspace),
+                                 0 if workspace is None else workspace.numel(), ctypes.byref(g),
+                                 _stream(q))
+    _check("paged_decode_q4", st)
+    return out
+
+
+def paged_kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                     keep: torch.Tensor, cu_keep: torch.Tensor,
+                     start: torch.Tensor | None = None,
+                     seqlens_out: torch.Tensor | None = None) -> None:
+    """Keep the positions keep[cu_keep[b]:cu_keep[b + 1]] of every sequence b
+    (and those below start[b]), moved together in place from start[b] on; pools
+    in fp32, bf16 or 4 bits.  seqlens_out receives the new lengths."""
+    _cuda_contig("k_cache", k_cache)
+    _cuda_contig("v_cache", v_cache, k_cache.dtype)
+    for n, t in (("block_table", block_table), ("keep", keep), ("cu_keep", cu_keep),
+                 ("start", start), ("seqlens_out", seqlens_out)):
+        if t is not None:
+            _cuda_contig(n, t, torch.int32)
+    batch = cu_keep.numel() - 1
+    if k_cache.shape != v_cache.shape or batch < 0 or block_table.shape[0] < batch or \
+            (start is not None and start.numel() < batch) or \
+            (seqlens_out is not None and seqlens_out.numel() < batch):
+        raise ValueError("shape mismatch")
+    g = q4_geom_of(k_cache, k_cache.shape[1]) if k_cache.dtype == torch.uint8 \
+        else geom_of(k_cache, k_cache.shape[2])
+    with torch.cuda.device(k_cache.device):
+        st = load_library().paged_kv_compact(
+            _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1], _ptr(start),
+            _ptr(keep), keep.numel(), _ptr(cu_keep), batch, _ptr(seqlens_out), ctypes.byref(g),
+            _stream(k_cache))
+    _check("paged_kv_compact", st)

@@ -224,4 +224,48 @@ cudaError_t launch_prefill(const DeviceInfo& dev, const void* q, const void* k_c
                            int block_size, int64_t num_blocks, unsigned int* err,
                            cudaStream_t stream);
 
+// ---- 4-bit pools (q4_cache.cu, q4_decode.cu) ---------------------------------
+// Quantised write and its inverse by slot_mapping; src_dtype / dst_dtype: the
+// rows' pkv_dtype (PKV_F32 or PKV_BF16).
+cudaError_t launch_q4_write(const void* k, const void* v, int src_dtype, const int32_t* slots,
+                            int64_t num_tokens, void* k_cache, void* v_cache, int hkv, int d,
+                            int block_size, int64_t num_slots, unsigned int* err,
+                            cudaStream_t stream);
+cudaError_t launch_q4_read(const void* k_cache, const void* v_cache, const int32_t* slots,
+                           int64_t num_tokens, void* k, void* v, int dst_dtype, int hkv, int d,
+                           int block_size, int64_t num_slots, unsigned int* err,
+                           cudaStream_t stream);
+
+struct Q4DecodePlan {
+    size_t ws_bytes;  // workspace bytes needed
+};
+
+// Returns false when the geometry is not supported.
+bool plan_q4_decode(const DeviceInfo& dev, int32_t batch, int hq, int hkv, int d, int block_size,
+                    int q_dtype, Q4DecodePlan* plan);
+
+cudaError_t launch_q4_decode(const Q4DecodePlan& plan, const void* q, const void* k_cache,
+                             const void* v_cache, const int32_t* table, int32_t max_blocks,
+                             const int32_t* seqlens, int32_t batch, float scale, void* out,
+                             void* workspace, int hq, int hkv, int d, int block_size,
+                             int64_t num_blocks, int q_dtype, unsigned int* err,
+                             cudaStream_t stream);
+
+// ---- compaction (compact.cu) ---------------------------------------------------
+// A token's row is `pieces` runs of piece_bytes, head_bytes apart; tokens are
+// token_bytes apart within a page, pages page_bytes apart.
+struct CompactLaunch {
+    void* k_cache;
+    void* v_cache;
+    const int32_t* table;
+    const int32_t* start;
+    const int32_t* keep;
+    const int32_t* cu_keep;
+    int32_t* seqlens_out;
+    int64_t page_bytes, token_bytes, head_bytes, piece_bytes, pieces;
+    int64_t num_blocks;
+    int32_t max_blocks, block_size, batch, total;
+};
+cudaError_t launch_compact(const CompactLaunch& c, unsigned int* err, cudaStream_t stream);
+
 }  // namespace pkv

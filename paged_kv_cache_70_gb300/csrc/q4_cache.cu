@@ -1,0 +1,282 @@
+// q4_cache.cu -- rows into and out of 4-bit K/V pools (format: q4.cuh).
+//
+// Write ("自己来实现一个", _update_paged_kv_cache_kernel, with a 4-bit cache
+// dtype): for every token n with s = slot_mapping[n] >= 0 and every KV head, each
+// group of 32 dims x of the row is stored as
+//   s = bf16((hi - lo) / 15)   z = bf16((lo / 2 + hi / 2) + s / 2)
+//   u = min(max(rint((x - z) * (1 / s)) + 8, 0), 15)
+// with lo, hi the group's minimum and maximum and every operation rounded to
+// fp32.  Values lie on both sides of z: u = 0 .. 15 spans z - 8s .. z + 7s, i.e.
+// lo .. hi.  s below 2^-126 is stored as 0 with every value z.  A NaN makes lo
+// and hi NaN and an infinity makes hi - lo infinite or NaN, so that such a group
+// reads back as NaN instead of as a plausible number.
+// Read: row n of the outputs is the values s (u - 8) + z at slot_mapping[n],
+// rounded once to the output's type; zeros for a negative slot.
+//
+// Both move bytes: one warp per token and pool (grid.y: K, V), a lane per 8
+// dims.  The four lanes of a group find lo and hi with two xor shuffles; two
+// more shuffles exchange 16-bit code units between the groups of a head, so
+// that the codes leave (and arrive) as whole 32-bit words, consecutive over the
+// lanes.
+#include <algorithm>
+
+#include "common.cuh"
+#include "launch.h"
+#include "q4.cuh"
+
+namespace pkv {
+
+namespace {
+
+constexpr int kQ4Warps = 4;   // tokens per CTA
+constexpr int kQ4Unroll = 4;  // 32-lane steps of a row in flight per warp
+
+struct Q4Rows {
+    const int32_t* slots;
+    int64_t num_tokens;
+    int64_t num_slots;
+    FastDiv block;   // tokens per page
+    int32_t hkv;
+    unsigned int* err;
+};
+
+// lane's place in its 32-lane step: head row, group, chunk of 8 dims
+template <int NG>
+__device__ __forceinline__ void lane_place(int vec, int* head, int* g, int* c) {
+    *head = vec / (4 * NG);
+    *g = (vec / 4) % NG;
+    *c = vec % 4;
+}
+
+// byte offset of head `h`'s row at `slot`
+template <int NG>
+__device__ __forceinline__ int64_t row_offset(const Q4Rows& a, int32_t page, int32_t at, int h) {
+    return (((int64_t)page * a.hkv + h) * a.block.d + at) * q4_row_bytes(NG * kQ4Group);
+}
+
+// word w of lane (g, c) holds its 8 codes as two units (r = 2c low, 2c + 1 high).
+// Exchange between the groups of a head: lane j of the NG lanes with the same
+// c gets the j-th 32-bit word of chunk c of the row.
+template <int NG>
+__device__ __forceinline__ uint32_t units_to_words(uint32_t w, int lane, int g) {
+    const int src = lane - 4 * g + 4 * (NG == 4 ? 2 * (g & 1) : 0);
+    const uint32_t a = __shfl_sync(0xffffffffu, w, src);
+    const uint32_t b = __shfl_sync(0xffffffffu, w, src + 4);
+    return __byte_perm(a, b, (NG == 4 ? g >> 1 : g) ? 0x7632 : 0x5410);
+}
+// the inverse
+template <int NG>
+__device__ __forceinline__ uint32_t words_to_units(uint32_t w, int lane, int g) {
+    const int src = lane - 4 * g + 4 * (NG == 4 ? g >> 1 : 0);
+    const uint32_t a = __shfl_sync(0xffffffffu, w, src);
+    const uint32_t b = __shfl_sync(0xffffffffu, w, src + (NG == 4 ? 8 : 4));
+    return __byte_perm(a, b, (g & 1) ? 0x7632 : 0x5410);
+}
+
+template <bool F32>
+struct Raw8 {
+    uint4 a, b;  // b: fp32 only
+};
+
+template <bool F32>
+__device__ __forceinline__ void load8(const void* base, int64_t elem, Raw8<F32>& x) {
+    if constexpr (F32) {
+        const uint4* p = reinterpret_cast<const uint4*>(static_cast<const float*>(base) + elem);
+        x.a = __ldcs(p);
+        x.b = __ldcs(p + 1);
+    } else {
+        x.a = __ldcs(reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(base) + elem));
+    }
+}
+
+template <bool F32>
+__device__ __forceinline__ void widen8(const Raw8<F32>& r, float* x) {
+    if constexpr (F32) {
+        x[0] = __uint_as_float(r.a.x); x[1] = __uint_as_float(r.a.y);
+        x[2] = __uint_as_float(r.a.z); x[3] = __uint_as_float(r.a.w);
+        x[4] = __uint_as_float(r.b.x); x[5] = __uint_as_float(r.b.y);
+        x[6] = __uint_as_float(r.b.z); x[7] = __uint_as_float(r.b.w);
+    } else {
+        x[0] = bf16lo(r.a.x); x[1] = bf16hi(r.a.x); x[2] = bf16lo(r.a.y); x[3] = bf16hi(r.a.y);
+        x[4] = bf16lo(r.a.z); x[5] = bf16hi(r.a.z); x[6] = bf16lo(r.a.w); x[7] = bf16hi(r.a.w);
+    }
+}
+
+// minimum and maximum that keep a NaN
+__device__ __forceinline__ float min_nan(float a, float b) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
+    return y;
+}
+
+template <int NG, bool F32>
+__global__ void __launch_bounds__(kQ4Warps * 32)
+q4_write_kernel(const void* __restrict__ k, const void* __restrict__ v, const Q4Rows a,
+                unsigned char* __restrict__ kc, unsigned char* __restrict__ vc) {
+    PKV_DEPENDENT_PROLOGUE();
+    constexpr int D = NG * kQ4Group;
+    const int lane = threadIdx.x & 31;
+    const int64_t n = (int64_t)blockIdx.x * kQ4Warps + (threadIdx.x >> 5);
+    if (n >= a.num_tokens) return;
+    const void* src = blockIdx.y ? v : k;
+    unsigned char* pool = blockIdx.y ? vc : kc;
+    const int vecs = a.hkv * (D / 8);  // lanes' worth of dims in a token's row
+    const int64_t e0 = n * a.hkv * D;
+    const int32_t slot = __ldg(a.slots + n);
+    if (slot < 0) return;
+    if (slot >= a.num_slots) {
+        if (lane == 0) flag_error(a.err, PKV_FLAG_BAD_SLOT);
+        return;
+    }
+    const int32_t page = (int32_t)a.block.quot((uint32_t)slot);
+    const int32_t at = slot - page * (int32_t)a.block.d;
+    for (int v0 = 0; v0 < vecs; v0 += 32 * kQ4Unroll) {
+        Raw8<F32> raw[kQ4Unroll];
+#pragma unroll
+        for (int u = 0; u < kQ4Unroll; ++u) {
+            const int vec = v0 + 32 * u + lane;
+            raw[u].a = make_uint4(0, 0, 0, 0);
+            raw[u].b = make_uint4(0, 0, 0, 0);
+            if (vec < vecs) load8<F32>(src, e0 + (int64_t)vec * 8, raw[u]);
+        }
+#pragma unroll
+        for (int u = 0; u < kQ4Unroll; ++u) {
+            const int vec = v0 + 32 * u + lane;
+            if (v0 + 32 * u >= vecs) break;  // warp-uniform
+            int head, g, c;
+            lane_place<NG>(vec, &head, &g, &c);
+            float x[8];
+            widen8<F32>(raw[u], x);
+            float lo = x[0], hi = x[0];
+#pragma unroll
+            for (int i = 1; i < 8; ++i) {
+                lo = min_nan(lo, x[i]);
+                hi = max_nan(hi, x[i]);
+            }
+#pragma unroll
+            for (int off = 1; off < 4; off <<= 1) {
+                lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
+                hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
+            }
+            // one rounding per operation (no contraction): the codes are the format's
+            uint32_t sb = f32_to_bf16_bits(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+            float s = __uint_as_float(sb << 16);
+            if (s < 1.17549435e-38f) {  // 2^-126; a NaN stays
+                s = 0.f;
+                sb = 0;
+            }
+            const uint32_t zb = f32_to_bf16_bits(
+                __fadd_rn(__fadd_rn(0.5f * lo, 0.5f * hi), 0.5f * s));
+            const float z = __uint_as_float(zb << 16);
+            const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
+            uint32_t w = 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float t = rintf(__fmul_rn(__fsub_rn(x[i], z), inv)) + 8.f;
+                w |= (uint32_t)fminf(fmaxf(t, 0.f), 15.f) << (4 * i);
+            }
+            w = units_to_words<NG>(w, lane, g);
+            if (vec < vecs) {
+                unsigned char* row = pool + row_offset<NG>(a, page, at, head);
+                *reinterpret_cast<uint32_t*>(row + c * (4 * NG) + g * 4) = w;
+                if (c == 0) *reinterpret_cast<uint32_t*>(row + D / 2 + g * 4) = sb | (zb << 16);
+            }
+        }
+    }
+}
+
+template <int NG, bool F32>
+__global__ void __launch_bounds__(kQ4Warps * 32)
+q4_read_kernel(const unsigned char* __restrict__ kc, const unsigned char* __restrict__ vc,
+               const Q4Rows a, void* __restrict__ k, void* __restrict__ v) {
+    PKV_DEPENDENT_PROLOGUE();
+    constexpr int D = NG * kQ4Group;
+    const int lane = threadIdx.x & 31;
+    const int64_t n = (int64_t)blockIdx.x * kQ4Warps + (threadIdx.x >> 5);
+    if (n >= a.num_tokens) return;
+    const unsigned char* pool = blockIdx.y ? vc : kc;
+    void* dst = blockIdx.y ? v : k;
+    const int vecs = a.hkv * (D / 8);
+    const int64_t e0 = n * a.hkv * D;
+    const int32_t slot = __ldg(a.slots + n);
+    const bool real = slot >= 0 && slot < a.num_slots;
+    if (slot >= a.num_slots && lane == 0) flag_error(a.err, PKV_FLAG_BAD_SLOT);
+    const int32_t page = real ? (int32_t)a.block.quot((uint32_t)slot) : 0;
+    const int32_t at = real ? slot - page * (int32_t)a.block.d : 0;
+    for (int v0 = 0; v0 < vecs; v0 += 32 * kQ4Unroll) {
+        uint32_t words[kQ4Unroll], sz[kQ4Unroll];
+#pragma unroll
+        for (int u = 0; u < kQ4Unroll; ++u) {
+            const int vec = v0 + 32 * u + lane;
+            words[u] = sz[u] = 0;
+            if (vec < vecs && real) {
+                int head, g, c;
+                lane_place<NG>(vec, &head, &g, &c);
+                const unsigned char* row = pool + row_offset<NG>(a, page, at, head);
+                words[u] = *reinterpret_cast<const uint32_t*>(row + c * (4 * NG) + g * 4);
+                sz[u] = *reinterpret_cast<const uint32_t*>(row + D / 2 + g * 4);
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kQ4Unroll; ++u) {
+            const int vec = v0 + 32 * u + lane;
+            if (v0 + 32 * u >= vecs) break;  // warp-uniform
+            const uint32_t w = words_to_units<NG>(words[u], lane, (vec / 4) % NG);
+            const float s = bf16lo(sz[u]), z = bf16hi(sz[u]);
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i)  // u - 8 times s is exact: one rounding
+                x[i] = fmaf((float)((w >> (4 * i)) & 15u) - 8.f, s, z);
+            if (vec >= vecs) continue;
+            const int64_t e = e0 + (int64_t)vec * 8;
+            if constexpr (F32) {
+                float4* o = reinterpret_cast<float4*>(static_cast<float*>(dst) + e);
+                o[0] = make_float4(x[0], x[1], x[2], x[3]);
+                o[1] = make_float4(x[4], x[5], x[6], x[7]);
+            } else {
+                *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + e) =
+                    make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
+                               pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+            }
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_q4_write(const void* k, const void* v, int src_dtype, const int32_t* slots,
+                            int64_t num_tokens, void* k_cache, void* v_cache, int hkv, int d,
+                            int block_size, int64_t num_slots, unsigned int* err,
+                            cudaStream_t stream) {
+    if (num_tokens == 0) return cudaSuccess;
+    const Q4Rows a{slots, num_tokens, num_slots, FastDiv((uint32_t)block_size), hkv, err};
+    const dim3 grid((unsigned)((num_tokens + kQ4Warps - 1) / kQ4Warps), 2);
+    const bool f32 = src_dtype == PKV_F32;
+    auto kern = d == 128 ? (f32 ? q4_write_kernel<4, true> : q4_write_kernel<4, false>)
+                         : (f32 ? q4_write_kernel<2, true> : q4_write_kernel<2, false>);
+    return launch_dependent(kern, grid, dim3(kQ4Warps * 32), 0, stream, k, v, a,
+                            static_cast<unsigned char*>(k_cache),
+                            static_cast<unsigned char*>(v_cache));
+}
+
+cudaError_t launch_q4_read(const void* k_cache, const void* v_cache, const int32_t* slots,
+                           int64_t num_tokens, void* k, void* v, int dst_dtype, int hkv, int d,
+                           int block_size, int64_t num_slots, unsigned int* err,
+                           cudaStream_t stream) {
+    if (num_tokens == 0) return cudaSuccess;
+    const Q4Rows a{slots, num_tokens, num_slots, FastDiv((uint32_t)block_size), hkv, err};
+    const dim3 grid((unsigned)((num_tokens + kQ4Warps - 1) / kQ4Warps), 2);
+    const bool f32 = dst_dtype == PKV_F32;
+    auto kern = d == 128 ? (f32 ? q4_read_kernel<4, true> : q4_read_kernel<4, false>)
+                         : (f32 ? q4_read_kernel<2, true> : q4_read_kernel<2, false>);
+    return launch_dependent(kern, grid, dim3(kQ4Warps * 32), 0, stream,
+                            static_cast<const unsigned char*>(k_cache),
+                            static_cast<const unsigned char*>(v_cache), a, k, v);
+}
+
+}  // namespace pkv
