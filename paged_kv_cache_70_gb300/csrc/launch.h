@@ -237,12 +237,21 @@ cudaError_t launch_q4_read(const void* k_cache, const void* v_cache, const int32
                            cudaStream_t stream);
 
 struct Q4DecodePlan {
-    size_t ws_bytes;  // workspace bytes needed
+    int qn;           // query heads a warp's columns hold (2, 4 or 8)
+    int no;           // warps' worth of query heads per KV head
+    int hc;           // KV heads per CTA
+    int wh;           // warps that share a head and its queries
+    int head_groups;  // grid.y = Hkv / hc
+    int ctas;         // grid.x (CTAs along the keys)
+    int tile;         // keys per stage
+    int stages;
+    size_t smem_bytes;
+    size_t ws_bytes;  // workspace bytes needed (the same for every max_blocks)
 };
 
 // Returns false when the geometry is not supported.
-bool plan_q4_decode(const DeviceInfo& dev, int32_t batch, int hq, int hkv, int d, int block_size,
-                    int q_dtype, Q4DecodePlan* plan);
+bool plan_q4_decode(const DeviceInfo& dev, int32_t batch, int32_t max_blocks, int hq, int hkv,
+                    int d, int block_size, int q_dtype, Q4DecodePlan* plan);
 
 cudaError_t launch_q4_decode(const Q4DecodePlan& plan, const void* q, const void* k_cache,
                              const void* v_cache, const int32_t* table, int32_t max_blocks,

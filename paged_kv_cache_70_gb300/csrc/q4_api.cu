@@ -71,7 +71,7 @@ size_t paged_decode_q4_workspace_size(int32_t batch, int32_t q_dtype, const pkv_
     DeviceInfo dev;
     if (pkv::current_device_info(&dev) != cudaSuccess) return 0;
     pkv::Q4DecodePlan plan;
-    if (!pkv::plan_q4_decode(dev, batch, geom->num_heads, geom->num_kv_heads, geom->head_dim,
+    if (!pkv::plan_q4_decode(dev, batch, 0, geom->num_heads, geom->num_kv_heads, geom->head_dim,
                              geom->block_size, q_dtype, &plan))
         return 0;
     return plan.ws_bytes;
@@ -93,8 +93,8 @@ int paged_decode_q4(const void* q, int32_t q_dtype, const void* k_cache, const v
     DeviceInfo dev;
     if (pkv::current_device_info(&dev) != cudaSuccess) return PKV_ERR_CUDA;
     pkv::Q4DecodePlan plan;
-    if (!pkv::plan_q4_decode(dev, batch, geom->num_heads, geom->num_kv_heads, geom->head_dim,
-                             geom->block_size, q_dtype, &plan))
+    if (!pkv::plan_q4_decode(dev, batch, max_blocks_per_seq, geom->num_heads, geom->num_kv_heads,
+                             geom->head_dim, geom->block_size, q_dtype, &plan))
         return PKV_ERR_UNSUPPORTED;
     if (plan.ws_bytes &&
         (!workspace || workspace_bytes < plan.ws_bytes || !aligned(workspace, 256)))

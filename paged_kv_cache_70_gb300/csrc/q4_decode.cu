@@ -1,11 +1,53 @@
 // q4_decode.cu -- paged decode (one query token per sequence) over a 4-bit cache.
 //
 //   out[b,h] = sum_j softmax_j(scale * q[b,h] . k_j) v_j,  j < cache_seqlens[b],
-// with k_j, v_j the values of the 4-bit rows (format: q4.cuh), read through block
-// table row b, merged by the online-softmax rule.
+// with k_j, v_j the values s (u - 8) + z of the 4-bit rows (format: q4.cuh), read
+// through block table row b and merged by the online-softmax rule ("11. Paged
+// attention 与 online softmax" §11.1-§11.2).  Per group of 32 dims
+//   score:   q . k_j = sum_g s_g(j) sum_{i in g} q_i (u_ji - 8) + z_g(j) sum_{i in g} q_i
+//   output:  o_i     = sum_j p_j s_g(j) (u_ji - 8) + sum_j p_j z_g(j)
+// so both are products of small whole numbers with 16-bit operands, and scales and
+// offsets enter once per group, key and query instead of once per value.
 //
-// One CTA per (sequence, query head); its warps take every fourth key and
-// merge their states at the end.
+// What bounds it: 160 bytes per key and KV head at d = 128 (K and V), 3.2 times
+// fewer than bf16.  At HBM's rate an SM gets a key of one head every ~7 cycles; on
+// the CUDA cores one query head alone would need 8 warp instructions of FMAs per
+// key plus 16 for unpacking, and the queries of a group multiply the first.  So
+// the products run on the tensor cores, from registers: a lane unpacks codes
+// straight into the operand fragments of mma.m16n8k16 (a nibble becomes the bf16
+// 128 + u with one shift and one logic operation per PAIR of codes), keys (score)
+// or dims (output) as the 16 rows and queries as the 8 columns.  tcgen05 would
+// need the unpacked operand written to shared or tensor memory first, four times
+// the bytes that came in, only to multiply it by 2 to 8 columns.
+//
+//  * Columns.  A group of QN = 2, 4 or 8 query heads (the next size up from
+//    Hq / Hkv; more heads: several warps) shares the 8 columns with 8 / QN groups
+//    of dims: column (g, q) holds query q with zeros outside group g, so one
+//    accumulator tile keeps the groups' sums apart without a product for the
+//    zeros that would not have been issued anyway.  The score tile is scaled per
+//    group, summed over the groups by a reduce-scatter among the 4 lanes of a row
+//    and each lane takes the exponential of its own share.
+//  * Offsets.  sum (u - 8) x = sum (128 + u) x - 136 sum x: the score's
+//    accumulator starts at -136 sum q; for the output a second product of the
+//    constant -136 with the same weights follows each first one, so the two cancel
+//    step by step and nothing large is carried through a long sum.  With fp32
+//    queries 136 is subtracted from the operand (exactly), and queries and
+//    weights enter as three bf16 parts (24 bits), three products each.
+//  * Weights are rounded to bf16 after the V scale is multiplied in (once, 2^-9
+//    relative at most, as every bf16 attention path here does); the offsets' part
+//    sum p z and all sums stay fp32.
+//  * Reference maximum: lags.  State and output are rescaled only when a score
+//    exceeds the reference by more than 2^8 (one vote per 16 keys).
+//  * Work split as in decode.cu: the tiles of all sequences in one list, cut into
+//    equal contiguous shares, one per CTA; each (CTA, sequence) piece leaves a
+//    partial state that a second kernel merges.  A producer warp brings tiles of K
+//    and V into a ring of stages, one bulk copy per page piece and head; consumer
+//    warps own (head, 8 queries) and take 16 keys at a time.
+//  * Keys of a page outside the pool are skipped and flagged; rows past the length
+//    never enter: their scales count as 0 and their scores as -inf, whatever the
+//    page holds there.  Every wait is time-limited.
+#include <algorithm>
+
 #include "common.cuh"
 #include "launch.h"
 #include "q4.cuh"
@@ -14,7 +56,15 @@ namespace pkv {
 
 namespace {
 
-constexpr int kWarps = 4;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kGrow = 8.f;  // rescale when a score passes the reference by 2^8
+constexpr int kMaxStages = 8;
+constexpr int kHeader = 512;  // barriers and stage tags
+
+// consumer warps: 16 leave 120 registers a thread; fp32 queries keep 3 parts
+// of every operand and run 8
+template <bool F32>
+__host__ __device__ constexpr int consumer_warps() { return F32 ? 8 : 16; }
 
 struct Q4DecodeArgs {
     const void* q;
@@ -22,106 +72,888 @@ struct Q4DecodeArgs {
     const unsigned char* vc;
     const int32_t* table;
     const int32_t* seqlens;
-    void* out;
+    float* part_o;     // [ctas + batch][hq][D]
+    float* part_ml;    // [ctas + batch][hq][2]
+    int32_t* tstart;   // [batch + 1]
     unsigned int* err;
     int64_t num_blocks;
     float qscale;  // scale * log2(e)
-    int32_t max_blocks, hq, hkv, block_size;
+    int32_t max_blocks, batch, hq, hkv, block_size;
+    int32_t hc;      // KV heads per CTA
+    int32_t no;      // warps' worth of query heads per KV head
+    int32_t wh;      // warps that share a head and its queries (16 keys each)
+    int32_t tile;    // keys per stage
+    int32_t stages;
 };
 
-template <int NG, bool F32>
-__global__ void __launch_bounds__(kWarps * 32) q4_decode_kernel(const Q4DecodeArgs a) {
-    PKV_DEPENDENT_PROLOGUE();
-    constexpr int D = NG * kQ4Group, R = q4_row_bytes(D), UNITS = 8 * NG;
-    __shared__ float so[kWarps][D], sm[kWarps], sl[kWarps];
-    const int b = blockIdx.x, h = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int kvh = h / (a.hq / a.hkv);
+// one stage's description, written by the producer
+struct Tag {
+    int32_t seq;   // sequence
+    int32_t rows;  // keys, -1: no more stages
+    int32_t last;  // the piece of the sequence ends here
+    int32_t bad;   // first key's position if a page was out of range, else -1
+};
+
+// ---- the split's shares: tile t of sequence b sits at t + b + 1 on a line (a
+// sequence's start counts as one tile) that is cut into equal parts
+__device__ __forceinline__ int32_t share_len(int32_t total, int32_t batch, int ctas) {
+    return max(1, (total + batch + ctas - 1) / ctas);
+}
+__device__ __forceinline__ int32_t share_first(const int32_t* tstart, int batch, int64_t x) {
+    int lo = 0, hi = batch;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if ((int64_t)tstart[mid + 1] + mid >= x) hi = mid; else lo = mid + 1;
+    }
+    if (lo >= batch) return tstart[batch];
+    return (int32_t)max((int64_t)tstart[lo], x - lo - 1);
+}
+
+__host__ __device__ constexpr size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
+
+// a warp's merged state in shared memory: 8 NT output values, 2 maxima and 2 sums
+// per lane
+__host__ __device__ constexpr size_t state_bytes(int nt) { return (size_t)(8 * nt + 4) * 128; }
+
+__device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+// codes i of both halves of x as two bf16: 128 + u, or (EXACT) u - 8
+template <bool EXACT>
+__device__ __forceinline__ uint32_t codes(uint32_t x, int i) {
+    uint32_t y = ((x >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
+    if constexpr (EXACT) {
+        const uint32_t c = 0xC308C308u;  // -136
+        const uint32_t one = 0x3F803F80u;
+        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(y), "r"(one), "r"(c));
+    }
+    return y;
+}
+
+// the k-th bf16 part of x, removed from it
+__device__ __forceinline__ uint32_t split_pair(float& a, float& b) {
+    const uint32_t p = pack_bf16x2(a, b);
+    a -= bf16lo(p);
+    b -= bf16hi(p);
+    return p;
+}
+
+// where the 16 keys of a step sit: MMA row r + 8 half of the score product, and
+// k index (2c, 2c+1, 2c+8, 2c+9 for i = 0..3) of the output product.  Chosen so
+// that the lanes of one shared-memory access touch all banks once at row
+// strides of 80 (d = 128) and 40 bytes (d = 64).
+template <int NG>
+__device__ __forceinline__ int score_key(int r, int half) {
+    return NG == 4 ? (r >> 1) + 4 * (r & 1) + 8 * half : 4 * (r & 3) + (r >> 2) + 2 * half;
+}
+template <int NG>
+__device__ __forceinline__ int output_key(int c, int i) {
+    return NG == 4 ? 2 * c + (i & 1) + 8 * (i >> 1) : 4 * c + i;
+}
+// the (r, half) whose score_key is `key`
+template <int NG>
+__device__ __forceinline__ void score_row(int key, int* r, int* half) {
+    if (NG == 4) {
+        *half = key >> 3;
+        *r = 2 * (key & 3) + ((key >> 2) & 1);
+    } else {
+        *half = (key >> 1) & 1;
+        *r = (key >> 2) + 4 * (key & 1);
+    }
+}
+
+template <int NG, int QN, bool F32>
+__global__ void __launch_bounds__((consumer_warps<F32>() + 1) * 32, 1)
+q4_split_kernel(const Q4DecodeArgs a) {
+    constexpr int WC = consumer_warps<F32>();
+    constexpr int D = NG * kQ4Group, R = q4_row_bytes(D);
+    constexpr int CPT = 8 / QN;                    // groups per column tile
+    constexpr int NT = NG > CPT ? NG / CPT : 1;    // column tiles
+    constexpr int MT = 2 * NG;                     // 16-dim tiles of the output
+    constexpr int PARTS = F32 ? 3 : 1;
+    constexpr int NP = QN == 2 ? 1 : 2;            // queries a lane takes exponentials for
+    constexpr int NV = QN == 8 ? 2 : 1;            // score rows a lane takes them for
+    extern __shared__ __align__(128) unsigned char smem[];
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem);
+    uint64_t* empty = full + kMaxStages;
+    uint64_t* merge_bar = empty + kMaxStages;  // [2]
+    Tag* tags = reinterpret_cast<Tag*>(smem + 256);
+    int32_t* tstart = reinterpret_cast<int32_t*>(smem + kHeader);
+    unsigned char* scratch = smem + kHeader + up((size_t)(a.batch + 1) * 4, 128);
+    const int units = a.hc * a.no;  // (head, queries) of the CTA
+    unsigned char* ring = scratch + (size_t)units * (a.wh - 1) * state_bytes(NT);
+    __shared__ int32_t warp_sum[WC + 1];
+
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    const int S = a.stages, T = a.tile;
+    const size_t half_bytes = (size_t)a.hc * T * R;  // K (or V) of a stage
+    const int active = units * a.wh;                 // consumer warps at work
+    if (tid == 0) {
+        for (int s = 0; s < S; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], active);
+        }
+        mbar_init(&merge_bar[0], units * (a.wh - 1) + 1);
+        mbar_init(&merge_bar[1], units);
+        fence_barrier_init();
+    }
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+
+    // ---- plan: tile starts of the sequences (an exclusive scan of their tiles)
     const int64_t cap = (int64_t)a.max_blocks * a.block_size;
-    int32_t L = a.seqlens[b];
-    if (L < 0 || L > cap) {
-        if (h == 0 && threadIdx.x == 0) flag_error(a.err, PKV_FLAG_BAD_LENGTH);
-        L = L < 0 ? 0 : (int32_t)cap;
+    const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0;
+    {
+        constexpr int N = (WC + 1) * 32;
+        const int per = (a.batch + N - 1) / N;
+        const int lo = tid * per, hi = min(lo + per, a.batch);
+        int32_t sum = 0;
+        for (int b = lo; b < hi; ++b) {
+            const int32_t L = __ldg(a.seqlens + b);
+            if (first_cta && (L < 0 || L > cap)) flag_error(a.err, PKV_FLAG_BAD_LENGTH);
+            const int32_t n = (int32_t)min((int64_t)max(L, 0), cap);
+            tstart[b + 1] = (n + T - 1) / T;
+            sum += tstart[b + 1];
+        }
+        int32_t inc = sum;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int32_t y = __shfl_up_sync(0xffffffffu, inc, off);
+            if (lane >= off) inc += y;
+        }
+        if (lane == 31) warp_sum[warp] = inc;
+        __syncthreads();
+        int32_t run = inc - sum;
+        for (int w = 0; w < warp; ++w) run += warp_sum[w];
+        for (int b = lo; b < hi; ++b) {
+            run += tstart[b + 1];
+            tstart[b + 1] = run;
+        }
+        if (tid == 0) tstart[0] = 0;
+        __syncthreads();
     }
-    const int unit = lane < UNITS ? lane : 0;  // this lane's 4 dims
-    const int g = unit % NG, dim = g * kQ4Group + 4 * (unit / NG);
-    const int64_t qi = ((int64_t)b * a.hq + h) * D + dim;
-    float q[4], o[4] = {0.f, 0.f, 0.f, 0.f}, m = -INFINITY, l = 0.f;
+    const int32_t total = tstart[a.batch];
+    if (first_cta) {
+        for (int b = tid; b <= a.batch; b += blockDim.x) a.tstart[b] = tstart[b];
+    }
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    const int32_t len = share_len(total, a.batch, gridDim.x);
+    const int32_t t0 = share_first(tstart, a.batch, (int64_t)blockIdx.x * len);
+    const int32_t t1 = share_first(tstart, a.batch, (int64_t)(blockIdx.x + 1) * len);
+    if (t0 >= t1) return;
+    const int head0 = blockIdx.y * a.hc;
+
+    if (warp == WC) {
+        // ------------------------------ producer ------------------------------
+        const uint64_t pol = l2_evict_first_policy();
+        int b = 0;  // the sequence of tile t0
+        {
+            int lo = 0, hi = a.batch;
+            while (lo < hi) {
+                const int mid = (lo + hi) >> 1;
+                if (tstart[mid + 1] <= t0) lo = mid + 1; else hi = mid;
+            }
+            b = lo;
+        }
+        int32_t L = (int32_t)min((int64_t)max(__ldg(a.seqlens + b), 0), cap);
+        const uint32_t inv_hc = 65536u / a.hc + 1;  // i / hc for i < 512, hc <= 16
+        const int64_t head_bytes = (int64_t)a.block_size * R;
+        int32_t k = 0;
+        bool stop = false;
+        // page ids of a tile's first 32 pages, one tile ahead
+        int32_t next_page = -1;
+        auto fetch = [&](int bb, int32_t p0, int32_t p1) {
+            const int32_t pg = p0 / a.block_size + lane;
+            return (int64_t)pg * a.block_size < p1
+                       ? __ldg(a.table + (int64_t)bb * a.max_blocks + pg) : -1;
+        };
+        {
+            const int32_t p0 = (t0 - tstart[b]) * T;
+            next_page = fetch(b, p0, min(L, p0 + T));
+        }
+        for (int32_t t = t0; t < t1 && !stop; ++t) {
+            const int32_t p0 = (t - tstart[b]) * T, p1 = min(L, p0 + T);
+            const int seq = b;
+            int32_t page = next_page;
+            const bool seq_end = t + 1 == tstart[b + 1];
+            if (t + 1 < t1) {  // the next tile's sequence and pages
+                if (seq_end) {
+                    do ++b; while (tstart[b + 1] <= t + 1);
+                    L = (int32_t)min((int64_t)max(__ldg(a.seqlens + b), 0), cap);
+                }
+                const int32_t q0 = (t + 1 - tstart[b]) * T;
+                next_page = fetch(b, q0, min(L, q0 + T));
+            }
+            const int s = k % S;
+            bool ok = true;
+            if (lane == 0) ok = mbar_wait(&empty[s], ((k / S) & 1) ^ 1, a.err);
+            if (!__all_sync(0xffffffffu, ok)) {
+                stop = true;
+                break;
+            }
+            ++k;
+            unsigned char* kd = ring + (size_t)s * 2 * half_bytes;
+            const int32_t pg0 = p0 / a.block_size;
+            const int np = (p1 - 1) / a.block_size - pg0 + 1;
+            // the bytes that will arrive: a first pass over the pages when they
+            // are more than the prefetched 32
+            uint32_t bytes = 0;
+            bool bad = false;
+            for (int c0 = 0; c0 < np; c0 += 32) {
+                const int32_t pg = pg0 + c0 + lane;
+                const int32_t id = c0 == 0 ? page
+                                   : (c0 + lane < np ? __ldg(a.table + (int64_t)seq * a.max_blocks + pg) : -1);
+                if (c0 + lane < np) {
+                    const int32_t lo = max(p0, pg * a.block_size);
+                    const int32_t hi = min((int64_t)p1, (int64_t)(pg + 1) * a.block_size);
+                    if (id < 0 || id >= a.num_blocks) bad = true;
+                    else bytes += (uint32_t)up((size_t)(hi - lo) * R, 16);
+                }
+            }
+            bad = __any_sync(0xffffffffu, bad);
+            bytes = __reduce_add_sync(0xffffffffu, bytes) * 2 * a.hc;
+            if (lane == 0) {
+                if (bad) flag_error(a.err, PKV_FLAG_BAD_BLOCK);
+                tags[s] = Tag{seq, p1 - p0, (seq_end || t + 1 == t1) ? 1 : 0, bad ? p0 : -1};
+                mbar_arrive_expect_tx(&full[s], bytes);
+            }
+            __syncwarp();
+            for (int c0 = 0; c0 < np; c0 += 32) {
+                if (c0 > 0) {
+                    const int32_t pg = pg0 + c0 + lane;
+                    page = c0 + lane < np ? __ldg(a.table + (int64_t)seq * a.max_blocks + pg) : -1;
+                }
+                const int n = min(32, np - c0) * a.hc;
+                for (int i0 = 0; i0 < n; i0 += 32) {
+                    const int i = min(i0 + lane, n - 1);
+                    const int p = (int)((i * inv_hc) >> 16), h = i - p * a.hc;
+                    const int32_t id = __shfl_sync(0xffffffffu, page, p);
+                    if (i0 + lane >= n || id < 0 || id >= a.num_blocks) continue;
+                    const int32_t pg = pg0 + c0 + p;
+                    const int32_t lo = max(p0, pg * a.block_size);
+                    const int32_t hi = min((int64_t)p1, (int64_t)(pg + 1) * a.block_size);
+                    const int64_t src = ((int64_t)id * a.hkv + head0 + h) * head_bytes +
+                                        (int64_t)(lo - pg * a.block_size) * R;
+                    unsigned char* dst = kd + ((size_t)h * T + (lo - p0)) * R;
+                    const uint32_t n16 = (uint32_t)up((size_t)(hi - lo) * R, 16);
+                    bulk_g2s(dst, a.kc + src, n16, &full[s], pol);
+                    bulk_g2s(dst + half_bytes, a.vc + src, n16, &full[s], pol);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane != 0) return;
+        if (!stop) {  // the closing stage
+            const int s = k % S;
+            if (mbar_wait(&empty[s], ((k / S) & 1) ^ 1, a.err)) {
+                tags[s].rows = -1;
+                mbar_arrive(&full[s]);
+                ++k;
+            }
+        }
+        // no copy may be in flight when the CTA exits (see decode.cu)
+        for (int32_t j = k > S ? k - S : 0; j < k; ++j)
+            if (!mbar_wait(&full[j % S], (j / S) & 1, a.err)) break;
+        return;
+    }
+    if (warp >= active) return;
+
+    // ------------------------------- consumers --------------------------------
+    const int unit = warp % units, rank = warp / units;
+    const int hc = unit % a.hc, oct = unit / a.hc;
+    const int r = lane >> 2, c = lane & 3;
+    const int G = a.hq / a.hkv;
+    const int q0 = oct * QN;                        // first query of this warp in its group
+    const int nq = min(QN, G - q0);                 // queries it has
+    const int qh0 = (head0 + hc) * G + q0;          // first query head
+    const int my_q = r % QN;                        // query of this lane's column (n = r)
+
+    // lanes that hold the weights of this lane's keys and query
+    int src_lane[4];
+#pragma unroll
     for (int i = 0; i < 4; ++i) {
-        q[i] = F32 ? static_cast<const float*>(a.q)[qi + i]
-                   : bf16lo(static_cast<const uint16_t*>(a.q)[qi + i]);
-        q[i] = lane < UNITS ? q[i] * a.qscale : 0.f;
+        int sr, half;
+        score_row<NG>(output_key<NG>(c, i), &sr, &half);
+        if (QN == 2) src_lane[i] = sr * 4 + half * 2 + my_q;
+        else if (QN == 4) src_lane[i] = sr * 4 + half * 2 + (my_q >> 1);
+        else src_lane[i] = (sr * 4 + (my_q >> 1)) | (half << 8);
     }
-    for (int32_t j = warp; j < L; j += kWarps) {
-        const int32_t page = a.table[(int64_t)b * a.max_blocks + j / a.block_size];
-        if (page < 0 || page >= a.num_blocks) {
-            if (lane == 0) flag_error(a.err, PKV_FLAG_BAD_BLOCK);
-            continue;
+
+    uint32_t qf[PARTS][NG][4];  // score product's columns: 2 k-steps of 2 words per group
+    float qs[NT][2];            // sum of q over the group of columns 2c, 2c + 1
+    float o[MT][4], zacc[NT], m[NP], l[NP];
+    int loaded = -1;
+    bool fresh = false;
+    int merges = 0;
+
+    for (int32_t k = 0;; ++k) {
+        const int s = k % S;
+        if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (k / S) & 1, a.err))) break;
+        const Tag tag = tags[s];
+        if (tag.rows < 0) break;
+        if (tag.seq != loaded) {  // the sequence's queries
+            loaded = tag.seq;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int g_col = j * CPT + r / QN;  // the group of this lane's column
+                float x[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] = 0.f;
+                if (g_col < NG && my_q < nq) {
+                    const int64_t at = ((int64_t)tag.seq * a.hq + qh0 + my_q) * D + g_col * 32 + c * 8;
+                    if constexpr (F32) {
+                        const float4* p = reinterpret_cast<const float4*>(
+                            static_cast<const float*>(a.q) + at);
+                        const float4 u = __ldg(p), v = __ldg(p + 1);
+                        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+                        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+                    } else {
+                        const uint4 w = __ldg(reinterpret_cast<const uint4*>(
+                            static_cast<const uint16_t*>(a.q) + at));
+                        x[0] = bf16lo(w.x); x[1] = bf16hi(w.x); x[2] = bf16lo(w.y);
+                        x[3] = bf16hi(w.y); x[4] = bf16lo(w.z); x[5] = bf16hi(w.z);
+                        x[6] = bf16lo(w.w); x[7] = bf16hi(w.w);
+                    }
+                }
+                float sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+                qs[j][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
+                qs[j][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) w[e] = split_pair(x[e], x[e + 4]);
+#pragma unroll
+                    for (int gi = 0; gi < CPT; ++gi) {
+                        const int g = j * CPT + gi;
+                        if (g >= NG) continue;
+                        const bool mine = g_col == g;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) qf[part][g][e] = mine ? w[e] : 0u;
+                    }
+                }
+            }
+            fresh = false;
         }
-        const int64_t row = (((int64_t)page * a.hkv + kvh) * a.block_size + j % a.block_size) * R;
-        const uint16_t ku = *reinterpret_cast<const uint16_t*>(a.kc + row + 2 * unit);
-        const uint32_t ks = *reinterpret_cast<const uint32_t*>(a.kc + row + D / 2 + 4 * g);
-        const uint16_t vu = *reinterpret_cast<const uint16_t*>(a.vc + row + 2 * unit);
-        const uint32_t vs = *reinterpret_cast<const uint32_t*>(a.vc + row + D / 2 + 4 * g);
-        float s = 0.f;
-        for (int i = 0; i < 4; ++i)
-            s += q[i] * fmaf((float)((ku >> (4 * i)) & 15) - 8.f, bf16lo(ks), bf16hi(ks));
-        if (lane >= UNITS) s = 0.f;
-        for (int off = 16; off > 0; off >>= 1) s += __shfl_xor_sync(0xffffffffu, s, off);
-        const float mn = fmaxf(m, s);
-        const float c = m == -INFINITY ? 0.f : ex2(m - mn);
-        const float p = s == -INFINITY ? 0.f : ex2(s - mn);  // a NaN score stays one
-        l = l * c + p;
-        for (int i = 0; i < 4; ++i)
-            o[i] = o[i] * c +
-                   p * fmaf((float)((vu >> (4 * i)) & 15) - 8.f, bf16lo(vs), bf16hi(vs));
-        m = mn;
-    }
-    if (lane < UNITS)
-        for (int i = 0; i < 4; ++i) so[warp][dim + i] = o[i];
-    if (lane == 0) {
-        sm[warp] = m;
-        sl[warp] = l;
-    }
-    __syncthreads();
-    float M = -INFINITY;
-    for (int w = 0; w < kWarps; ++w) M = fmaxf(M, sm[w]);
-    for (int i = threadIdx.x; i < D; i += kWarps * 32) {
-        float L1 = 0.f, acc = 0.f;
-        for (int w = 0; w < kWarps; ++w) {
-            const float c = sm[w] == -INFINITY ? 0.f : ex2(sm[w] - M);
-            L1 += sl[w] * c;
-            acc += so[w][i] * c;
+        if (!fresh) {  // a new piece: empty state
+            fresh = true;
+#pragma unroll
+            for (int i = 0; i < MT; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) zacc[j] = 0.f;
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                m[i] = -INFINITY;
+                l[i] = 0.f;
+            }
         }
-        acc = L1 == 0.f ? 0.f : acc / L1;
-        const int64_t oi = ((int64_t)b * a.hq + h) * D + i;
-        if (F32) static_cast<float*>(a.out)[oi] = acc;
-        else static_cast<uint16_t*>(a.out)[oi] = f32_to_bf16_bits(acc);
+        const unsigned char* ks = ring + (size_t)s * 2 * half_bytes + (size_t)hc * T * R;
+        const unsigned char* vs = ks + half_bytes;
+        for (int base = rank * 16; base < tag.rows; base += a.wh * 16) {
+            const bool whole = base + 16 <= tag.rows && tag.bad < 0;
+            auto valid = [&](int key) {  // (only asked when not whole)
+                if (base + key >= tag.rows) return false;
+                if (tag.bad < 0) return true;
+                const int32_t id = __ldg(a.table + (int64_t)tag.seq * a.max_blocks +
+                                         (tag.bad + base + key) / a.block_size);
+                return id >= 0 && id < a.num_blocks;
+            };
+            // ---- scores: 16 keys x 8 columns
+            const unsigned char* kr[2] = {ks + (base + score_key<NG>(r, 0)) * R,
+                                          ks + (base + score_key<NG>(r, 1)) * R};
+            float sc[NT][4];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                sc[j][0] = sc[j][2] = F32 ? 0.f : -136.f * qs[j][0];
+                sc[j][1] = sc[j][3] = F32 ? 0.f : -136.f * qs[j][1];
+            }
+            uint32_t kw[2][NG];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if constexpr (NG == 4) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(kr[h] + 16 * c);
+                    kw[h][0] = w.x; kw[h][1] = w.y; kw[h][2] = w.z; kw[h][3] = w.w;
+                } else {
+                    const uint2 w = *reinterpret_cast<const uint2*>(kr[h] + 8 * c);
+                    kw[h][0] = w.x; kw[h][1] = w.y;
+                }
+            }
+            uint32_t ksz[NT][2];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int g = j * CPT + 2 * c / QN;
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    ksz[j][h] = g < NG ? *reinterpret_cast<const uint32_t*>(kr[h] + D / 2 + 4 * g) : 0u;
+            }
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                uint32_t x[2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+                    x[h] = __byte_perm(kw[h][NG == 4 ? g >> 1 : 0], kw[h][NG == 4 ? 2 + (g >> 1) : 1],
+                                       (g & 1) ? 0x7632 : 0x5410);
+#pragma unroll
+                for (int st = 0; st < 2; ++st) {
+                    const uint32_t af[4] = {codes<F32>(x[0], 2 * st), codes<F32>(x[1], 2 * st),
+                                            codes<F32>(x[0], 2 * st + 1), codes<F32>(x[1], 2 * st + 1)};
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part)
+                        mma(sc[g / CPT], af, qf[part][g][2 * st], qf[part][g][2 * st + 1]);
+                }
+            }
+            // scale per group, sum over the groups: v[row half][query 2c, 2c+1]
+            float v[2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                float2 acc = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const float ss = bf16lo(ksz[j][h]), zz = bf16hi(ksz[j][h]);
+                    acc = ffma2(make_float2(ss, ss), make_float2(sc[j][2 * h], sc[j][2 * h + 1]), acc);
+                    acc = ffma2(make_float2(zz, zz), make_float2(qs[j][0], qs[j][1]), acc);
+                }
+                v[h][0] = acc.x;
+                v[h][1] = acc.y;
+            }
+            float p[NV][NP];  // this lane's scores, then weights
+            if constexpr (QN == 8) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) p[h][i] = v[h][i];
+            } else {
+                // lanes c and c ^ 2 hold other groups of the same queries: each
+                // keeps one row half
+                const bool up_half = c & 2;
+                float w[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const float got = __shfl_xor_sync(0xffffffffu, up_half ? v[0][i] : v[1][i], 2);
+                    w[i] = (up_half ? v[1][i] : v[0][i]) + got;
+                }
+                if constexpr (QN == 4) {
+                    p[0][0] = w[0];
+                    p[0][1] = w[1];
+                } else {  // lanes c and c ^ 1: each keeps one query
+                    const float got = __shfl_xor_sync(0xffffffffu, (c & 1) ? w[0] : w[1], 1);
+                    p[0][0] = ((c & 1) ? w[1] : w[0]) + got;
+                }
+            }
+            bool grow = false;
+#pragma unroll
+            for (int h = 0; h < NV; ++h) {
+                const bool ok = whole || valid(score_key<NG>(r, QN == 8 ? h : c >> 1));
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    p[h][i] = ok ? p[h][i] * a.qscale : -INFINITY;
+                    grow |= p[h][i] > m[i] + kGrow;
+                }
+            }
+            if (__any_sync(0xffffffffu, grow)) {  // move the reference to the running maximum
+                float f[NP];
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    float mx = p[0][i];
+                    if constexpr (NV == 2) mx = fmaxf(mx, p[1][i]);
+#pragma unroll
+                    for (int off = QN == 8 ? 4 : 2; off < 32; off <<= 1)
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                    const float mn = fmaxf(m[i], mx);
+                    f[i] = m[i] == -INFINITY ? 0.f : ex2(m[i] - mn);
+                    m[i] = mn;
+                    l[i] *= f[i];
+                }
+                // factors of this lane's columns 2c, 2c + 1 and of column r
+                float f0, f1, fr;
+                if constexpr (QN == 2) {
+                    f0 = __shfl_sync(0xffffffffu, f[0], lane & ~1);
+                    f1 = __shfl_sync(0xffffffffu, f[0], lane | 1);
+                    fr = my_q ? f1 : f0;
+                } else {
+                    f0 = f[0];
+                    f1 = f[1];
+                    const float x0 = __shfl_sync(0xffffffffu, f[0], (lane & ~3) | (my_q >> 1));
+                    const float x1 = __shfl_sync(0xffffffffu, f[1], (lane & ~3) | (my_q >> 1));
+                    fr = (my_q & 1) ? x1 : x0;
+                }
+#pragma unroll
+                for (int j = 0; j < NT; ++j) zacc[j] *= fr;
+#pragma unroll
+                for (int i = 0; i < MT; ++i) {
+                    o[i][0] *= f0;
+                    o[i][1] *= f1;
+                    o[i][2] *= f0;
+                    o[i][3] *= f1;
+                }
+            }
+#pragma unroll
+            for (int h = 0; h < NV; ++h)
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    p[h][i] = ex2(p[h][i] - (m[i] == -INFINITY ? 0.f : m[i]));
+                    l[i] += p[h][i];
+                }
+            // ---- output: the weights of this lane's 4 keys and query
+            float w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (QN == 2) {
+                    w[i] = __shfl_sync(0xffffffffu, p[0][0], src_lane[i]);
+                } else if constexpr (QN == 4) {
+                    const float x0 = __shfl_sync(0xffffffffu, p[0][0], src_lane[i]);
+                    const float x1 = __shfl_sync(0xffffffffu, p[0][1], src_lane[i]);
+                    w[i] = (my_q & 1) ? x1 : x0;
+                } else {
+                    // key i's row half is the same for the whole warp (d = 128:
+                    // i >> 1) or i's (d = 64: (i >> 1) & 1): pick it before
+                    constexpr int kNone = 0;
+                    const int h = (i >> 1) & 1;
+                    const float x0 = __shfl_sync(0xffffffffu, h ? p[NV - 1][0] : p[0][0], src_lane[i] & 31);
+                    const float x1 = __shfl_sync(0xffffffffu, h ? p[NV - 1][NP - 1] : p[0][NP - 1],
+                                                 src_lane[i] & 31);
+                    w[i] = (my_q & 1) ? x1 : x0;
+                    (void)kNone;
+                }
+            }
+            const unsigned char* vr[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) vr[i] = vs + (base + output_key<NG>(c, i)) * R;
+            uint32_t pf[PARTS][NT][2];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int g = j * CPT + r / QN;
+                float ws[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    uint32_t sz = g < NG ? *reinterpret_cast<const uint32_t*>(vr[i] + D / 2 + 4 * g) : 0u;
+                    if (!whole && !valid(output_key<NG>(c, i))) sz = 0u;
+                    ws[i] = w[i] * bf16lo(sz);
+                    zacc[j] = fmaf(w[i], bf16hi(sz), zacc[j]);
+                }
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part) {
+                    pf[part][j][0] = split_pair(ws[0], ws[1]);
+                    pf[part][j][1] = split_pair(ws[2], ws[3]);
+                }
+            }
+            uint32_t vw[4][NG / 2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (NG == 4) {
+                    const uint2 x = *reinterpret_cast<const uint2*>(vr[i] + 8 * r);
+                    vw[i][0] = x.x;
+                    vw[i][NG / 2 - 1] = x.y;
+                } else {
+                    vw[i][0] = *reinterpret_cast<const uint32_t*>(vr[i] + 4 * r);
+                }
+            }
+            const uint32_t off[4] = {0xC308C308u, 0xC308C308u, 0xC308C308u, 0xC308C308u};  // -136
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+                const uint32_t xa = __byte_perm(vw[0][g >> 1], vw[1][g >> 1], (g & 1) ? 0x7632 : 0x5410);
+                const uint32_t xb = __byte_perm(vw[2][g >> 1], vw[3][g >> 1], (g & 1) ? 0x7632 : 0x5410);
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const uint32_t af[4] = {codes<F32>(xa, 2 * h), codes<F32>(xa, 2 * h + 1),
+                                            codes<F32>(xb, 2 * h), codes<F32>(xb, 2 * h + 1)};
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part)
+                        mma(o[2 * g + h], af, pf[part][g / CPT][0], pf[part][g / CPT][1]);
+                    if constexpr (!F32)
+                        mma(o[2 * g + h], off, pf[0][g / CPT][0], pf[0][g / CPT][1]);
+                }
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&empty[s]);
+        if (!tag.last) continue;
+
+        // ---- end of the piece: this warp's state, in output layout: dims 32 g +
+        // 4 r .. + 3 of queries 2c, 2c + 1 (mod QN) for g = j CPT + 2c / QN
+        fresh = false;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+#pragma unroll
+            for (int off = QN == 8 ? 4 : 2; off < 32; off <<= 1)
+                l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
+            if (l[i] != l[i] && m[i] == -INFINITY) m[i] = 0.f;  // every score a NaN
+        }
+        float m2[2], l2[2], val[NT][2][4];
+        if constexpr (QN == 2) {
+            m2[0] = __shfl_sync(0xffffffffu, m[0], lane & ~1);
+            m2[1] = __shfl_sync(0xffffffffu, m[0], lane | 1);
+            l2[0] = __shfl_sync(0xffffffffu, l[0], lane & ~1);
+            l2[1] = __shfl_sync(0xffffffffu, l[0], lane | 1);
+        } else {
+            m2[0] = m[0];
+            m2[1] = m[NP - 1];
+            l2[0] = l[0];
+            l2[1] = l[NP - 1];
+        }
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            float z = zacc[j];
+            z += __shfl_xor_sync(0xffffffffu, z, 1);
+            z += __shfl_xor_sync(0xffffffffu, z, 2);
+            const float z0 = __shfl_sync(0xffffffffu, z, 8 * c);
+            const float z1 = __shfl_sync(0xffffffffu, z, 8 * c + 4);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) val[j][0][e] = val[j][1][e] = 0.f;
+#pragma unroll
+            for (int gi = 0; gi < CPT; ++gi) {
+                const int g = j * CPT + gi;
+                if (g >= NG || gi != 2 * c / QN) continue;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    val[j][0][e] = o[2 * g + (e >> 1)][2 * (e & 1)] + z0;
+                    val[j][1][e] = o[2 * g + (e >> 1)][2 * (e & 1) + 1] + z1;
+                }
+            }
+        }
+        if (a.wh > 1) {  // the warps of this head and queries: rank 0 merges
+            if (rank > 0) {
+                if (merges > 0 &&
+                    !__all_sync(0xffffffffu, mbar_wait(&merge_bar[1], (merges - 1) & 1, a.err)))
+                    break;
+                float* x = reinterpret_cast<float*>(
+                    scratch + (size_t)((rank - 1) * units + unit) * state_bytes(NT));
+                float4* y = reinterpret_cast<float4*>(x);
+                y[lane] = make_float4(m2[0], m2[1], l2[0], l2[1]);
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        y[(1 + 2 * j + i) * 32 + lane] = make_float4(val[j][i][0], val[j][i][1],
+                                                                     val[j][i][2], val[j][i][3]);
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&merge_bar[0]);
+            } else {
+                if (unit == 0 && lane == 0) mbar_arrive(&merge_bar[0]);
+                if (!__all_sync(0xffffffffu, mbar_wait(&merge_bar[0], merges & 1, a.err))) break;
+                for (int wv = 1; wv < a.wh; ++wv) {
+                    const float4* y = reinterpret_cast<const float4*>(
+                        scratch + (size_t)((wv - 1) * units + unit) * state_bytes(NT));
+                    const float4 st = y[lane];
+                    const float mo[2] = {st.x, st.y}, lo[2] = {st.z, st.w};
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float M = fmaxf(m2[i], mo[i]);
+                        const float ca = m2[i] == -INFINITY ? 0.f : ex2(m2[i] - M);
+                        const float cb = mo[i] == -INFINITY ? 0.f : ex2(mo[i] - M);
+                        l2[i] = l2[i] * ca + lo[i] * cb;
+                        m2[i] = M;
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) {
+                            const float4 x = y[(1 + 2 * j + i) * 32 + lane];
+                            val[j][i][0] = val[j][i][0] * ca + x.x * cb;
+                            val[j][i][1] = val[j][i][1] * ca + x.y * cb;
+                            val[j][i][2] = val[j][i][2] * ca + x.z * cb;
+                            val[j][i][3] = val[j][i][3] * ca + x.w * cb;
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&merge_bar[1]);
+            }
+            ++merges;
+        }
+        if (rank != 0) continue;
+        const int64_t slot = (int64_t)blockIdx.x + tag.seq;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int qi = (2 * c + i) % QN;
+            if (qi >= nq) continue;
+            const int64_t at = slot * a.hq + qh0 + qi;
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int g = j * CPT + 2 * c / QN;
+                if (g < NG)
+                    *reinterpret_cast<float4*>(a.part_o + at * D + 32 * g + 4 * r) =
+                        make_float4(val[j][i][0], val[j][i][1], val[j][i][2], val[j][i][3]);
+            }
+            if (r == 0 && 2 * c / QN == 0)
+                *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(m2[i], l2[i]);
+        }
     }
+}
+
+// ---- combine: one warp per (sequence, query head) -------------------------------
+struct Q4CombineArgs {
+    const float* part_o;
+    const float* part_ml;
+    const int32_t* tstart;
+    void* out;
+    int32_t batch, hq, ctas;
+};
+constexpr int kCombineWarps = 4;
+constexpr int kCombineLoads = 8;  // partial states in flight
+
+template <int D, bool F32>
+__global__ void __launch_bounds__(kCombineWarps * 32) q4_combine_kernel(const Q4CombineArgs a) {
+    PKV_DEPENDENT_PROLOGUE();
+    constexpr int E = D / 32;
+    const int lane = threadIdx.x & 31;
+    const int64_t w = (int64_t)blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
+    if (w >= (int64_t)a.batch * a.hq) return;
+    const int b = (int)(w / a.hq), h = (int)(w % a.hq);
+    const int32_t ta = a.tstart[b], tb = a.tstart[b + 1];
+    const int32_t len = share_len(a.tstart[a.batch], a.batch, a.ctas);
+    const int c0 = (ta + b + 1) / len, c1 = tb > ta ? (tb + b) / len : c0 - 1;
+    float M = -INFINITY, L = 0.f, acc[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    for (int base = c0; base <= c1; base += kCombineLoads) {
+        float2 ml[kCombineLoads];
+        float x[kCombineLoads][E];
+#pragma unroll
+        for (int i = 0; i < kCombineLoads; ++i) {
+            ml[i] = make_float2(-INFINITY, 0.f);
+            if (base + i <= c1) {
+                const int64_t at = ((int64_t)(base + i) + b) * a.hq + h;
+                ml[i] = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
+                const float* p = a.part_o + at * D + lane * E;
+                if constexpr (E == 4) {
+                    const float4 y = *reinterpret_cast<const float4*>(p);
+                    x[i][0] = y.x; x[i][1] = y.y; x[i][E - 2] = y.z; x[i][E - 1] = y.w;
+                } else {
+                    const float2 y = *reinterpret_cast<const float2*>(p);
+                    x[i][0] = y.x; x[i][1] = y.y;
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < kCombineLoads; ++i) {
+            if (ml[i].x == -INFINITY) continue;  // holds nothing
+            const float mn = fmaxf(M, ml[i].x);
+            const float ca = M == -INFINITY ? 0.f : ex2(M - mn), cb = ex2(ml[i].x - mn);
+            L = L * ca + ml[i].y * cb;
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] = acc[e] * ca + x[i][e] * cb;
+            M = mn;
+        }
+    }
+    const float inv = L == 0.f ? 0.f : 1.f / L;
+    const int64_t at = w * D + lane * E;
+    if constexpr (F32) {
+        float* o = static_cast<float*>(a.out) + at;
+#pragma unroll
+        for (int e = 0; e < E; ++e) o[e] = acc[e] * inv;
+    } else {
+        uint32_t* o = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + at);
+#pragma unroll
+        for (int e = 0; e < E; e += 2) o[e / 2] = pack_bf16x2(acc[e] * inv, acc[e + 1] * inv);
+    }
+}
+
+template <int NG, int QN, bool F32>
+cudaError_t launch_split(const Q4DecodePlan& p, const Q4DecodeArgs& a, cudaStream_t stream) {
+    auto kern = q4_split_kernel<NG, QN, F32>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                               (int)p.smem_bytes);
+    if (e != cudaSuccess) return e;
+    return launch_dependent(kern, dim3(p.ctas, p.head_groups),
+                            dim3((consumer_warps<F32>() + 1) * 32), p.smem_bytes, stream, a);
 }
 
 }  // namespace
 
-bool plan_q4_decode(const DeviceInfo& dev, int32_t batch, int hq, int hkv, int d, int block_size,
-                    int q_dtype, Q4DecodePlan* plan) {
-    plan->ws_bytes = 0;
-    return (d == 64 || d == 128) && batch <= kDecodeMaxBatch && hq <= 65535;
+bool plan_q4_decode(const DeviceInfo& dev, int32_t batch, int32_t max_blocks, int hq, int hkv,
+                    int d, int block_size, int q_dtype, Q4DecodePlan* p) {
+    if ((d != 64 && d != 128) || batch > kDecodeMaxBatch) return false;
+    // rows of 40 bytes: copies of a page piece start on 16 bytes when pages
+    // hold an even number of rows
+    if (d == 64 && block_size % 2) return false;
+    const bool f32 = q_dtype == PKV_F32;
+    const int wc = f32 ? consumer_warps<true>() : consumer_warps<false>();
+    const int G = hq / hkv;
+    p->qn = G <= 2 ? 2 : (G <= 4 ? 4 : 8);
+    p->no = (G + p->qn - 1) / p->qn;
+    if (p->no > wc) return false;
+    p->hc = 1;  // the most KV heads whose queries the consumer warps hold
+    for (int h = 1; h * p->no <= wc && h <= hkv; ++h)
+        if (hkv % h == 0) p->hc = h;
+    p->head_groups = hkv / p->hc;
+    if (p->head_groups > 65535) return false;
+    const int units = p->hc * p->no;
+    p->wh = wc / units;
+    p->tile = 16 * p->wh;
+    const int R = q4_row_bytes(d);
+    const int nt = std::max(1, d / kQ4Group * p->qn / 8);
+    const size_t stage = (size_t)2 * p->hc * p->tile * R;
+    const size_t fixed = kHeader + up((size_t)(batch + 1) * 4, 128) +
+                         (size_t)units * (p->wh - 1) * state_bytes(nt);
+    const size_t room = dev.max_smem_optin - 1024;  // static shared memory, alignment
+    if (room < fixed + 2 * stage) return false;
+    p->stages = (int)std::min<size_t>(kMaxStages, (room - fixed) / stage);
+    p->smem_bytes = fixed + p->stages * stage;
+    // one CTA per SM, no more than there can be tiles
+    const int64_t tiles = ((int64_t)max_blocks * block_size + p->tile - 1) / p->tile * batch;
+    const int64_t most = std::max(1, dev.num_sms / p->head_groups);
+    p->ctas = (int)std::max<int64_t>(1, std::min(most, tiles));
+    const size_t slots = (size_t)most + batch;  // whatever the table's width is
+    p->ws_bytes = up((size_t)(batch + 1) * 4, 256) + up(slots * hq * 2 * 4, 256) +
+                  up(slots * hq * d * 4, 256);
+    return true;
 }
 
-cudaError_t launch_q4_decode(const Q4DecodePlan& plan, const void* q, const void* k_cache,
+cudaError_t launch_q4_decode(const Q4DecodePlan& p, const void* q, const void* k_cache,
                              const void* v_cache, const int32_t* table, int32_t max_blocks,
                              const int32_t* seqlens, int32_t batch, float scale, void* out,
                              void* workspace, int hq, int hkv, int d, int block_size,
                              int64_t num_blocks, int q_dtype, unsigned int* err,
                              cudaStream_t stream) {
     if (batch == 0) return cudaSuccess;
-    const Q4DecodeArgs a{q, static_cast<const unsigned char*>(k_cache),
-                         static_cast<const unsigned char*>(v_cache), table, seqlens, out, err,
-                         num_blocks, scale * 1.4426950408889634f, max_blocks, hq, hkv, block_size};
+    Q4DecodeArgs a{};
+    a.q = q;
+    a.kc = static_cast<const unsigned char*>(k_cache);
+    a.vc = static_cast<const unsigned char*>(v_cache);
+    a.table = table;
+    a.seqlens = seqlens;
+    const size_t slots = (size_t)p.ctas + batch;
+    unsigned char* ws = static_cast<unsigned char*>(workspace);
+    a.tstart = reinterpret_cast<int32_t*>(ws);
+    ws += up((size_t)(batch + 1) * 4, 256);
+    a.part_ml = reinterpret_cast<float*>(ws);
+    ws += up(slots * hq * 2 * 4, 256);
+    a.part_o = reinterpret_cast<float*>(ws);
+    a.err = err;
+    a.num_blocks = num_blocks;
+    a.qscale = scale * kLog2e;
+    a.max_blocks = max_blocks;
+    a.batch = batch;
+    a.hq = hq;
+    a.hkv = hkv;
+    a.block_size = block_size;
+    a.hc = p.hc;
+    a.no = p.no;
+    a.wh = p.wh;
+    a.tile = p.tile;
+    a.stages = p.stages;
     const bool f32 = q_dtype == PKV_F32;
-    auto kern = d == 128 ? (f32 ? q4_decode_kernel<4, true> : q4_decode_kernel<4, false>)
-                         : (f32 ? q4_decode_kernel<2, true> : q4_decode_kernel<2, false>);
-    return launch_dependent(kern, dim3((unsigned)batch, (unsigned)hq), dim3(kWarps * 32), 0, stream,
-                            a);
+    cudaError_t e = cudaErrorInvalidValue;
+#define PKV_Q4_CASE(NN, QQ, FF) \
+    if (d == NN * kQ4Group && p.qn == QQ && f32 == FF) e = launch_split<NN, QQ, FF>(p, a, stream);
+    PKV_Q4_CASE(4, 2, false) PKV_Q4_CASE(4, 4, false) PKV_Q4_CASE(4, 8, false)
+    PKV_Q4_CASE(4, 2, true) PKV_Q4_CASE(4, 4, true) PKV_Q4_CASE(4, 8, true)
+    PKV_Q4_CASE(2, 2, false) PKV_Q4_CASE(2, 4, false) PKV_Q4_CASE(2, 8, false)
+    PKV_Q4_CASE(2, 2, true) PKV_Q4_CASE(2, 4, true) PKV_Q4_CASE(2, 8, true)
+#undef PKV_Q4_CASE
+    if (e != cudaSuccess) return e;
+    const Q4CombineArgs c{a.part_o, a.part_ml, a.tstart, out, batch, hq, p.ctas};
+    auto kern = d == 128 ? (f32 ? q4_combine_kernel<128, true> : q4_combine_kernel<128, false>)
+                         : (f32 ? q4_combine_kernel<64, true> : q4_combine_kernel<64, false>);
+    const int64_t warps = (int64_t)batch * hq;
+    return launch_dependent(kern, dim3((unsigned)((warps + kCombineWarps - 1) / kCombineWarps)),
+                            dim3(kCombineWarps * 32), 0, stream, c);
 }
 
 }  // namespace pkv
