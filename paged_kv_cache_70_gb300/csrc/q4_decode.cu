@@ -46,6 +46,8 @@
 //  * Keys of a page outside the pool are skipped and flagged; rows past the length
 //    never enter: their scales count as 0 and their scores as -inf, whatever the
 //    page holds there.  Every wait is time-limited.
+#include <cuda_fp16.h>
+
 #include <algorithm>
 
 #include "common.cuh"
@@ -57,14 +59,24 @@ namespace pkv {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kGrow = 8.f;  // rescale when a score passes the reference by 2^8
+constexpr int kHold = 8;          // steps between additions of the offsets' sums
+constexpr float kGrow = 8.f;       // rescale when a score passes the reference by 2^8
+constexpr float kScaleGrow = 4.f;  // or a V scale its bound by 2^4: weights stay below 2^12
 constexpr int kMaxStages = 8;
 constexpr int kHeader = 512;  // barriers and stage tags
 
-// consumer warps: 16 leave 120 registers a thread; fp32 queries keep 3 parts
-// of every operand and run 8
-template <bool F32>
-__host__ __device__ constexpr int consumer_warps() { return F32 ? 8 : 16; }
+constexpr int kConsumers = 8;  // consumer warps
+constexpr int kProducers = 4;  // producer warps, each with every 4th tile
+constexpr int kThreads = (kConsumers + kProducers) * 32;  // 168 registers a thread
+
+// 16-key products a warp runs side by side
+template <int QN, bool F32>
+__host__ __device__ constexpr int key_steps() { return F32 || QN == 8 ? 1 : 2; }
+inline int key_steps_of(int qn, bool f32) {
+    return qn == 2 ? (f32 ? key_steps<2, true>() : key_steps<2, false>())
+                   : (qn == 4 ? (f32 ? key_steps<4, true>() : key_steps<4, false>())
+                              : (f32 ? key_steps<8, true>() : key_steps<8, false>()));
+}
 
 struct Q4DecodeArgs {
     const void* q;
@@ -89,7 +101,7 @@ struct Q4DecodeArgs {
 // one stage's description, written by the producer
 struct Tag {
     int32_t seq;   // sequence
-    int32_t rows;  // keys, -1: no more stages
+    int32_t rows;  // keys
     int32_t last;  // the piece of the sequence ends here
     int32_t bad;   // first key's position if a page was out of range, else -1
 };
@@ -116,31 +128,43 @@ __host__ __device__ constexpr size_t up(size_t x, size_t a) { return (x + a - 1)
 __host__ __device__ constexpr size_t state_bytes(int nt) { return (size_t)(8 * nt + 4) * 128; }
 
 __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, "
+    asm(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
         "{%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
-// codes i of both halves of x as two bf16: 128 + u, or (EXACT) u - 8
-template <bool EXACT>
+// Codes i of both halves of x as two fp16.  A code in the low bits of the
+// mantissa is a subnormal, u 2^-24, and one four bits up is 16 u 2^-24: no
+// conversion, one logic operation per pair of codes and a shift for every other
+// pair.  The factor 16 is taken out of the other operand (scores) or of the
+// result (output), 2^24 at the end.
+// With CENTRED 8 is subtracted (exactly; subnormals again).
+template <bool CENTRED>
 __device__ __forceinline__ uint32_t codes(uint32_t x, int i) {
-    uint32_t y = ((x >> (4 * i)) & 0x000F000Fu) | 0x43004300u;
-    if constexpr (EXACT) {
-        const uint32_t c = 0xC308C308u;  // -136
-        const uint32_t one = 0x3F803F80u;
-        asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(y) : "r"(y), "r"(one), "r"(c));
-    }
+    uint32_t y = (i & 2 ? x >> 8 : x) & (i & 1 ? 0x00F000F0u : 0x000F000Fu);
+    if constexpr (CENTRED)
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(y) : "r"(i & 1 ? 0x00800080u : 0x00080008u));
     return y;
 }
+constexpr float kUnit = 1.f / 16777216.f;  // 2^-24
 
-// the k-th bf16 part of x, removed from it
-__device__ __forceinline__ uint32_t split_pair(float& a, float& b) {
-    const uint32_t p = pack_bf16x2(a, b);
-    a -= bf16lo(p);
-    b -= bf16hi(p);
-    return p;
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t y;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(y) : "f"(hi), "f"(lo));
+    return y;
+}
+// a and b rounded to fp16; what was rounded off stays in them (REST)
+template <bool REST>
+__device__ __forceinline__ uint32_t take_f16x2(float& a, float& b) {
+    const uint32_t y = pack_f16x2(a, b);
+    if constexpr (REST) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&y));
+        a -= f.x;
+        b -= f.y;
+    }
+    return y;
 }
 
 // where the 16 keys of a step sit: MMA row r + 8 half of the score product, and
@@ -168,16 +192,18 @@ __device__ __forceinline__ void score_row(int key, int* r, int* half) {
 }
 
 template <int NG, int QN, bool F32>
-__global__ void __launch_bounds__((consumer_warps<F32>() + 1) * 32, 1)
+__global__ void __launch_bounds__(kThreads, 1)
 q4_split_kernel(const Q4DecodeArgs a) {
-    constexpr int WC = consumer_warps<F32>();
+    constexpr int WC = kConsumers;
     constexpr int D = NG * kQ4Group, R = q4_row_bytes(D);
     constexpr int CPT = 8 / QN;                    // groups per column tile
     constexpr int NT = NG > CPT ? NG / CPT : 1;    // column tiles
     constexpr int MT = 2 * NG;                     // 16-dim tiles of the output
-    constexpr int PARTS = F32 ? 3 : 1;
+    constexpr int PARTS = F32 ? 2 : 1;
     constexpr int NP = QN == 2 ? 1 : 2;            // queries a lane takes exponentials for
     constexpr int NV = QN == 8 ? 2 : 1;            // score rows a lane takes them for
+    constexpr int KS = key_steps<QN, F32>();       // 16-key products side by side
+    constexpr int KEYS = 16 * KS;
     extern __shared__ __align__(128) unsigned char smem[];
     uint64_t* full = reinterpret_cast<uint64_t*>(smem);
     uint64_t* empty = full + kMaxStages;
@@ -187,7 +213,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
     unsigned char* scratch = smem + kHeader + up((size_t)(a.batch + 1) * 4, 128);
     const int units = a.hc * a.no;  // (head, queries) of the CTA
     unsigned char* ring = scratch + (size_t)units * (a.wh - 1) * state_bytes(NT);
-    __shared__ int32_t warp_sum[WC + 1];
+    __shared__ int32_t warp_sum[kThreads / 32];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int S = a.stages, T = a.tile;
@@ -208,7 +234,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
     const int64_t cap = (int64_t)a.max_blocks * a.block_size;
     const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0;
     {
-        constexpr int N = (WC + 1) * 32;
+        constexpr int N = kThreads;
         const int per = (a.batch + N - 1) / N;
         const int lo = tid * per, hi = min(lo + per, a.batch);
         int32_t sum = 0;
@@ -247,81 +273,85 @@ q4_split_kernel(const Q4DecodeArgs a) {
     if (t0 >= t1) return;
     const int head0 = blockIdx.y * a.hc;
 
-    if (warp == WC) {
-        // ------------------------------ producer ------------------------------
+    if (warp >= WC) {
+        // ------------------------------ producers -----------------------------
+        // Warp w prepares tiles t0 + w, t0 + w + 4, ..: one tile costs a chain of
+        // ~2000 cycles (slot, table entry, address, barrier) whatever its size.
+        // No more warps than stages: a warp then has seen its stage's last but one
+        // contents consumed (with its own previous tile) before it waits for the
+        // last, which a wait on the phase's parity alone could not tell apart.
+        const int prods = min(kProducers, S);
+        if (warp - WC >= prods) return;
         const uint64_t pol = l2_evict_first_policy();
-        int b = 0;  // the sequence of tile t0
+        const uint32_t inv_hc = 65536u / a.hc + 1;  // i / hc for i < 512, hc <= 16
+        const int64_t head_bytes = (int64_t)a.block_size * R;
+        const int32_t tf = t0 + warp - WC;
+        if (tf >= t1) return;
+        int b = 0;  // the sequence of tile t
         {
             int lo = 0, hi = a.batch;
             while (lo < hi) {
                 const int mid = (lo + hi) >> 1;
-                if (tstart[mid + 1] <= t0) lo = mid + 1; else hi = mid;
+                if (tstart[mid + 1] <= tf) lo = mid + 1; else hi = mid;
             }
             b = lo;
         }
         int32_t L = (int32_t)min((int64_t)max(__ldg(a.seqlens + b), 0), cap);
-        const uint32_t inv_hc = 65536u / a.hc + 1;  // i / hc for i < 512, hc <= 16
-        const int64_t head_bytes = (int64_t)a.block_size * R;
-        int32_t k = 0;
-        bool stop = false;
-        // page ids of a tile's first 32 pages, one tile ahead
-        int32_t next_page = -1;
+        // ids of a tile's first 32 pages, one tile ahead
         auto fetch = [&](int bb, int32_t p0, int32_t p1) {
             const int32_t pg = p0 / a.block_size + lane;
             return (int64_t)pg * a.block_size < p1
                        ? __ldg(a.table + (int64_t)bb * a.max_blocks + pg) : -1;
         };
-        {
-            const int32_t p0 = (t0 - tstart[b]) * T;
-            next_page = fetch(b, p0, min(L, p0 + T));
-        }
-        for (int32_t t = t0; t < t1 && !stop; ++t) {
-            const int32_t p0 = (t - tstart[b]) * T, p1 = min(L, p0 + T);
+        int32_t p0 = (tf - tstart[b]) * T, p1 = min(L, p0 + T);
+        int32_t next_page = fetch(b, p0, p1);
+        int32_t last_k = -1;
+        for (int32_t t = tf; t < t1; t += prods) {
             const int seq = b;
+            const int32_t q0 = p0, q1 = p1;  // this tile's keys
             int32_t page = next_page;
-            const bool seq_end = t + 1 == tstart[b + 1];
-            if (t + 1 < t1) {  // the next tile's sequence and pages
-                if (seq_end) {
-                    do ++b; while (tstart[b + 1] <= t + 1);
+            const bool last = t + 1 == tstart[b + 1] || t + 1 == t1;
+            if (t + prods < t1) {  // the next tile's sequence and pages
+                if (t + prods >= tstart[b + 1]) {
+                    do ++b; while (tstart[b + 1] <= t + prods);
                     L = (int32_t)min((int64_t)max(__ldg(a.seqlens + b), 0), cap);
                 }
-                const int32_t q0 = (t + 1 - tstart[b]) * T;
-                next_page = fetch(b, q0, min(L, q0 + T));
+                p0 = (t + prods - tstart[b]) * T;
+                p1 = min(L, p0 + T);
+                next_page = fetch(b, p0, p1);
             }
+            const int32_t k = t - t0;
             const int s = k % S;
-            bool ok = true;
-            if (lane == 0) ok = mbar_wait(&empty[s], ((k / S) & 1) ^ 1, a.err);
-            if (!__all_sync(0xffffffffu, ok)) {
-                stop = true;
-                break;
-            }
-            ++k;
-            unsigned char* kd = ring + (size_t)s * 2 * half_bytes;
-            const int32_t pg0 = p0 / a.block_size;
-            const int np = (p1 - 1) / a.block_size - pg0 + 1;
-            // the bytes that will arrive: a first pass over the pages when they
-            // are more than the prefetched 32
+            const int32_t pg0 = q0 / a.block_size;
+            const int np = (q1 - 1) / a.block_size - pg0 + 1;
+            // the bytes that will arrive
             uint32_t bytes = 0;
             bool bad = false;
             for (int c0 = 0; c0 < np; c0 += 32) {
                 const int32_t pg = pg0 + c0 + lane;
-                const int32_t id = c0 == 0 ? page
-                                   : (c0 + lane < np ? __ldg(a.table + (int64_t)seq * a.max_blocks + pg) : -1);
                 if (c0 + lane < np) {
-                    const int32_t lo = max(p0, pg * a.block_size);
-                    const int32_t hi = min((int64_t)p1, (int64_t)(pg + 1) * a.block_size);
+                    const int32_t id =
+                        c0 == 0 ? page : __ldg(a.table + (int64_t)seq * a.max_blocks + pg);
+                    const int32_t lo = max(q0, pg * a.block_size);
+                    const int32_t hi = (int32_t)min((int64_t)q1, (int64_t)(pg + 1) * a.block_size);
                     if (id < 0 || id >= a.num_blocks) bad = true;
                     else bytes += (uint32_t)up((size_t)(hi - lo) * R, 16);
                 }
             }
             bad = __any_sync(0xffffffffu, bad);
             bytes = __reduce_add_sync(0xffffffffu, bytes) * 2 * a.hc;
+            bool ok = true;
             if (lane == 0) {
-                if (bad) flag_error(a.err, PKV_FLAG_BAD_BLOCK);
-                tags[s] = Tag{seq, p1 - p0, (seq_end || t + 1 == t1) ? 1 : 0, bad ? p0 : -1};
-                mbar_arrive_expect_tx(&full[s], bytes);
+                ok = mbar_wait(&empty[s], ((k / S) & 1) ^ 1, a.err);
+                if (ok) {
+                    if (bad) flag_error(a.err, PKV_FLAG_BAD_BLOCK);
+                    tags[s] = Tag{seq, q1 - q0, last ? 1 : 0, bad ? q0 : -1};
+                    mbar_arrive_expect_tx(&full[s], bytes);
+                }
             }
-            __syncwarp();
+            if (!__all_sync(0xffffffffu, ok)) break;
+            last_k = k;
+            unsigned char* kd = ring + (size_t)s * 2 * half_bytes;
             for (int c0 = 0; c0 < np; c0 += 32) {
                 if (c0 > 0) {
                     const int32_t pg = pg0 + c0 + lane;
@@ -334,30 +364,24 @@ q4_split_kernel(const Q4DecodeArgs a) {
                     const int32_t id = __shfl_sync(0xffffffffu, page, p);
                     if (i0 + lane >= n || id < 0 || id >= a.num_blocks) continue;
                     const int32_t pg = pg0 + c0 + p;
-                    const int32_t lo = max(p0, pg * a.block_size);
-                    const int32_t hi = min((int64_t)p1, (int64_t)(pg + 1) * a.block_size);
+                    const int32_t lo = max(q0, pg * a.block_size);
+                    const int32_t hi = (int32_t)min((int64_t)q1, (int64_t)(pg + 1) * a.block_size);
                     const int64_t src = ((int64_t)id * a.hkv + head0 + h) * head_bytes +
                                         (int64_t)(lo - pg * a.block_size) * R;
-                    unsigned char* dst = kd + ((size_t)h * T + (lo - p0)) * R;
+                    unsigned char* dst = kd + ((size_t)h * T + (lo - q0)) * R;
                     const uint32_t n16 = (uint32_t)up((size_t)(hi - lo) * R, 16);
                     bulk_g2s(dst, a.kc + src, n16, &full[s], pol);
                     bulk_g2s(dst + half_bytes, a.vc + src, n16, &full[s], pol);
                 }
             }
+            __syncwarp();
         }
-        __syncwarp();
-        if (lane != 0) return;
-        if (!stop) {  // the closing stage
-            const int s = k % S;
-            if (mbar_wait(&empty[s], ((k / S) & 1) ^ 1, a.err)) {
-                tags[s].rows = -1;
-                mbar_arrive(&full[s]);
-                ++k;
-            }
-        }
-        // no copy may be in flight when the CTA exits (see decode.cu)
-        for (int32_t j = k > S ? k - S : 0; j < k; ++j)
-            if (!mbar_wait(&full[j % S], (j / S) & 1, a.err)) break;
+        // no copy may be in flight when the CTA exits (after a timeout the
+        // consumers may have stopped waiting): wait for the fills that no later
+        // one follows
+        if (lane == 0)
+            for (int32_t k = last_k; k >= 0 && k >= t1 - t0 - S; k -= prods)
+                if (!mbar_wait(&full[k % S], (k / S) & 1, a.err)) break;
         return;
     }
     if (warp >= active) return;
@@ -380,23 +404,39 @@ q4_split_kernel(const Q4DecodeArgs a) {
         score_row<NG>(output_key<NG>(c, i), &sr, &half);
         if (QN == 2) src_lane[i] = sr * 4 + half * 2 + my_q;
         else if (QN == 4) src_lane[i] = sr * 4 + half * 2 + (my_q >> 1);
-        else src_lane[i] = (sr * 4 + (my_q >> 1)) | (half << 8);
+        else src_lane[i] = sr * 4 + (my_q >> 1);
     }
 
     uint32_t qf[PARTS][NG][4];  // score product's columns: 2 k-steps of 2 words per group
-    float qs[NT][2];            // sum of q over the group of columns 2c, 2c + 1
-    float o[MT][4], zacc[NT], m[NP], l[NP];
+    float qs[NT][2];            // 2^-24 sum of q over the group of columns 2c, 2c + 1
+    float cq[NP];               // from a product to log2 units, for this lane's queries
+    float start[NT][2];         // -8 times those: where a score product starts
+    float o[MT][4], ct[NT][4], zacc[NT], l[NP];
+    // reference of the queries' weights, the same with -inf as 0, and the score
+    // that makes it move; log2 of the V scale it counts with, and their limit
+    float m[NP], mr[NP], lim[NP], sref = 0.f, slim = 0.f;
+    int held = 0;               // steps since the offsets' sums were last added
+    auto settle = [&]() {
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) o[i][e] += ct[i / 2 / CPT][e];
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ct[j][e] = 0.f;
+    };
     int loaded = -1;
     bool fresh = false;
     int merges = 0;
 
-    for (int32_t k = 0;; ++k) {
+    for (int32_t k = 0; k < t1 - t0; ++k) {
         const int s = k % S;
         if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (k / S) & 1, a.err))) break;
         const Tag tag = tags[s];
-        if (tag.rows < 0) break;
         if (tag.seq != loaded) {  // the sequence's queries
             loaded = tag.seq;
+            float xs[NT][8];
 #pragma unroll
             for (int j = 0; j < NT; ++j) {
                 const int g_col = j * CPT + r / QN;  // the group of this lane's column
@@ -419,16 +459,53 @@ q4_split_kernel(const Q4DecodeArgs a) {
                         x[6] = bf16lo(w.w); x[7] = bf16hi(w.w);
                     }
                 }
+#pragma unroll
+                for (int e = 0; e < 8; ++e) xs[j][e] = x[e];
+            }
+            // the query scaled by a power of two to below 2^12: fp16 then holds
+            // bf16 queries exactly down to 2^-25 of the largest, and two parts
+            // hold 23 bits of fp32 ones
+            float mx = 0.f;
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(xs[j][e]));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+#pragma unroll
+            for (int off = 4 * QN; off < 32; off <<= 1)
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+            const int ex = (int)(__float_as_uint(mx) >> 23);
+            const float up_q = __uint_as_float((uint32_t)min(max(265 - ex, 1), 252) << 23);
+            const float down = a.qscale / kUnit / up_q;
+            if constexpr (QN == 2) {
+                cq[0] = __shfl_sync(0xffffffffu, down, 4 * (c & 1));
+            } else {
+                const int n = QN == 4 ? 2 * (c & 1) : 2 * c;
+                cq[0] = __shfl_sync(0xffffffffu, down, 4 * n);
+                cq[NP - 1] = __shfl_sync(0xffffffffu, down, 4 * n + 4);
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                const int g_col = j * CPT + r / QN;
+                float* x = xs[j];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) x[e] *= up_q;
                 float sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+                sum *= kUnit;
                 sum += __shfl_xor_sync(0xffffffffu, sum, 1);
                 sum += __shfl_xor_sync(0xffffffffu, sum, 2);
                 qs[j][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
                 qs[j][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+                start[j][0] = F32 ? 0.f : -8.f * qs[j][0];
+                start[j][1] = F32 ? 0.f : -8.f * qs[j][1];
+#pragma unroll
+                for (int e = 1; e < 8; e += 2) x[e] *= 0.0625f;  // its codes count 16 times
 #pragma unroll
                 for (int part = 0; part < PARTS; ++part) {
                     uint32_t w[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = split_pair(x[e], x[e + 4]);
+                    for (int e = 0; e < 4; ++e) w[e] = take_f16x2<F32>(x[e], x[e + 4]);
 #pragma unroll
                     for (int gi = 0; gi < CPT; ++gi) {
                         const int g = j * CPT + gi;
@@ -448,128 +525,193 @@ q4_split_kernel(const Q4DecodeArgs a) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) zacc[j] = 0.f;
+            for (int j = 0; j < NT; ++j) {
+                zacc[j] = 0.f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) ct[j][e] = 0.f;
+            }
+            held = 0;
+            sref = -60.f;
+            slim = 0.f;
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
-                m[i] = -INFINITY;
+                m[i] = lim[i] = -INFINITY;
+                mr[i] = 0.f;
                 l[i] = 0.f;
             }
         }
         const unsigned char* ks = ring + (size_t)s * 2 * half_bytes + (size_t)hc * T * R;
         const unsigned char* vs = ks + half_bytes;
-        for (int base = rank * 16; base < tag.rows; base += a.wh * 16) {
-            const bool whole = base + 16 <= tag.rows && tag.bad < 0;
-            auto valid = [&](int key) {  // (only asked when not whole)
-                if (base + key >= tag.rows) return false;
-                if (tag.bad < 0) return true;
-                const int32_t id = __ldg(a.table + (int64_t)tag.seq * a.max_blocks +
-                                         (tag.bad + base + key) / a.block_size);
-                return id >= 0 && id < a.num_blocks;
-            };
-            // ---- scores: 16 keys x 8 columns
-            const unsigned char* kr[2] = {ks + (base + score_key<NG>(r, 0)) * R,
-                                          ks + (base + score_key<NG>(r, 1)) * R};
-            float sc[NT][4];
+        for (int base = rank * KEYS; base < tag.rows; base += a.wh * KEYS) {
+            // ---- scores: KS times 16 keys x 8 columns
+            float sc[KS][NT][4], alt[KS][4];
+            uint32_t ksz[KS][NT][2];
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                sc[j][0] = sc[j][2] = F32 ? 0.f : -136.f * qs[j][0];
-                sc[j][1] = sc[j][3] = F32 ? 0.f : -136.f * qs[j][1];
-            }
-            uint32_t kw[2][NG];
+            for (int y = 0; y < KS; ++y) {
+                const unsigned char* kr[2] = {ks + (base + 16 * y + score_key<NG>(r, 0)) * R,
+                                              ks + (base + 16 * y + score_key<NG>(r, 1)) * R};
+                uint32_t kw[2][NG];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if constexpr (NG == 4) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(kr[h] + 16 * c);
-                    kw[h][0] = w.x; kw[h][1] = w.y; kw[h][2] = w.z; kw[h][3] = w.w;
-                } else {
-                    const uint2 w = *reinterpret_cast<const uint2*>(kr[h] + 8 * c);
-                    kw[h][0] = w.x; kw[h][1] = w.y;
+                for (int h = 0; h < 2; ++h) {
+                    if constexpr (NG == 4) {
+                        const uint4 w = *reinterpret_cast<const uint4*>(kr[h] + 16 * c);
+                        kw[h][0] = w.x; kw[h][1] = w.y; kw[h][NG - 2] = w.z; kw[h][NG - 1] = w.w;
+                    } else {
+                        const uint2 w = *reinterpret_cast<const uint2*>(kr[h] + 8 * c);
+                        kw[h][0] = w.x; kw[h][1] = w.y;
+                    }
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const int g = j * CPT + 2 * c / QN;
+                        ksz[y][j][h] =
+                            g < NG ? *reinterpret_cast<const uint32_t*>(kr[h] + D / 2 + 4 * g) : 0u;
+                    }
                 }
-            }
-            uint32_t ksz[NT][2];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int g = j * CPT + 2 * c / QN;
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    ksz[j][h] = g < NG ? *reinterpret_cast<const uint32_t*>(kr[h] + D / 2 + 4 * g) : 0u;
-            }
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                uint32_t x[2];
-#pragma unroll
-                for (int h = 0; h < 2; ++h)
-                    x[h] = __byte_perm(kw[h][NG == 4 ? g >> 1 : 0], kw[h][NG == 4 ? 2 + (g >> 1) : 1],
-                                       (g & 1) ? 0x7632 : 0x5410);
-#pragma unroll
-                for (int st = 0; st < 2; ++st) {
-                    const uint32_t af[4] = {codes<F32>(x[0], 2 * st), codes<F32>(x[1], 2 * st),
-                                            codes<F32>(x[0], 2 * st + 1), codes<F32>(x[1], 2 * st + 1)};
-#pragma unroll
-                    for (int part = 0; part < PARTS; ++part)
-                        mma(sc[g / CPT], af, qf[part][g][2 * st], qf[part][g][2 * st + 1]);
-                }
-            }
-            // scale per group, sum over the groups: v[row half][query 2c, 2c+1]
-            float v[2][2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                float2 acc = make_float2(0.f, 0.f);
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    const float ss = bf16lo(ksz[j][h]), zz = bf16hi(ksz[j][h]);
-                    acc = ffma2(make_float2(ss, ss), make_float2(sc[j][2 * h], sc[j][2 * h + 1]), acc);
-                    acc = ffma2(make_float2(zz, zz), make_float2(qs[j][0], qs[j][1]), acc);
+                    sc[y][j][0] = sc[y][j][2] = start[j][0];
+                    sc[y][j][1] = sc[y][j][3] = start[j][1];
                 }
-                v[h][0] = acc.x;
-                v[h][1] = acc.y;
+                if constexpr (NT == 1) alt[y][0] = alt[y][1] = alt[y][2] = alt[y][3] = 0.f;
+#pragma unroll
+                for (int g = 0; g < NG; ++g) {
+                    uint32_t x[2];
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        x[h] = __byte_perm(kw[h][NG == 4 ? g >> 1 : 0],
+                                           kw[h][NG == 4 ? 2 + (g >> 1) : 1],
+                                           (g & 1) ? 0x7632 : 0x5410);
+#pragma unroll
+                    for (int st = 0; st < 2; ++st) {
+                        const uint32_t af[4] = {codes<F32>(x[0], 2 * st), codes<F32>(x[1], 2 * st),
+                                                codes<F32>(x[0], 2 * st + 1), codes<F32>(x[1], 2 * st + 1)};
+                        // one column tile: two chains of products
+                        float* to = NT == 1 && st ? alt[y] : sc[y][g / CPT];
+#pragma unroll
+                        for (int part = 0; part < PARTS; ++part)
+                            mma(to, af, qf[part][g][2 * st], qf[part][g][2 * st + 1]);
+                    }
+                }
             }
-            float p[NV][NP];  // this lane's scores, then weights
-            if constexpr (QN == 8) {
+            // the V scales of this lane's keys and column groups
+            uint32_t vsz[KS][NT][4];
+#pragma unroll
+            for (int y = 0; y < KS; ++y)
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    const int g = j * CPT + r / QN;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        vsz[y][j][i] = g < NG ? *reinterpret_cast<const uint32_t*>(
+                                                    vs + (base + 16 * y + output_key<NG>(c, i)) * R +
+                                                    D / 2 + 4 * g)
+                                              : 0u;
+                }
+            // scale per group, sum over the groups
+            float p[KS][NV][NP];  // this lane's scores, then weights
+#pragma unroll
+            for (int y = 0; y < KS; ++y) {
+                float v[2][2];  // [row half][query 2c, 2c + 1]
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) p[h][i] = v[h][i];
-            } else {
-                // lanes c and c ^ 2 hold other groups of the same queries: each
-                // keeps one row half
-                const bool up_half = c & 2;
-                float w[2];
+                    for (int i = 0; i < 2; ++i) {
+                        v[h][i] = 0.f;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const float got = __shfl_xor_sync(0xffffffffu, up_half ? v[0][i] : v[1][i], 2);
-                    w[i] = (up_half ? v[1][i] : v[0][i]) + got;
-                }
-                if constexpr (QN == 4) {
-                    p[0][0] = w[0];
-                    p[0][1] = w[1];
-                } else {  // lanes c and c ^ 1: each keeps one query
-                    const float got = __shfl_xor_sync(0xffffffffu, (c & 1) ? w[0] : w[1], 1);
-                    p[0][0] = ((c & 1) ? w[1] : w[0]) + got;
+                        for (int j = 0; j < NT; ++j) {
+                            const float x = NT == 1 ? sc[y][j][2 * h + i] + alt[y][2 * h + i]
+                                                    : sc[y][j][2 * h + i];
+                            v[h][i] = fmaf(bf16lo(ksz[y][j][h]), x, v[h][i]);
+                            v[h][i] = fmaf(bf16hi(ksz[y][j][h]), qs[j][i], v[h][i]);
+                        }
+                    }
+                if constexpr (QN == 8) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) p[y][NV == 2 ? h : 0][NP == 2 ? i : 0] = v[h][i] * cq[NP == 2 ? i : 0];
+                } else {
+                    // lanes c and c ^ 2 hold other groups of the same queries: each
+                    // keeps one row half
+                    const bool up_half = c & 2;
+                    float w[2];
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) {
+                        const float got = __shfl_xor_sync(0xffffffffu, up_half ? v[0][i] : v[1][i], 2);
+                        w[i] = (up_half ? v[1][i] : v[0][i]) + got;
+                    }
+                    if constexpr (QN == 4) {
+                        p[y][0][0] = w[0] * cq[0];
+                        p[y][0][NP - 1] = w[1] * cq[NP - 1];
+                    } else {  // lanes c and c ^ 1: each keeps one query
+                        const float got = __shfl_xor_sync(0xffffffffu, (c & 1) ? w[0] : w[1], 1);
+                        p[y][0][0] = (((c & 1) ? w[1] : w[0]) + got) * cq[0];
+                    }
                 }
             }
+            if (base + KEYS > tag.rows || tag.bad >= 0) {  // keys that do not count
+                auto valid = [&](int key) {
+                    if (base + key >= tag.rows) return false;
+                    if (tag.bad < 0) return true;
+                    const int32_t id = __ldg(a.table + (int64_t)tag.seq * a.max_blocks +
+                                             (tag.bad + base + key) / a.block_size);
+                    return id >= 0 && id < a.num_blocks;
+                };
+#pragma unroll
+                for (int y = 0; y < KS; ++y) {
+#pragma unroll
+                    for (int h = 0; h < NV; ++h) {
+                        const bool ok = valid(16 * y + score_key<NG>(r, QN == 8 ? h : c >> 1));
+#pragma unroll
+                        for (int i = 0; i < NP; ++i) p[y][h][i] = ok ? p[y][h][i] : -INFINITY;
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const bool ok = valid(16 * y + output_key<NG>(c, i));
+#pragma unroll
+                        for (int j = 0; j < NT; ++j) vsz[y][j][i] = ok ? vsz[y][j][i] : 0u;
+                    }
+                }
+            }
+            float smax = 0.f;
             bool grow = false;
 #pragma unroll
-            for (int h = 0; h < NV; ++h) {
-                const bool ok = whole || valid(score_key<NG>(r, QN == 8 ? h : c >> 1));
+            for (int y = 0; y < KS; ++y) {
 #pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    p[h][i] = ok ? p[h][i] * a.qscale : -INFINITY;
-                    grow |= p[h][i] > m[i] + kGrow;
-                }
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) smax = fmaxf(smax, bf16lo(vsz[y][j][i]));
+#pragma unroll
+                for (int h = 0; h < NV; ++h)
+#pragma unroll
+                    for (int i = 0; i < NP; ++i) grow |= p[y][h][i] > lim[i];
             }
+            grow |= smax > slim;
             if (__any_sync(0xffffffffu, grow)) {  // move the reference to the running maximum
+#pragma unroll
+                for (int off = 1; off < 32; off <<= 1)
+                    smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, off));
+                // the least power of two above the scales so far, 2^-60 .. 2^100
+                const int se = min(max((int)(__float_as_uint(smax) >> 23) - 126, -60), 100);
+                const float sold = sref;
+                sref = fmaxf(sref, (float)se);
+                slim = exp2f(sref + kScaleGrow);
                 float f[NP];
 #pragma unroll
                 for (int i = 0; i < NP; ++i) {
-                    float mx = p[0][i];
-                    if constexpr (NV == 2) mx = fmaxf(mx, p[1][i]);
+                    float mx = -INFINITY;
+#pragma unroll
+                    for (int y = 0; y < KS; ++y)
+#pragma unroll
+                        for (int h = 0; h < NV; ++h) mx = fmaxf(mx, p[y][h][i]);
 #pragma unroll
                     for (int off = QN == 8 ? 4 : 2; off < 32; off <<= 1)
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                    const float mn = fmaxf(m[i], mx);
+                    const float mn = fmaxf(m[i] - sold, mx) + sref;
                     f[i] = m[i] == -INFINITY ? 0.f : ex2(m[i] - mn);
                     m[i] = mn;
+                    mr[i] = mn == -INFINITY ? 0.f : mn;
+                    lim[i] = mn - sref + kGrow;
                     l[i] *= f[i];
                 }
                 // factors of this lane's columns 2c, 2c + 1 and of column r
@@ -580,13 +722,19 @@ q4_split_kernel(const Q4DecodeArgs a) {
                     fr = my_q ? f1 : f0;
                 } else {
                     f0 = f[0];
-                    f1 = f[1];
-                    const float x0 = __shfl_sync(0xffffffffu, f[0], (lane & ~3) | (my_q >> 1));
-                    const float x1 = __shfl_sync(0xffffffffu, f[1], (lane & ~3) | (my_q >> 1));
+                    f1 = f[NP - 1];
+                    const float x0 = __shfl_sync(0xffffffffu, f0, (lane & ~3) | (my_q >> 1));
+                    const float x1 = __shfl_sync(0xffffffffu, f1, (lane & ~3) | (my_q >> 1));
                     fr = (my_q & 1) ? x1 : x0;
                 }
 #pragma unroll
-                for (int j = 0; j < NT; ++j) zacc[j] *= fr;
+                for (int j = 0; j < NT; ++j) {
+                    zacc[j] *= fr;
+                    ct[j][0] *= f0;
+                    ct[j][1] *= f1;
+                    ct[j][2] *= f0;
+                    ct[j][3] *= f1;
+                }
 #pragma unroll
                 for (int i = 0; i < MT; ++i) {
                     o[i][0] *= f0;
@@ -596,81 +744,79 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 }
             }
 #pragma unroll
-            for (int h = 0; h < NV; ++h)
+            for (int y = 0; y < KS; ++y) {
 #pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    p[h][i] = ex2(p[h][i] - (m[i] == -INFINITY ? 0.f : m[i]));
-                    l[i] += p[h][i];
-                }
-            // ---- output: the weights of this lane's 4 keys and query
-            float w[4];
+                for (int h = 0; h < NV; ++h)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (QN == 2) {
-                    w[i] = __shfl_sync(0xffffffffu, p[0][0], src_lane[i]);
-                } else if constexpr (QN == 4) {
-                    const float x0 = __shfl_sync(0xffffffffu, p[0][0], src_lane[i]);
-                    const float x1 = __shfl_sync(0xffffffffu, p[0][1], src_lane[i]);
-                    w[i] = (my_q & 1) ? x1 : x0;
-                } else {
-                    // key i's row half is the same for the whole warp (d = 128:
-                    // i >> 1) or i's (d = 64: (i >> 1) & 1): pick it before
-                    constexpr int kNone = 0;
-                    const int h = (i >> 1) & 1;
-                    const float x0 = __shfl_sync(0xffffffffu, h ? p[NV - 1][0] : p[0][0], src_lane[i] & 31);
-                    const float x1 = __shfl_sync(0xffffffffu, h ? p[NV - 1][NP - 1] : p[0][NP - 1],
-                                                 src_lane[i] & 31);
-                    w[i] = (my_q & 1) ? x1 : x0;
-                    (void)kNone;
-                }
-            }
-            const unsigned char* vr[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) vr[i] = vs + (base + output_key<NG>(c, i)) * R;
-            uint32_t pf[PARTS][NT][2];
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int g = j * CPT + r / QN;
-                float ws[4];
+                    for (int i = 0; i < NP; ++i) {
+                        p[y][h][i] = ex2(p[y][h][i] - mr[i]);
+                        l[i] += p[y][h][i];
+                    }
+                // ---- output: the weights of this lane's 4 keys and query
+                float w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    uint32_t sz = g < NG ? *reinterpret_cast<const uint32_t*>(vr[i] + D / 2 + 4 * g) : 0u;
-                    if (!whole && !valid(output_key<NG>(c, i))) sz = 0u;
-                    ws[i] = w[i] * bf16lo(sz);
-                    zacc[j] = fmaf(w[i], bf16hi(sz), zacc[j]);
+                    if constexpr (QN == 2) {
+                        w[i] = __shfl_sync(0xffffffffu, p[y][0][0], src_lane[i]);
+                    } else {
+                        // (8 queries: key i's row half is i >> 1 in every lane)
+                        const int h = QN == 8 && i >= 2 ? NV - 1 : 0;
+                        const float x0 = __shfl_sync(0xffffffffu, p[y][h][0], src_lane[i]);
+                        const float x1 = __shfl_sync(0xffffffffu, p[y][h][NP - 1], src_lane[i]);
+                        w[i] = (my_q & 1) ? x1 : x0;
+                    }
+                }
+                uint32_t pf[PARTS][NT][2];
+#pragma unroll
+                for (int j = 0; j < NT; ++j) {
+                    float ws[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        ws[i] = w[i] * bf16lo(vsz[y][j][i]);
+                        zacc[j] = fmaf(w[i], bf16hi(vsz[y][j][i]), zacc[j]);
+                    }
+#pragma unroll
+                    for (int part = 0; part < PARTS; ++part) {
+                        pf[part][j][0] = take_f16x2<F32>(ws[0], ws[1]);
+                        pf[part][j][1] = take_f16x2<F32>(ws[2], ws[3]);
+                        if constexpr (!F32) {
+                            // -8 in the units of rows r (codes 0, 2) and r + 8 (codes 1, 3)
+                            const uint32_t off[4] = {0x80088008u, 0x80808080u, 0x80088008u,
+                                                     0x80808080u};
+                            mma(ct[j], off, pf[part][j][0], pf[part][j][1]);
+                        }
+                    }
+                }
+                uint32_t vw[4][2];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const unsigned char* vr = vs + (base + 16 * y + output_key<NG>(c, i)) * R;
+                    if constexpr (NG == 4) {
+                        const uint2 x = *reinterpret_cast<const uint2*>(vr + 8 * r);
+                        vw[i][0] = x.x;
+                        vw[i][1] = x.y;
+                    } else {
+                        vw[i][0] = *reinterpret_cast<const uint32_t*>(vr + 4 * r);
+                    }
                 }
 #pragma unroll
-                for (int part = 0; part < PARTS; ++part) {
-                    pf[part][j][0] = split_pair(ws[0], ws[1]);
-                    pf[part][j][1] = split_pair(ws[2], ws[3]);
+                for (int g = 0; g < NG; ++g) {
+                    const uint32_t sel = (g & 1) ? 0x7632 : 0x5410;
+                    const uint32_t xa = __byte_perm(vw[0][g >> 1], vw[1][g >> 1], sel);
+                    const uint32_t xb = __byte_perm(vw[2][g >> 1], vw[3][g >> 1], sel);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t af[4] = {codes<F32>(xa, 2 * h), codes<F32>(xa, 2 * h + 1),
+                                                codes<F32>(xb, 2 * h), codes<F32>(xb, 2 * h + 1)};
+#pragma unroll
+                        for (int part = 0; part < PARTS; ++part)
+                            mma(o[2 * g + h], af, pf[part][g / CPT][0], pf[part][g / CPT][1]);
+                    }
                 }
             }
-            uint32_t vw[4][NG / 2];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if constexpr (NG == 4) {
-                    const uint2 x = *reinterpret_cast<const uint2*>(vr[i] + 8 * r);
-                    vw[i][0] = x.x;
-                    vw[i][NG / 2 - 1] = x.y;
-                } else {
-                    vw[i][0] = *reinterpret_cast<const uint32_t*>(vr[i] + 4 * r);
-                }
-            }
-            const uint32_t off[4] = {0xC308C308u, 0xC308C308u, 0xC308C308u, 0xC308C308u};  // -136
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                const uint32_t xa = __byte_perm(vw[0][g >> 1], vw[1][g >> 1], (g & 1) ? 0x7632 : 0x5410);
-                const uint32_t xb = __byte_perm(vw[2][g >> 1], vw[3][g >> 1], (g & 1) ? 0x7632 : 0x5410);
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    const uint32_t af[4] = {codes<F32>(xa, 2 * h), codes<F32>(xa, 2 * h + 1),
-                                            codes<F32>(xb, 2 * h), codes<F32>(xb, 2 * h + 1)};
-#pragma unroll
-                    for (int part = 0; part < PARTS; ++part)
-                        mma(o[2 * g + h], af, pf[part][g / CPT][0], pf[part][g / CPT][1]);
-                    if constexpr (!F32)
-                        mma(o[2 * g + h], off, pf[0][g / CPT][0], pf[0][g / CPT][1]);
-                }
+            if (!F32 && ++held == kHold) {
+                held = 0;
+                settle();
             }
         }
         __syncwarp();
@@ -680,6 +826,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
         // ---- end of the piece: this warp's state, in output layout: dims 32 g +
         // 4 r .. + 3 of queries 2c, 2c + 1 (mod QN) for g = j CPT + 2c / QN
         fresh = false;
+        if constexpr (!F32) settle();
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
 #pragma unroll
@@ -714,8 +861,9 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 if (g >= NG || gi != 2 * c / QN) continue;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    val[j][0][e] = o[2 * g + (e >> 1)][2 * (e & 1)] + z0;
-                    val[j][1][e] = o[2 * g + (e >> 1)][2 * (e & 1) + 1] + z1;
+                    const float u = e & 1 ? 1.f / (16.f * kUnit) : 1.f / kUnit;
+                    val[j][0][e] = fmaf(o[2 * g + (e >> 1)][2 * (e & 1)], u, z0);
+                    val[j][1][e] = fmaf(o[2 * g + (e >> 1)][2 * (e & 1) + 1], u, z1);
                 }
             }
         }
@@ -861,7 +1009,7 @@ cudaError_t launch_split(const Q4DecodePlan& p, const Q4DecodeArgs& a, cudaStrea
                                                (int)p.smem_bytes);
     if (e != cudaSuccess) return e;
     return launch_dependent(kern, dim3(p.ctas, p.head_groups),
-                            dim3((consumer_warps<F32>() + 1) * 32), p.smem_bytes, stream, a);
+                            dim3(kThreads), p.smem_bytes, stream, a);
 }
 
 }  // namespace
@@ -873,7 +1021,7 @@ bool plan_q4_decode(const DeviceInfo& dev, int32_t batch, int32_t max_blocks, in
     // hold an even number of rows
     if (d == 64 && block_size % 2) return false;
     const bool f32 = q_dtype == PKV_F32;
-    const int wc = f32 ? consumer_warps<true>() : consumer_warps<false>();
+    const int wc = kConsumers;
     const int G = hq / hkv;
     p->qn = G <= 2 ? 2 : (G <= 4 ? 4 : 8);
     p->no = (G + p->qn - 1) / p->qn;
@@ -885,7 +1033,7 @@ bool plan_q4_decode(const DeviceInfo& dev, int32_t batch, int32_t max_blocks, in
     if (p->head_groups > 65535) return false;
     const int units = p->hc * p->no;
     p->wh = wc / units;
-    p->tile = 16 * p->wh;
+    p->tile = 16 * key_steps_of(p->qn, f32) * p->wh;
     const int R = q4_row_bytes(d);
     const int nt = std::max(1, d / kQ4Group * p->qn / 8);
     const size_t stage = (size_t)2 * p->hc * p->tile * R;
