@@ -65,18 +65,21 @@ constexpr float kScaleGrow = 4.f;  // or a V scale its bound by 2^4: weights sta
 constexpr int kMaxStages = 8;
 constexpr int kHeader = 512;  // barriers and stage tags
 
-constexpr int kConsumers = 8;  // consumer warps
 constexpr int kProducers = 4;  // producer warps, each with every 4th tile
-constexpr int kThreads = (kConsumers + kProducers) * 32;  // 168 registers a thread
 
-// 16-key products a warp runs side by side
+// Consumer warps and the 16-key products one runs side by side.  With 2 or 4
+// queries 16 warps fit (20 warps are launched with 96 registers; setmaxnreg
+// moves some from the producers' warpgroup to the consumers'); 8 queries and
+// fp32 ones keep more in registers and run 8 (12 warps with 168).
+template <int QN, bool F32>
+__host__ __device__ constexpr int consumers() { return 8; }
 template <int QN, bool F32>
 __host__ __device__ constexpr int key_steps() { return F32 || QN == 8 ? 1 : 2; }
-inline int key_steps_of(int qn, bool f32) {
-    return qn == 2 ? (f32 ? key_steps<2, true>() : key_steps<2, false>())
-                   : (qn == 4 ? (f32 ? key_steps<4, true>() : key_steps<4, false>())
-                              : (f32 ? key_steps<8, true>() : key_steps<8, false>()));
-}
+template <int QN, bool F32>
+__host__ __device__ constexpr int threads() { return (consumers<QN, F32>() + kProducers) * 32; }
+constexpr int kConsumerRegs = 104, kProducerRegs = 64;
+static_assert(16 * kConsumerRegs + kProducers * kProducerRegs <= 20 * 96,
+              "register split exceeds the launch");
 
 struct Q4DecodeArgs {
     const void* q;
@@ -135,6 +138,15 @@ __device__ __forceinline__ void mma(float* c, const uint32_t* a, uint32_t b0, ui
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
 
+// d = a b + (c0, c1, c0, c1)
+__device__ __forceinline__ void mma_from(float* d, const uint32_t* a, uint32_t b0, uint32_t b1,
+                                         float c0, float c1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, "
+        "{%4, %5, %6, %7}, {%8, %9}, {%10, %11, %10, %11};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
+}
+
 // Codes i of both halves of x as two fp16.  A code in the low bits of the
 // mantissa is a subnormal, u 2^-24, and one four bits up is 16 u 2^-24: no
 // conversion, one logic operation per pair of codes and a shift for every other
@@ -167,6 +179,35 @@ __device__ __forceinline__ uint32_t take_f16x2(float& a, float& b) {
     return y;
 }
 
+// ---- barriers by 32-bit shared address (computed once per warp)
+__device__ __forceinline__ bool try_phase(uint32_t bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
+    return ok != 0;
+}
+__device__ __noinline__ bool wait_phase_slow(uint32_t bar, uint32_t parity, unsigned int* err) {
+    const uint64_t t0 = global_ns();
+    while (!__all_sync(0xffffffffu, try_phase(bar, parity))) {
+        if (global_ns() - t0 > kWaitLimitNs) {
+            flag_error(err, PKV_FLAG_TIMEOUT);
+            return false;
+        }
+    }
+    return true;
+}
+// the whole warp waits for a phase; false (flagged) if it does not end in time
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, unsigned int* err) {
+    if (__all_sync(0xffffffffu, try_phase(bar, parity))) return true;
+    return __all_sync(0xffffffffu, wait_phase_slow(bar, parity, err));
+}
+__device__ __forceinline__ void arrive(uint32_t bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
 // where the 16 keys of a step sit: MMA row r + 8 half of the score product, and
 // k index (2c, 2c+1, 2c+8, 2c+9 for i = 0..3) of the output product.  Chosen so
 // that the lanes of one shared-memory access touch all banks once at row
@@ -192,13 +233,12 @@ __device__ __forceinline__ void score_row(int key, int* r, int* half) {
 }
 
 template <int NG, int QN, bool F32>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads<QN, F32>(), 1)
 q4_split_kernel(const Q4DecodeArgs a) {
-    constexpr int WC = kConsumers;
+    constexpr int WC = consumers<QN, F32>();
     constexpr int D = NG * kQ4Group, R = q4_row_bytes(D);
     constexpr int CPT = 8 / QN;                    // groups per column tile
     constexpr int NT = NG > CPT ? NG / CPT : 1;    // column tiles
-    constexpr int MT = 2 * NG;                     // 16-dim tiles of the output
     constexpr int PARTS = F32 ? 2 : 1;
     constexpr int NP = QN == 2 ? 1 : 2;            // queries a lane takes exponentials for
     constexpr int NV = QN == 8 ? 2 : 1;            // score rows a lane takes them for
@@ -213,7 +253,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
     unsigned char* scratch = smem + kHeader + up((size_t)(a.batch + 1) * 4, 128);
     const int units = a.hc * a.no;  // (head, queries) of the CTA
     unsigned char* ring = scratch + (size_t)units * (a.wh - 1) * state_bytes(NT);
-    __shared__ int32_t warp_sum[kThreads / 32];
+    __shared__ int32_t warp_sum[threads<QN, F32>() / 32];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const int S = a.stages, T = a.tile;
@@ -234,7 +274,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
     const int64_t cap = (int64_t)a.max_blocks * a.block_size;
     const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0;
     {
-        constexpr int N = kThreads;
+        constexpr int N = threads<QN, F32>();
         const int per = (a.batch + N - 1) / N;
         const int lo = tid * per, hi = min(lo + per, a.batch);
         int32_t sum = 0;
@@ -275,6 +315,8 @@ q4_split_kernel(const Q4DecodeArgs a) {
 
     if (warp >= WC) {
         // ------------------------------ producers -----------------------------
+        if constexpr (WC == 16)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
         // Warp w prepares tiles t0 + w, t0 + w + 4, ..: one tile costs a chain of
         // ~2000 cycles (slot, table entry, address, barrier) whatever its size.
         // No more warps than stages: a warp then has seen its stage's last but one
@@ -306,6 +348,8 @@ q4_split_kernel(const Q4DecodeArgs a) {
         int32_t p0 = (tf - tstart[b]) * T, p1 = min(L, p0 + T);
         int32_t next_page = fetch(b, p0, p1);
         int32_t last_k = -1;
+        int s = tf - t0;      // stage and the times it was filled before
+        uint32_t fills = 0;
         for (int32_t t = tf; t < t1; t += prods) {
             const int seq = b;
             const int32_t q0 = p0, q1 = p1;  // this tile's keys
@@ -321,7 +365,6 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 next_page = fetch(b, p0, p1);
             }
             const int32_t k = t - t0;
-            const int s = k % S;
             const int32_t pg0 = q0 / a.block_size;
             const int np = (q1 - 1) / a.block_size - pg0 + 1;
             // the bytes that will arrive
@@ -342,7 +385,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
             bytes = __reduce_add_sync(0xffffffffu, bytes) * 2 * a.hc;
             bool ok = true;
             if (lane == 0) {
-                ok = mbar_wait(&empty[s], ((k / S) & 1) ^ 1, a.err);
+                ok = mbar_wait(&empty[s], (fills & 1) ^ 1, a.err);
                 if (ok) {
                     if (bad) flag_error(a.err, PKV_FLAG_BAD_BLOCK);
                     tags[s] = Tag{seq, q1 - q0, last ? 1 : 0, bad ? q0 : -1};
@@ -375,6 +418,11 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 }
             }
             __syncwarp();
+            s += prods;
+            if (s >= S) {
+                s -= S;
+                ++fills;
+            }
         }
         // no copy may be in flight when the CTA exits (after a timeout the
         // consumers may have stopped waiting): wait for the fills that no later
@@ -384,6 +432,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 if (!mbar_wait(&full[k % S], (k / S) & 1, a.err)) break;
         return;
     }
+    if constexpr (WC == 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
     if (warp >= active) return;
 
     // ------------------------------- consumers --------------------------------
@@ -407,398 +456,476 @@ q4_split_kernel(const Q4DecodeArgs a) {
         else src_lane[i] = sr * 4 + (my_q >> 1);
     }
 
-    uint32_t qf[PARTS][NG][4];  // score product's columns: 2 k-steps of 2 words per group
+    // One or two groups share a column tile's products (QN <= 4): the two 16-bit
+    // halves of a code word then are two groups' codes, in columns of their own
+    // (zeros meet the other half), and need no rearranging.  With 8 queries a tile
+    // holds one group and a byte permutation brings its codes together.
+    constexpr bool PAIR = QN < 8;
+    const float even = ((r / QN) & 1) ? 0.f : 1.f, odd = 1.f - even;  // this column's half
+    uint32_t qf[PARTS][NG][4];  // score product's columns: 2 k-steps of 2 words per code word
     float qs[NT][2];            // 2^-24 sum of q over the group of columns 2c, 2c + 1
-    float cq[NP];               // from a product to log2 units, for this lane's queries
     float start[NT][2];         // -8 times those: where a score product starts
-    float o[MT][4], ct[NT][4], zacc[NT], l[NP];
+    float cq[NP];               // from a product to log2 units, for this lane's queries
+    constexpr int OT = PAIR ? NG : 2 * NG;  // output tiles of 16 rows
+    float o[OT][4], ct[NT][4], zacc[NT], l[NP];
     // reference of the queries' weights, the same with -inf as 0, and the score
     // that makes it move; log2 of the V scale it counts with, and their limit
     float m[NP], mr[NP], lim[NP], sref = 0.f, slim = 0.f;
     int held = 0;               // steps since the offsets' sums were last added
     auto settle = [&]() {
 #pragma unroll
-        for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < OT; ++i)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) o[i][e] += ct[i / 2 / CPT][e];
+            for (int e = 0; e < 4; ++e) o[i][e] += ct[(PAIR ? i / 2 * 2 : i / 2) / CPT][e];
 #pragma unroll
         for (int j = 0; j < NT; ++j)
 #pragma unroll
             for (int e = 0; e < 4; ++e) ct[j][e] = 0.f;
     };
-    int loaded = -1;
-    bool fresh = false;
-    int merges = 0;
-
-    for (int32_t k = 0; k < t1 - t0; ++k) {
-        const int s = k % S;
-        if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (k / S) & 1, a.err))) break;
-        const Tag tag = tags[s];
-        if (tag.seq != loaded) {  // the sequence's queries
-            loaded = tag.seq;
-            float xs[NT][8];
+    auto clear = [&]() {  // the state of a new piece
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int g_col = j * CPT + r / QN;  // the group of this lane's column
-                float x[8];
+        for (int i = 0; i < OT; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] = 0.f;
-                if (g_col < NG && my_q < nq) {
-                    const int64_t at = ((int64_t)tag.seq * a.hq + qh0 + my_q) * D + g_col * 32 + c * 8;
-                    if constexpr (F32) {
-                        const float4* p = reinterpret_cast<const float4*>(
-                            static_cast<const float*>(a.q) + at);
-                        const float4 u = __ldg(p), v = __ldg(p + 1);
-                        x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
-                        x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
-                    } else {
-                        const uint4 w = __ldg(reinterpret_cast<const uint4*>(
-                            static_cast<const uint16_t*>(a.q) + at));
-                        x[0] = bf16lo(w.x); x[1] = bf16hi(w.x); x[2] = bf16lo(w.y);
-                        x[3] = bf16hi(w.y); x[4] = bf16lo(w.z); x[5] = bf16hi(w.z);
-                        x[6] = bf16lo(w.w); x[7] = bf16hi(w.w);
+            for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            zacc[j] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) ct[j][e] = 0.f;
+        }
+        held = 0;
+        sref = -60.f;
+        slim = 0.f;
+#pragma unroll
+        for (int i = 0; i < NP; ++i) {
+            m[i] = lim[i] = -INFINITY;
+            mr[i] = 0.f;
+            l[i] = 0.f;
+        }
+    };
+    auto load_queries = [&](int32_t seq) {
+        float xs[NT][8];
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const int g_col = j * CPT + r / QN;  // the group of this lane's column
+            float* x = xs[j];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] = 0.f;
+            if (g_col < NG && my_q < nq) {
+                const int64_t at = ((int64_t)seq * a.hq + qh0 + my_q) * D + g_col * 32 + c * 8;
+                if constexpr (F32) {
+                    const float4* p =
+                        reinterpret_cast<const float4*>(static_cast<const float*>(a.q) + at);
+                    const float4 u = __ldg(p), v = __ldg(p + 1);
+                    x[0] = u.x; x[1] = u.y; x[2] = u.z; x[3] = u.w;
+                    x[4] = v.x; x[5] = v.y; x[6] = v.z; x[7] = v.w;
+                } else {
+                    const uint4 w = __ldg(
+                        reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.q) + at));
+                    x[0] = bf16lo(w.x); x[1] = bf16hi(w.x); x[2] = bf16lo(w.y);
+                    x[3] = bf16hi(w.y); x[4] = bf16lo(w.z); x[5] = bf16hi(w.z);
+                    x[6] = bf16lo(w.w); x[7] = bf16hi(w.w);
+                }
+            }
+        }
+        // the query scaled by a power of two to below 2^12: fp16 then holds
+        // bf16 queries exactly down to 2^-25 of the largest, and two parts
+        // hold 23 bits of fp32 ones
+        float mx = 0.f;
+#pragma unroll
+        for (int j = 0; j < NT; ++j)
+#pragma unroll
+            for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(xs[j][e]));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+#pragma unroll
+        for (int off = 4 * QN; off < 32; off <<= 1)
+            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+        const int ex = (int)(__float_as_uint(mx) >> 23);
+        const float up_q = __uint_as_float((uint32_t)min(max(265 - ex, 1), 252) << 23);
+        const float down = a.qscale / kUnit / up_q;
+        if constexpr (QN == 2) {
+            cq[0] = __shfl_sync(0xffffffffu, down, 4 * (c & 1));
+        } else {
+            const int n = QN == 4 ? 2 * (c & 1) : 2 * c;
+            cq[0] = __shfl_sync(0xffffffffu, down, 4 * n);
+            cq[NP - 1] = __shfl_sync(0xffffffffu, down, 4 * n + 4);
+        }
+#pragma unroll
+        for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+            for (int w = 0; w < NG; ++w)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) qf[part][w][e] = 0u;
+#pragma unroll
+        for (int j = 0; j < NT; ++j) {
+            const int g_col = j * CPT + r / QN;
+            float* x = xs[j];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) x[e] *= up_q;
+            float sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
+            sum *= kUnit;
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            qs[j][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
+            qs[j][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
+            start[j][0] = F32 ? 0.f : -8.f * qs[j][0];
+            start[j][1] = F32 ? 0.f : -8.f * qs[j][1];
+#pragma unroll
+            for (int e = 1; e < 8; e += 2) x[e] *= 0.0625f;  // its codes count 16 times
+            if constexpr (PAIR) {
+                // word (unit u of 2, pair of groups gp): dims 4u .. 4u + 3 of the
+                // chunk, k-step e / 2, word e % 2
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float lo = x[4 * u + e] * even, hi = x[4 * u + e] * odd;
+#pragma unroll
+                        for (int part = 0; part < PARTS; ++part) {
+                            const uint32_t w = take_f16x2<F32>(lo, hi);
+#pragma unroll
+                            for (int gp = 0; gp < NG / 2; ++gp)
+                                if (2 * gp / CPT == j && g_col >> 1 == gp)
+                                    qf[part][u * (NG / 2) + gp][e] = w;
+                        }
                     }
+            } else {
+#pragma unroll
+                for (int part = 0; part < PARTS; ++part)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        qf[part][j][e] = take_f16x2<F32>(x[e], x[e + 4]);
+            }
+        }
+    };
+    // Where this lane's chunks sit in a head's rows of a stage (K: row of score
+    // row r, V: row of its first key); other rows are constants away.
+    constexpr int kHalfRow = (NG == 4 ? 8 : 2) * R;  // score row r + 8
+    const int k_codes = score_key<NG>(r, 0) * R + 4 * NG * c;
+    const int k_scale = score_key<NG>(r, 0) * R + D / 2 + 4 * (NT * CPT > NG ? (2 * c / QN) % NG : 2 * c / QN);
+    const int v_codes = output_key<NG>(c, 0) * R + 2 * NG * r;
+    const int v_scale = output_key<NG>(c, 0) * R + D / 2 + 4 * (NT * CPT > NG ? (r / QN) % NG : r / QN);
+    const bool k_live = NT * CPT <= NG || 2 * c / QN < NG, v_live = NT * CPT <= NG || r / QN < NG;
+    // scores of the step's keys in log2 units, for this lane's rows and queries,
+    // and the V scales of its keys and columns
+    auto scores = [&](const unsigned char* ks, const unsigned char* vs,
+                      float (&p)[KS][NV][NP], uint32_t (&vsz)[KS][NT][4]) {
+#pragma unroll
+        for (int y = 0; y < KS; ++y) {
+            uint32_t kw[2][NG], ksz[NT][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const unsigned char* at = ks + k_codes + 16 * y * R + h * kHalfRow;
+                if constexpr (NG == 4) {
+                    const uint4 w = *reinterpret_cast<const uint4*>(at);
+                    kw[h][0] = w.x; kw[h][1] = w.y; kw[h][NG - 2] = w.z; kw[h][NG - 1] = w.w;
+                } else {
+                    const uint2 w = *reinterpret_cast<const uint2*>(at);
+                    kw[h][0] = w.x; kw[h][1] = w.y;
                 }
 #pragma unroll
-                for (int e = 0; e < 8; ++e) xs[j][e] = x[e];
+                for (int j = 0; j < NT; ++j) {
+                    ksz[j][h] = *reinterpret_cast<const uint32_t*>(ks + k_scale + 16 * y * R +
+                                                                   h * kHalfRow + 4 * CPT * j);
+                    if (!k_live) ksz[j][h] = 0u;
+                }
             }
-            // the query scaled by a power of two to below 2^12: fp16 then holds
-            // bf16 queries exactly down to 2^-25 of the largest, and two parts
-            // hold 23 bits of fp32 ones
-            float mx = 0.f;
 #pragma unroll
             for (int j = 0; j < NT; ++j)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(xs[j][e]));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-#pragma unroll
-            for (int off = 4 * QN; off < 32; off <<= 1)
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-            const int ex = (int)(__float_as_uint(mx) >> 23);
-            const float up_q = __uint_as_float((uint32_t)min(max(265 - ex, 1), 252) << 23);
-            const float down = a.qscale / kUnit / up_q;
-            if constexpr (QN == 2) {
-                cq[0] = __shfl_sync(0xffffffffu, down, 4 * (c & 1));
-            } else {
-                const int n = QN == 4 ? 2 * (c & 1) : 2 * c;
-                cq[0] = __shfl_sync(0xffffffffu, down, 4 * n);
-                cq[NP - 1] = __shfl_sync(0xffffffffu, down, 4 * n + 4);
-            }
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int g_col = j * CPT + r / QN;
-                float* x = xs[j];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) x[e] *= up_q;
-                float sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-                sum *= kUnit;
-                sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-                sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-                qs[j][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
-                qs[j][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
-                start[j][0] = F32 ? 0.f : -8.f * qs[j][0];
-                start[j][1] = F32 ? 0.f : -8.f * qs[j][1];
-#pragma unroll
-                for (int e = 1; e < 8; e += 2) x[e] *= 0.0625f;  // its codes count 16 times
-#pragma unroll
-                for (int part = 0; part < PARTS; ++part) {
-                    uint32_t w[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) w[e] = take_f16x2<F32>(x[e], x[e + 4]);
-#pragma unroll
-                    for (int gi = 0; gi < CPT; ++gi) {
-                        const int g = j * CPT + gi;
-                        if (g >= NG) continue;
-                        const bool mine = g_col == g;
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) qf[part][g][e] = mine ? w[e] : 0u;
-                    }
+                for (int i = 0; i < 4; ++i) {
+                    vsz[y][j][i] = *reinterpret_cast<const uint32_t*>(
+                        vs + v_scale + 16 * y * R + output_key<NG>(0, i) * R + 4 * CPT * j);
+                    if (!v_live) vsz[y][j][i] = 0u;
                 }
-            }
-            fresh = false;
-        }
-        if (!fresh) {  // a new piece: empty state
-            fresh = true;
+            float sc[NT][4], alt[4];
 #pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) o[i][e] = 0.f;
-#pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                zacc[j] = 0.f;
-#pragma unroll
-                for (int e = 0; e < 4; ++e) ct[j][e] = 0.f;
-            }
-            held = 0;
-            sref = -60.f;
-            slim = 0.f;
-#pragma unroll
-            for (int i = 0; i < NP; ++i) {
-                m[i] = lim[i] = -INFINITY;
-                mr[i] = 0.f;
-                l[i] = 0.f;
-            }
-        }
-        const unsigned char* ks = ring + (size_t)s * 2 * half_bytes + (size_t)hc * T * R;
-        const unsigned char* vs = ks + half_bytes;
-        for (int base = rank * KEYS; base < tag.rows; base += a.wh * KEYS) {
-            // ---- scores: KS times 16 keys x 8 columns
-            float sc[KS][NT][4], alt[KS][4];
-            uint32_t ksz[KS][NT][2];
-#pragma unroll
-            for (int y = 0; y < KS; ++y) {
-                const unsigned char* kr[2] = {ks + (base + 16 * y + score_key<NG>(r, 0)) * R,
-                                              ks + (base + 16 * y + score_key<NG>(r, 1)) * R};
-                uint32_t kw[2][NG];
+            for (int w = 0; w < NG; ++w) {
+                uint32_t x[2];
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    if constexpr (NG == 4) {
-                        const uint4 w = *reinterpret_cast<const uint4*>(kr[h] + 16 * c);
-                        kw[h][0] = w.x; kw[h][1] = w.y; kw[h][NG - 2] = w.z; kw[h][NG - 1] = w.w;
-                    } else {
-                        const uint2 w = *reinterpret_cast<const uint2*>(kr[h] + 8 * c);
-                        kw[h][0] = w.x; kw[h][1] = w.y;
-                    }
-#pragma unroll
-                    for (int j = 0; j < NT; ++j) {
-                        const int g = j * CPT + 2 * c / QN;
-                        ksz[y][j][h] =
-                            g < NG ? *reinterpret_cast<const uint32_t*>(kr[h] + D / 2 + 4 * g) : 0u;
-                    }
+                    if constexpr (PAIR) x[h] = kw[h][w];
+                    else x[h] = __byte_perm(kw[h][NG == 4 ? w >> 1 : 0], kw[h][NG == 4 ? 2 + (w >> 1) : 1],
+                                            (w & 1) ? 0x7632 : 0x5410);
                 }
+                const int j = PAIR ? 2 * (w % (NG / 2)) / CPT : w;
+                const bool opens = PAIR ? w < NG / 2 && (NT > 1 || w == 0) : true;  // tile j's first
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    sc[y][j][0] = sc[y][j][2] = start[j][0];
-                    sc[y][j][1] = sc[y][j][3] = start[j][1];
-                }
-                if constexpr (NT == 1) alt[y][0] = alt[y][1] = alt[y][2] = alt[y][3] = 0.f;
+                for (int st = 0; st < 2; ++st) {
+                    const uint32_t af[4] = {codes<F32>(x[0], 2 * st), codes<F32>(x[1], 2 * st),
+                                            codes<F32>(x[0], 2 * st + 1), codes<F32>(x[1], 2 * st + 1)};
+                    // one tile: two chains
+                    float* to = NT == 1 && st ? alt : sc[j];
 #pragma unroll
-                for (int g = 0; g < NG; ++g) {
-                    uint32_t x[2];
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        x[h] = __byte_perm(kw[h][NG == 4 ? g >> 1 : 0],
-                                           kw[h][NG == 4 ? 2 + (g >> 1) : 1],
-                                           (g & 1) ? 0x7632 : 0x5410);
-#pragma unroll
-                    for (int st = 0; st < 2; ++st) {
-                        const uint32_t af[4] = {codes<F32>(x[0], 2 * st), codes<F32>(x[1], 2 * st),
-                                                codes<F32>(x[0], 2 * st + 1), codes<F32>(x[1], 2 * st + 1)};
-                        // one column tile: two chains of products
-                        float* to = NT == 1 && st ? alt[y] : sc[y][g / CPT];
-#pragma unroll
-                        for (int part = 0; part < PARTS; ++part)
-                            mma(to, af, qf[part][g][2 * st], qf[part][g][2 * st + 1]);
+                    for (int part = 0; part < PARTS; ++part) {
+                        const uint32_t b0 = qf[part][w][2 * st], b1 = qf[part][w][2 * st + 1];
+                        if (opens && part == 0 && (st == 0 || NT == 1)) {
+                            const bool at = st == 0 && !F32;
+                            mma_from(to, af, b0, b1, at ? start[j][0] : 0.f, at ? start[j][1] : 0.f);
+                        } else {
+                            mma(to, af, b0, b1);
+                        }
                     }
                 }
             }
-            // the V scales of this lane's keys and column groups
-            uint32_t vsz[KS][NT][4];
-#pragma unroll
-            for (int y = 0; y < KS; ++y)
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    const int g = j * CPT + r / QN;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        vsz[y][j][i] = g < NG ? *reinterpret_cast<const uint32_t*>(
-                                                    vs + (base + 16 * y + output_key<NG>(c, i)) * R +
-                                                    D / 2 + 4 * g)
-                                              : 0u;
-                }
             // scale per group, sum over the groups
-            float p[KS][NV][NP];  // this lane's scores, then weights
+            float v[2][2];  // [row half][query 2c, 2c + 1]
 #pragma unroll
-            for (int y = 0; y < KS; ++y) {
-                float v[2][2];  // [row half][query 2c, 2c + 1]
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    v[h][i] = 0.f;
+#pragma unroll
+                    for (int j = 0; j < NT; ++j) {
+                        const float x = NT == 1 ? sc[j][2 * h + i] + alt[2 * h + i] : sc[j][2 * h + i];
+                        v[h][i] = fmaf(bf16lo(ksz[j][h]), x, v[h][i]);
+                        v[h][i] = fmaf(bf16hi(ksz[j][h]), qs[j][i], v[h][i]);
+                    }
+                }
+            if constexpr (QN == 8) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        v[h][i] = 0.f;
+                    for (int i = 0; i < 2; ++i)
+                        p[y][NV == 2 ? h : 0][NP == 2 ? i : 0] = v[h][i] * cq[NP == 2 ? i : 0];
+            } else {
+                // lanes c and c ^ 2 hold other groups of the same queries: each
+                // keeps one row half
+                const bool up_half = c & 2;
+                float w[2];
 #pragma unroll
-                        for (int j = 0; j < NT; ++j) {
-                            const float x = NT == 1 ? sc[y][j][2 * h + i] + alt[y][2 * h + i]
-                                                    : sc[y][j][2 * h + i];
-                            v[h][i] = fmaf(bf16lo(ksz[y][j][h]), x, v[h][i]);
-                            v[h][i] = fmaf(bf16hi(ksz[y][j][h]), qs[j][i], v[h][i]);
-                        }
-                    }
-                if constexpr (QN == 8) {
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) p[y][NV == 2 ? h : 0][NP == 2 ? i : 0] = v[h][i] * cq[NP == 2 ? i : 0];
-                } else {
-                    // lanes c and c ^ 2 hold other groups of the same queries: each
-                    // keeps one row half
-                    const bool up_half = c & 2;
-                    float w[2];
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const float got = __shfl_xor_sync(0xffffffffu, up_half ? v[0][i] : v[1][i], 2);
-                        w[i] = (up_half ? v[1][i] : v[0][i]) + got;
-                    }
-                    if constexpr (QN == 4) {
-                        p[y][0][0] = w[0] * cq[0];
-                        p[y][0][NP - 1] = w[1] * cq[NP - 1];
-                    } else {  // lanes c and c ^ 1: each keeps one query
-                        const float got = __shfl_xor_sync(0xffffffffu, (c & 1) ? w[0] : w[1], 1);
-                        p[y][0][0] = (((c & 1) ? w[1] : w[0]) + got) * cq[0];
-                    }
+                for (int i = 0; i < 2; ++i) {
+                    const float got = __shfl_xor_sync(0xffffffffu, up_half ? v[0][i] : v[1][i], 2);
+                    w[i] = (up_half ? v[1][i] : v[0][i]) + got;
+                }
+                if constexpr (QN == 4) {
+                    p[y][0][0] = w[0] * cq[0];
+                    p[y][0][NP - 1] = w[1] * cq[NP - 1];
+                } else {  // lanes c and c ^ 1: each keeps one query
+                    const float got = __shfl_xor_sync(0xffffffffu, (c & 1) ? w[0] : w[1], 1);
+                    p[y][0][0] = (((c & 1) ? w[1] : w[0]) + got) * cq[0];
                 }
             }
-            if (base + KEYS > tag.rows || tag.bad >= 0) {  // keys that do not count
-                auto valid = [&](int key) {
-                    if (base + key >= tag.rows) return false;
-                    if (tag.bad < 0) return true;
-                    const int32_t id = __ldg(a.table + (int64_t)tag.seq * a.max_blocks +
-                                             (tag.bad + base + key) / a.block_size);
-                    return id >= 0 && id < a.num_blocks;
-                };
-#pragma unroll
-                for (int y = 0; y < KS; ++y) {
-#pragma unroll
-                    for (int h = 0; h < NV; ++h) {
-                        const bool ok = valid(16 * y + score_key<NG>(r, QN == 8 ? h : c >> 1));
-#pragma unroll
-                        for (int i = 0; i < NP; ++i) p[y][h][i] = ok ? p[y][h][i] : -INFINITY;
-                    }
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const bool ok = valid(16 * y + output_key<NG>(c, i));
-#pragma unroll
-                        for (int j = 0; j < NT; ++j) vsz[y][j][i] = ok ? vsz[y][j][i] : 0u;
-                    }
-                }
+        }
+    };
+
+    int merges = 0;
+    const int32_t n_tiles = t1 - t0;
+    uint32_t full_bar = smem_u32(full), empty_bar = smem_u32(empty);
+    asm volatile("" : "+r"(full_bar), "+r"(empty_bar));  // (keep them)
+    // this warp's keys in stage 0 (one step per tile)
+    const unsigned char* keys0 = ring + ((size_t)hc * T + rank * KEYS) * R;
+    const uint32_t stage_bytes = 2 * (uint32_t)half_bytes;
+    float p[KS][NV][NP];
+    uint32_t vsz[KS][NT][4];
+    if (!wait_phase(full_bar, 0, a.err)) return;
+    Tag tag = tags[0];
+    load_queries(tag.seq);
+    clear();
+    scores(keys0, keys0 + half_bytes, p, vsz);
+
+    // Tile k's weights and output products run beside tile k + 1's scores, which
+    // need nothing of them: the two fill each other's latencies.
+    int s = 0, sn = 0;        // stages of tile k and of the next
+    uint32_t phase = 0;       // of stage sn
+    for (int32_t k = 0; k < n_tiles; ++k) {
+        if (k + 1 < n_tiles) {  // (after the last tile: itself again, unused)
+            if (++sn == S) {
+                sn = 0;
+                phase ^= 1;
             }
-            float smax = 0.f;
-            bool grow = false;
+            if (!wait_phase(full_bar + 8 * sn, phase, a.err)) break;
+        }
+        const Tag next = tags[sn];
+        const int base = rank * KEYS;
+        if (base + KEYS > tag.rows || tag.bad >= 0) {  // keys that do not count
+            auto valid = [&](int key) {
+                if (base + key >= tag.rows) return false;
+                if (tag.bad < 0) return true;
+                const int32_t id = __ldg(a.table + (int64_t)tag.seq * a.max_blocks +
+                                         (tag.bad + base + key) / a.block_size);
+                return id >= 0 && id < a.num_blocks;
+            };
 #pragma unroll
             for (int y = 0; y < KS; ++y) {
 #pragma unroll
-                for (int j = 0; j < NT; ++j)
+                for (int h = 0; h < NV; ++h) {
+                    const bool ok = valid(16 * y + score_key<NG>(r, QN == 8 ? h : c >> 1));
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) smax = fmaxf(smax, bf16lo(vsz[y][j][i]));
-#pragma unroll
-                for (int h = 0; h < NV; ++h)
-#pragma unroll
-                    for (int i = 0; i < NP; ++i) grow |= p[y][h][i] > lim[i];
-            }
-            grow |= smax > slim;
-            if (__any_sync(0xffffffffu, grow)) {  // move the reference to the running maximum
-#pragma unroll
-                for (int off = 1; off < 32; off <<= 1)
-                    smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, off));
-                // the least power of two above the scales so far, 2^-60 .. 2^100
-                const int se = min(max((int)(__float_as_uint(smax) >> 23) - 126, -60), 100);
-                const float sold = sref;
-                sref = fmaxf(sref, (float)se);
-                slim = exp2f(sref + kScaleGrow);
-                float f[NP];
-#pragma unroll
-                for (int i = 0; i < NP; ++i) {
-                    float mx = -INFINITY;
-#pragma unroll
-                    for (int y = 0; y < KS; ++y)
-#pragma unroll
-                        for (int h = 0; h < NV; ++h) mx = fmaxf(mx, p[y][h][i]);
-#pragma unroll
-                    for (int off = QN == 8 ? 4 : 2; off < 32; off <<= 1)
-                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                    const float mn = fmaxf(m[i] - sold, mx) + sref;
-                    f[i] = m[i] == -INFINITY ? 0.f : ex2(m[i] - mn);
-                    m[i] = mn;
-                    mr[i] = mn == -INFINITY ? 0.f : mn;
-                    lim[i] = mn - sref + kGrow;
-                    l[i] *= f[i];
+                    for (int i = 0; i < NP; ++i) p[y][h][i] = ok ? p[y][h][i] : -INFINITY;
                 }
-                // factors of this lane's columns 2c, 2c + 1 and of column r
-                float f0, f1, fr;
-                if constexpr (QN == 2) {
-                    f0 = __shfl_sync(0xffffffffu, f[0], lane & ~1);
-                    f1 = __shfl_sync(0xffffffffu, f[0], lane | 1);
-                    fr = my_q ? f1 : f0;
-                } else {
-                    f0 = f[0];
-                    f1 = f[NP - 1];
-                    const float x0 = __shfl_sync(0xffffffffu, f0, (lane & ~3) | (my_q >> 1));
-                    const float x1 = __shfl_sync(0xffffffffu, f1, (lane & ~3) | (my_q >> 1));
-                    fr = (my_q & 1) ? x1 : x0;
-                }
-#pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    zacc[j] *= fr;
-                    ct[j][0] *= f0;
-                    ct[j][1] *= f1;
-                    ct[j][2] *= f0;
-                    ct[j][3] *= f1;
-                }
-#pragma unroll
-                for (int i = 0; i < MT; ++i) {
-                    o[i][0] *= f0;
-                    o[i][1] *= f1;
-                    o[i][2] *= f0;
-                    o[i][3] *= f1;
-                }
-            }
-#pragma unroll
-            for (int y = 0; y < KS; ++y) {
-#pragma unroll
-                for (int h = 0; h < NV; ++h)
-#pragma unroll
-                    for (int i = 0; i < NP; ++i) {
-                        p[y][h][i] = ex2(p[y][h][i] - mr[i]);
-                        l[i] += p[y][h][i];
-                    }
-                // ---- output: the weights of this lane's 4 keys and query
-                float w[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    if constexpr (QN == 2) {
-                        w[i] = __shfl_sync(0xffffffffu, p[y][0][0], src_lane[i]);
-                    } else {
-                        // (8 queries: key i's row half is i >> 1 in every lane)
-                        const int h = QN == 8 && i >= 2 ? NV - 1 : 0;
-                        const float x0 = __shfl_sync(0xffffffffu, p[y][h][0], src_lane[i]);
-                        const float x1 = __shfl_sync(0xffffffffu, p[y][h][NP - 1], src_lane[i]);
-                        w[i] = (my_q & 1) ? x1 : x0;
-                    }
-                }
-                uint32_t pf[PARTS][NT][2];
+                    const bool ok = valid(16 * y + output_key<NG>(c, i));
 #pragma unroll
-                for (int j = 0; j < NT; ++j) {
-                    float ws[4];
+                    for (int j = 0; j < NT; ++j) vsz[y][j][i] = ok ? vsz[y][j][i] : 0u;
+                }
+            }
+        }
+        float smax = 0.f;
+        bool grow = false;
+#pragma unroll
+        for (int y = 0; y < KS; ++y) {
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; i += 2)
+                    smax = fmax3(smax, bf16lo(vsz[y][j][i]), bf16lo(vsz[y][j][i + 1]));
+#pragma unroll
+            for (int h = 0; h < NV; ++h)
+#pragma unroll
+                for (int i = 0; i < NP; ++i) grow |= p[y][h][i] > lim[i];
+        }
+        grow |= smax > slim;
+        if (__any_sync(0xffffffffu, grow)) {  // move the reference to the running maximum
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1)
+                smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, off));
+            // the least power of two above the scales so far, 2^-60 .. 2^100
+            const int se = min(max((int)(__float_as_uint(smax) >> 23) - 126, -60), 100);
+            const float sold = sref;
+            sref = fmaxf(sref, (float)se);
+            slim = exp2f(sref + kScaleGrow);
+            float f[NP];
+#pragma unroll
+            for (int i = 0; i < NP; ++i) {
+                float mx = -INFINITY;
+#pragma unroll
+                for (int y = 0; y < KS; ++y)
+#pragma unroll
+                    for (int h = 0; h < NV; ++h) mx = fmaxf(mx, p[y][h][i]);
+#pragma unroll
+                for (int off = QN == 8 ? 4 : 2; off < 32; off <<= 1)
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                const float mn = fmaxf(m[i] - sold, mx) + sref;
+                f[i] = m[i] == -INFINITY ? 0.f : ex2(m[i] - mn);
+                m[i] = mn;
+                mr[i] = mn == -INFINITY ? 0.f : mn;
+                lim[i] = mn - sref + kGrow;
+                l[i] *= f[i];
+            }
+            // factors of this lane's columns 2c, 2c + 1 and of column r
+            float f0, f1, fr;
+            if constexpr (QN == 2) {
+                f0 = __shfl_sync(0xffffffffu, f[0], lane & ~1);
+                f1 = __shfl_sync(0xffffffffu, f[0], lane | 1);
+                fr = my_q ? f1 : f0;
+            } else {
+                f0 = f[0];
+                f1 = f[NP - 1];
+                const float x0 = __shfl_sync(0xffffffffu, f0, (lane & ~3) | (my_q >> 1));
+                const float x1 = __shfl_sync(0xffffffffu, f1, (lane & ~3) | (my_q >> 1));
+                fr = (my_q & 1) ? x1 : x0;
+            }
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                zacc[j] *= fr;
+                ct[j][0] *= f0;
+                ct[j][1] *= f1;
+                ct[j][2] *= f0;
+                ct[j][3] *= f1;
+            }
+#pragma unroll
+            for (int i = 0; i < OT; ++i) {
+                o[i][0] *= f0;
+                o[i][1] *= f1;
+                o[i][2] *= f0;
+                o[i][3] *= f1;
+            }
+        }
+        if (next.seq != tag.seq) load_queries(next.seq);
+
+        float pn[KS][NV][NP];
+        uint32_t vszn[KS][NT][4];
+        const unsigned char* kn = keys0 + sn * stage_bytes;
+        scores(kn, kn + half_bytes, pn, vszn);
+        const unsigned char* vs = keys0 + s * stage_bytes + half_bytes + v_codes;
+#pragma unroll
+        for (int y = 0; y < KS; ++y) {
+#pragma unroll
+            for (int h = 0; h < NV; ++h)
+#pragma unroll
+                for (int i = 0; i < NP; ++i) {
+                    p[y][h][i] = ex2(p[y][h][i] - mr[i]);
+                    l[i] += p[y][h][i];
+                }
+            // the weights of this lane's 4 keys and query
+            float w[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if constexpr (QN == 2) {
+                    w[i] = __shfl_sync(0xffffffffu, p[y][0][0], src_lane[i]);
+                } else {
+                    // (8 queries: key i's row half is i >> 1 in every lane)
+                    const int h = QN == 8 && i >= 2 ? NV - 1 : 0;
+                    const float x0 = __shfl_sync(0xffffffffu, p[y][h][0], src_lane[i]);
+                    const float x1 = __shfl_sync(0xffffffffu, p[y][h][NP - 1], src_lane[i]);
+                    w[i] = (my_q & 1) ? x1 : x0;
+                }
+            }
+            uint32_t vw[4][2];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const unsigned char* vr = vs + (16 * y + output_key<NG>(0, i)) * R;
+                if constexpr (NG == 4) {
+                    const uint2 x = *reinterpret_cast<const uint2*>(vr);
+                    vw[i][0] = x.x;
+                    vw[i][1] = x.y;
+                } else {
+                    vw[i][0] = *reinterpret_cast<const uint32_t*>(vr);
+                }
+            }
+            // columns: a word per key (its weight in this column's half), or per two
+            // keys
+            constexpr int PW = PAIR ? 4 : 2;
+            uint32_t pf[PARTS][NT][PW];
+#pragma unroll
+            for (int j = 0; j < NT; ++j) {
+                float ws[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    ws[i] = w[i] * bf16lo(vsz[y][j][i]);
+                    zacc[j] = fmaf(w[i], bf16hi(vsz[y][j][i]), zacc[j]);
+                }
+                if constexpr (PAIR) {
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
-                        ws[i] = w[i] * bf16lo(vsz[y][j][i]);
-                        zacc[j] = fmaf(w[i], bf16hi(vsz[y][j][i]), zacc[j]);
+                        float lo = ws[i] * even, hi = ws[i] * odd;
+#pragma unroll
+                        for (int part = 0; part < PARTS; ++part)
+                            pf[part][j][i] = take_f16x2<F32>(lo, hi);
                     }
+                } else {
 #pragma unroll
                     for (int part = 0; part < PARTS; ++part) {
                         pf[part][j][0] = take_f16x2<F32>(ws[0], ws[1]);
                         pf[part][j][1] = take_f16x2<F32>(ws[2], ws[3]);
-                        if constexpr (!F32) {
-                            // -8 in the units of rows r (codes 0, 2) and r + 8 (codes 1, 3)
-                            const uint32_t off[4] = {0x80088008u, 0x80808080u, 0x80088008u,
-                                                     0x80808080u};
-                            mma(ct[j], off, pf[part][j][0], pf[part][j][1]);
-                        }
                     }
                 }
-                uint32_t vw[4][2];
+                if constexpr (!F32) {
+                    // -8 in the units of rows r (codes 0, 2) and r + 8 (codes 1, 3)
+                    const uint32_t off[4] = {0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u};
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const unsigned char* vr = vs + (base + 16 * y + output_key<NG>(c, i)) * R;
-                    if constexpr (NG == 4) {
-                        const uint2 x = *reinterpret_cast<const uint2*>(vr + 8 * r);
-                        vw[i][0] = x.x;
-                        vw[i][1] = x.y;
-                    } else {
-                        vw[i][0] = *reinterpret_cast<const uint32_t*>(vr + 4 * r);
-                    }
+                    for (int i = 0; i < PW; i += 2) mma(ct[j], off, pf[0][j][i], pf[0][j][i + 1]);
                 }
+            }
+            if constexpr (PAIR) {
+#pragma unroll
+                for (int gp = 0; gp < NG / 2; ++gp)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+#pragma unroll
+                        for (int u = 0; u < 4; u += 2) {
+                            const uint32_t af[4] = {
+                                codes<F32>(vw[u][gp], 2 * h), codes<F32>(vw[u][gp], 2 * h + 1),
+                                codes<F32>(vw[u + 1][gp], 2 * h), codes<F32>(vw[u + 1][gp], 2 * h + 1)};
+                            const int j = 2 * gp / CPT;
+#pragma unroll
+                            for (int part = 0; part < PARTS; ++part)
+                                mma(o[2 * gp + h], af, pf[part][j][u], pf[part][j][u + 1]);
+                        }
+            } else {
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     const uint32_t sel = (g & 1) ? 0x7632 : 0x5410;
@@ -810,22 +937,35 @@ q4_split_kernel(const Q4DecodeArgs a) {
                                                 codes<F32>(xb, 2 * h), codes<F32>(xb, 2 * h + 1)};
 #pragma unroll
                         for (int part = 0; part < PARTS; ++part)
-                            mma(o[2 * g + h], af, pf[part][g / CPT][0], pf[part][g / CPT][1]);
+                            mma(o[2 * g + h], af, pf[part][g][0], pf[part][g][1]);
                     }
                 }
             }
-            if (!F32 && ++held == kHold) {
-                held = 0;
-                settle();
-            }
+        }
+        if (!F32 && ++held == kHold) {
+            held = 0;
+            settle();
         }
         __syncwarp();
-        if (lane == 0) mbar_arrive(&empty[s]);
-        if (!tag.last) continue;
+        if (lane == 0) arrive(empty_bar + 8 * s);
+        s = sn;
+        const Tag cur = tag;
+        tag = next;
+#pragma unroll
+        for (int y = 0; y < KS; ++y) {
+#pragma unroll
+            for (int h = 0; h < NV; ++h)
+#pragma unroll
+                for (int i = 0; i < NP; ++i) p[y][h][i] = pn[y][h][i];
+#pragma unroll
+            for (int j = 0; j < NT; ++j)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) vsz[y][j][i] = vszn[y][j][i];
+        }
+        if (!cur.last) continue;
 
         // ---- end of the piece: this warp's state, in output layout: dims 32 g +
         // 4 r .. + 3 of queries 2c, 2c + 1 (mod QN) for g = j CPT + 2c / QN
-        fresh = false;
         if constexpr (!F32) settle();
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
@@ -862,11 +1002,13 @@ q4_split_kernel(const Q4DecodeArgs a) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float u = e & 1 ? 1.f / (16.f * kUnit) : 1.f / kUnit;
-                    val[j][0][e] = fmaf(o[2 * g + (e >> 1)][2 * (e & 1)], u, z0);
-                    val[j][1][e] = fmaf(o[2 * g + (e >> 1)][2 * (e & 1) + 1], u, z1);
+                    const float* x = o[(PAIR ? g >> 1 : g) * 2 + (e >> 1)] + 2 * (e & 1);
+                    val[j][0][e] = fmaf(x[0], u, z0);
+                    val[j][1][e] = fmaf(x[1], u, z1);
                 }
             }
         }
+        clear();
         if (a.wh > 1) {  // the warps of this head and queries: rank 0 merges
             if (rank > 0) {
                 if (merges > 0 &&
@@ -915,7 +1057,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
             ++merges;
         }
         if (rank != 0) continue;
-        const int64_t slot = (int64_t)blockIdx.x + tag.seq;
+        const int64_t slot = (int64_t)blockIdx.x + cur.seq;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int qi = (2 * c + i) % QN;
@@ -1009,7 +1151,7 @@ cudaError_t launch_split(const Q4DecodePlan& p, const Q4DecodeArgs& a, cudaStrea
                                                (int)p.smem_bytes);
     if (e != cudaSuccess) return e;
     return launch_dependent(kern, dim3(p.ctas, p.head_groups),
-                            dim3(kThreads), p.smem_bytes, stream, a);
+                            dim3(threads<QN, F32>()), p.smem_bytes, stream, a);
 }
 
 }  // namespace
@@ -1021,9 +1163,9 @@ bool plan_q4_decode(const DeviceInfo& dev, int32_t batch, int32_t max_blocks, in
     // hold an even number of rows
     if (d == 64 && block_size % 2) return false;
     const bool f32 = q_dtype == PKV_F32;
-    const int wc = kConsumers;
     const int G = hq / hkv;
     p->qn = G <= 2 ? 2 : (G <= 4 ? 4 : 8);
+    const int wc = f32 || p->qn == 8 ? consumers<8, true>() : consumers<2, false>();
     p->no = (G + p->qn - 1) / p->qn;
     if (p->no > wc) return false;
     p->hc = 1;  // the most KV heads whose queries the consumer warps hold
@@ -1033,7 +1175,7 @@ bool plan_q4_decode(const DeviceInfo& dev, int32_t batch, int32_t max_blocks, in
     if (p->head_groups > 65535) return false;
     const int units = p->hc * p->no;
     p->wh = wc / units;
-    p->tile = 16 * key_steps_of(p->qn, f32) * p->wh;
+    p->tile = 16 * (f32 || p->qn == 8 ? key_steps<8, true>() : key_steps<2, false>()) * p->wh;
     const int R = q4_row_bytes(d);
     const int nt = std::max(1, d / kQ4Group * p->qn / 8);
     const size_t stage = (size_t)2 * p->hc * p->tile * R;
