@@ -1076,39 +1076,61 @@ q4_split_kernel(const Q4DecodeArgs a) {
     }
 }
 
-// ---- combine: one warp per (sequence, query head) -------------------------------
+// ---- combine ---------------------------------------------------------------------
+// Merges the partial states of a (sequence, query head) and normalises.  W warps
+// share one, each with every W-th piece, up to 8 in flight: a batch of one has as
+// many pieces as CTAs, and 19 rounds of one warp took 15 us of a 21 us call.
 struct Q4CombineArgs {
     const float* part_o;
     const float* part_ml;
     const int32_t* tstart;
     void* out;
     int32_t batch, hq, ctas;
+    int32_t w;  // warps per (sequence, query head)
 };
-constexpr int kCombineWarps = 4;
-constexpr int kCombineLoads = 8;  // partial states in flight
+constexpr int kCombineWarps = 4;  // at least, per CTA
+constexpr int kCombineLoads = 8;  // partial states in flight per warp
+constexpr int kCombineMost = 16;  // warps of one (sequence, query head)
+
+// the state (mo, lo, x) joins (M, L, acc)
+template <int E>
+__device__ __forceinline__ void join(float& M, float& L, float* acc, float mo, float lo,
+                                     const float* x) {
+    if (mo == -INFINITY) return;  // holds nothing
+    const float mn = fmaxf(M, mo);
+    const float ca = M == -INFINITY ? 0.f : ex2(M - mn), cb = ex2(mo - mn);
+    L = L * ca + lo * cb;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = acc[e] * ca + x[e] * cb;
+    M = mn;
+}
 
 template <int D, bool F32>
-__global__ void __launch_bounds__(kCombineWarps * 32) q4_combine_kernel(const Q4CombineArgs a) {
+__global__ void __launch_bounds__(kCombineMost * 32) q4_combine_kernel(const Q4CombineArgs a) {
     PKV_DEPENDENT_PROLOGUE();
     constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (int64_t)blockIdx.x * kCombineWarps + (threadIdx.x >> 5);
-    if (w >= (int64_t)a.batch * a.hq) return;
-    const int b = (int)(w / a.hq), h = (int)(w % a.hq);
+    __shared__ float part[kCombineMost][32 * E + 2];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int per_cta = (blockDim.x >> 5) / a.w;  // (sequence, query head)s per CTA: 1 if w > 1
+    const int rank = warp % a.w;
+    const int64_t id = (int64_t)blockIdx.x * per_cta + warp / a.w;
+    const bool live = id < (int64_t)a.batch * a.hq;
+    const int b = live ? (int)(id / a.hq) : 0, h = live ? (int)(id % a.hq) : 0;
     const int32_t ta = a.tstart[b], tb = a.tstart[b + 1];
     const int32_t len = share_len(a.tstart[a.batch], a.batch, a.ctas);
-    const int c0 = (ta + b + 1) / len, c1 = tb > ta ? (tb + b) / len : c0 - 1;
+    const int c0 = (ta + b + 1) / len, c1 = tb > ta && live ? (tb + b) / len : c0 - 1;
     float M = -INFINITY, L = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int base = c0; base <= c1; base += kCombineLoads) {
+    for (int base = c0 + rank; base <= c1; base += kCombineLoads * a.w) {
         float2 ml[kCombineLoads];
         float x[kCombineLoads][E];
 #pragma unroll
         for (int i = 0; i < kCombineLoads; ++i) {
+            const int piece = base + i * a.w;
             ml[i] = make_float2(-INFINITY, 0.f);
-            if (base + i <= c1) {
-                const int64_t at = ((int64_t)(base + i) + b) * a.hq + h;
+            if (piece <= c1) {
+                const int64_t at = ((int64_t)piece + b) * a.hq + h;
                 ml[i] = *reinterpret_cast<const float2*>(a.part_ml + at * 2);
                 const float* p = a.part_o + at * D + lane * E;
                 if constexpr (E == 4) {
@@ -1121,18 +1143,27 @@ __global__ void __launch_bounds__(kCombineWarps * 32) q4_combine_kernel(const Q4
             }
         }
 #pragma unroll
-        for (int i = 0; i < kCombineLoads; ++i) {
-            if (ml[i].x == -INFINITY) continue;  // holds nothing
-            const float mn = fmaxf(M, ml[i].x);
-            const float ca = M == -INFINITY ? 0.f : ex2(M - mn), cb = ex2(ml[i].x - mn);
-            L = L * ca + ml[i].y * cb;
+        for (int i = 0; i < kCombineLoads; ++i) join<E>(M, L, acc, ml[i].x, ml[i].y, x[i]);
+    }
+    if (a.w > 1) {  // (then the CTA is one (sequence, query head))
 #pragma unroll
-            for (int e = 0; e < E; ++e) acc[e] = acc[e] * ca + x[i][e] * cb;
-            M = mn;
+        for (int e = 0; e < E; ++e) part[warp][e * 32 + lane] = acc[e];
+        if (lane == 0) {
+            part[warp][32 * E] = M;
+            part[warp][32 * E + 1] = L;
+        }
+        __syncthreads();
+        if (warp > 0) return;
+        for (int w = 1; w < a.w; ++w) {
+            float x[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e) x[e] = part[w][e * 32 + lane];
+            join<E>(M, L, acc, part[w][32 * E], part[w][32 * E + 1], x);
         }
     }
+    if (!live) return;
     const float inv = L == 0.f ? 0.f : 1.f / L;
-    const int64_t at = w * D + lane * E;
+    const int64_t at = id * D + lane * E;
     if constexpr (F32) {
         float* o = static_cast<float*>(a.out) + at;
 #pragma unroll
@@ -1238,12 +1269,16 @@ cudaError_t launch_q4_decode(const Q4DecodePlan& p, const void* q, const void* k
     PKV_Q4_CASE(2, 2, true) PKV_Q4_CASE(2, 4, true) PKV_Q4_CASE(2, 8, true)
 #undef PKV_Q4_CASE
     if (e != cudaSuccess) return e;
-    const Q4CombineArgs c{a.part_o, a.part_ml, a.tstart, out, batch, hq, p.ctas};
+    // pieces of a sequence: about its share of the CTAs, and one at either end
+    const int pieces = p.ctas / batch + 2;
+    const int w = std::min(kCombineMost, (pieces + kCombineLoads - 1) / kCombineLoads);
+    const Q4CombineArgs c{a.part_o, a.part_ml, a.tstart, out, batch, hq, p.ctas, w};
     auto kern = d == 128 ? (f32 ? q4_combine_kernel<128, true> : q4_combine_kernel<128, false>)
                          : (f32 ? q4_combine_kernel<64, true> : q4_combine_kernel<64, false>);
-    const int64_t warps = (int64_t)batch * hq;
-    return launch_dependent(kern, dim3((unsigned)((warps + kCombineWarps - 1) / kCombineWarps)),
-                            dim3(kCombineWarps * 32), 0, stream, c);
+    const int per_cta = w > 1 ? 1 : kCombineWarps;
+    const int64_t pairs = (int64_t)batch * hq;
+    return launch_dependent(kern, dim3((unsigned)((pairs + per_cta - 1) / per_cta)),
+                            dim3(per_cta * w * 32), 0, stream, c);
 }
 
 }  // namespace pkv
