@@ -59,27 +59,18 @@ namespace pkv {
 namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr int kHold = 8;          // steps between additions of the offsets' sums
+constexpr int kHold = 16;         // 16-key products between additions of the offsets' sums
 constexpr float kGrow = 8.f;       // rescale when a score passes the reference by 2^8
 constexpr float kScaleGrow = 4.f;  // or a V scale its bound by 2^4: weights stay below 2^12
+constexpr int kConsumers = 8;  // 12 warps in all leave 168 registers a thread
+constexpr int kProducers = 4;
+constexpr int kThreads = (kConsumers + kProducers) * 32;
 constexpr int kMaxStages = 8;
 constexpr int kHeader = 512;  // barriers and stage tags
 
-constexpr int kProducers = 4;  // producer warps, each with every 4th tile
-
-// Consumer warps and the 16-key products one runs side by side.  With 2 or 4
-// queries 16 warps fit (20 warps are launched with 96 registers; setmaxnreg
-// moves some from the producers' warpgroup to the consumers'); 8 queries and
-// fp32 ones keep more in registers and run 8 (12 warps with 168).
+// 16-key products that a warp runs side by side (its share of a tile)
 template <int QN, bool F32>
-__host__ __device__ constexpr int consumers() { return 8; }
-template <int QN, bool F32>
-__host__ __device__ constexpr int key_steps() { return F32 || QN == 8 ? 1 : 2; }
-template <int QN, bool F32>
-__host__ __device__ constexpr int threads() { return (consumers<QN, F32>() + kProducers) * 32; }
-constexpr int kConsumerRegs = 104, kProducerRegs = 64;
-static_assert(16 * kConsumerRegs + kProducers * kProducerRegs <= 20 * 96,
-              "register split exceeds the launch");
+__host__ __device__ constexpr int key_steps() { return QN == 8 ? 1 : 2; }
 
 struct Q4DecodeArgs {
     const void* q;
@@ -97,15 +88,19 @@ struct Q4DecodeArgs {
     int32_t hc;      // KV heads per CTA
     int32_t no;      // warps' worth of query heads per KV head
     int32_t wh;      // warps that share a head and its queries (16 keys each)
-    int32_t tile;    // keys per stage
     int32_t stages;
+    FastDiv block;   // by the page size
 };
 
-// one stage's description, written by the producer
+// One stage's description, written by the producer: a word of flags and the key
+// count, which every tile reads, and what only some do.
+constexpr uint32_t kTagLast = 1;     // the piece of the sequence ends here
+constexpr uint32_t kTagFirst = 2;    // a sequence starts in this CTA: load its queries
+constexpr uint32_t kTagPartial = 4;  // fewer keys than the tile holds, or a bad page
 struct Tag {
-    int32_t seq;   // sequence
+    uint32_t flags;
     int32_t rows;  // keys
-    int32_t last;  // the piece of the sequence ends here
+    int32_t seq;   // sequence
     int32_t bad;   // first key's position if a page was out of range, else -1
 };
 
@@ -233,9 +228,9 @@ __device__ __forceinline__ void score_row(int key, int* r, int* half) {
 }
 
 template <int NG, int QN, bool F32>
-__global__ void __launch_bounds__(threads<QN, F32>(), 1)
+__global__ void __launch_bounds__(kThreads, 1)
 q4_split_kernel(const Q4DecodeArgs a) {
-    constexpr int WC = consumers<QN, F32>();
+    constexpr int WC = kConsumers;
     constexpr int D = NG * kQ4Group, R = q4_row_bytes(D);
     constexpr int CPT = 8 / QN;                    // groups per column tile
     constexpr int NT = NG > CPT ? NG / CPT : 1;    // column tiles
@@ -243,7 +238,6 @@ q4_split_kernel(const Q4DecodeArgs a) {
     constexpr int NP = QN == 2 ? 1 : 2;            // queries a lane takes exponentials for
     constexpr int NV = QN == 8 ? 2 : 1;            // score rows a lane takes them for
     constexpr int KS = key_steps<QN, F32>();       // 16-key products side by side
-    constexpr int KEYS = 16 * KS;
     extern __shared__ __align__(128) unsigned char smem[];
     uint64_t* full = reinterpret_cast<uint64_t*>(smem);
     uint64_t* empty = full + kMaxStages;
@@ -253,12 +247,16 @@ q4_split_kernel(const Q4DecodeArgs a) {
     unsigned char* scratch = smem + kHeader + up((size_t)(a.batch + 1) * 4, 128);
     const int units = a.hc * a.no;  // (head, queries) of the CTA
     unsigned char* ring = scratch + (size_t)units * (a.wh - 1) * state_bytes(NT);
-    __shared__ int32_t warp_sum[threads<QN, F32>() / 32];
+    __shared__ int32_t warp_sum[kThreads / 32];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int S = a.stages, T = a.tile;
-    const size_t half_bytes = (size_t)a.hc * T * R;  // K (or V) of a stage
-    const int active = units * a.wh;                 // consumer warps at work
+    // A tile is the next T = KEYS * wh keys of a sequence: KEYS for each of the
+    // wh warps of a head.
+    constexpr int KEYS = 16 * KS;
+    const int S = a.stages, T = KEYS * a.wh;
+    const uint32_t half_bytes = (uint32_t)(a.hc * T * R);  // K (or V) of a stage
+    const uint32_t stage_bytes = 2 * half_bytes;
+    const int active = units * a.wh;  // consumer warps at work
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
             mbar_init(&full[s], 1);
@@ -274,7 +272,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
     const int64_t cap = (int64_t)a.max_blocks * a.block_size;
     const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0;
     {
-        constexpr int N = threads<QN, F32>();
+        constexpr int N = kThreads;
         const int per = (a.batch + N - 1) / N;
         const int lo = tid * per, hi = min(lo + per, a.batch);
         int32_t sum = 0;
@@ -315,8 +313,6 @@ q4_split_kernel(const Q4DecodeArgs a) {
 
     if (warp >= WC) {
         // ------------------------------ producers -----------------------------
-        if constexpr (WC == 16)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kProducerRegs));
         // Warp w prepares tiles t0 + w, t0 + w + 4, ..: one tile costs a chain of
         // ~2000 cycles (slot, table entry, address, barrier) whatever its size.
         // No more warps than stages: a warp then has seen its stage's last but one
@@ -341,7 +337,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
         int32_t L = (int32_t)min((int64_t)max(__ldg(a.seqlens + b), 0), cap);
         // ids of a tile's first 32 pages, one tile ahead
         auto fetch = [&](int bb, int32_t p0, int32_t p1) {
-            const int32_t pg = p0 / a.block_size + lane;
+            const int32_t pg = (int32_t)a.block.quot((uint32_t)p0) + lane;
             return (int64_t)pg * a.block_size < p1
                        ? __ldg(a.table + (int64_t)bb * a.max_blocks + pg) : -1;
         };
@@ -365,8 +361,8 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 next_page = fetch(b, p0, p1);
             }
             const int32_t k = t - t0;
-            const int32_t pg0 = q0 / a.block_size;
-            const int np = (q1 - 1) / a.block_size - pg0 + 1;
+            const int32_t pg0 = (int32_t)a.block.quot((uint32_t)q0);
+            const int np = (int32_t)a.block.quot((uint32_t)(q1 - 1)) - pg0 + 1;
             // the bytes that will arrive
             uint32_t bytes = 0;
             bool bad = false;
@@ -388,7 +384,10 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 ok = mbar_wait(&empty[s], (fills & 1) ^ 1, a.err);
                 if (ok) {
                     if (bad) flag_error(a.err, PKV_FLAG_BAD_BLOCK);
-                    tags[s] = Tag{seq, q1 - q0, last ? 1 : 0, bad ? q0 : -1};
+                    tags[s] = Tag{(last ? kTagLast : 0u) |
+                                      (k == 0 || t == tstart[seq] ? kTagFirst : 0u) |
+                                      (bad || q1 - q0 < T ? kTagPartial : 0u),
+                                  q1 - q0, seq, bad ? q0 : -1};
                     mbar_arrive_expect_tx(&full[s], bytes);
                 }
             }
@@ -432,7 +431,6 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 if (!mbar_wait(&full[k % S], (k / S) & 1, a.err)) break;
         return;
     }
-    if constexpr (WC == 16) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kConsumerRegs));
     if (warp >= active) return;
 
     // ------------------------------- consumers --------------------------------
@@ -461,7 +459,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
     // (zeros meet the other half), and need no rearranging.  With 8 queries a tile
     // holds one group and a byte permutation brings its codes together.
     constexpr bool PAIR = QN < 8;
-    const float even = ((r / QN) & 1) ? 0.f : 1.f, odd = 1.f - even;  // this column's half
+    const uint32_t half_shift = (r / QN) & 1 ? 16 : 0;  // this column's half
     uint32_t qf[PARTS][NG][4];  // score product's columns: 2 k-steps of 2 words per code word
     float qs[NT][2];            // 2^-24 sum of q over the group of columns 2c, 2c + 1
     float start[NT][2];         // -8 times those: where a score product starts
@@ -471,7 +469,6 @@ q4_split_kernel(const Q4DecodeArgs a) {
     // reference of the queries' weights, the same with -inf as 0, and the score
     // that makes it move; log2 of the V scale it counts with, and their limit
     float m[NP], mr[NP], lim[NP], sref = 0.f, slim = 0.f;
-    int held = 0;               // steps since the offsets' sums were last added
     auto settle = [&]() {
 #pragma unroll
         for (int i = 0; i < OT; ++i)
@@ -493,7 +490,6 @@ q4_split_kernel(const Q4DecodeArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) ct[j][e] = 0.f;
         }
-        held = 0;
         sref = -60.f;
         slim = 0.f;
 #pragma unroll
@@ -580,10 +576,10 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 for (int u = 0; u < 2; ++u)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float lo = x[4 * u + e] * even, hi = x[4 * u + e] * odd;
+                        float none = 0.f;
 #pragma unroll
                         for (int part = 0; part < PARTS; ++part) {
-                            const uint32_t w = take_f16x2<F32>(lo, hi);
+                            const uint32_t w = take_f16x2<F32>(x[4 * u + e], none) << half_shift;
 #pragma unroll
                             for (int gp = 0; gp < NG / 2; ++gp)
                                 if (2 * gp / CPT == j && g_col >> 1 == gp)
@@ -609,14 +605,16 @@ q4_split_kernel(const Q4DecodeArgs a) {
     const bool k_live = NT * CPT <= NG || 2 * c / QN < NG, v_live = NT * CPT <= NG || r / QN < NG;
     // scores of the step's keys in log2 units, for this lane's rows and queries,
     // and the V scales of its keys and columns
-    auto scores = [&](const unsigned char* ks, const unsigned char* vs,
-                      float (&p)[KS][NV][NP], uint32_t (&vsz)[KS][NT][4]) {
+    auto scores = [&](const unsigned char* tile, float (&p)[KS][NV][NP],
+                      uint32_t (&vsz)[KS][NT][4]) {
 #pragma unroll
         for (int y = 0; y < KS; ++y) {
+            const unsigned char* ks = tile + y * 16 * R;
+            const unsigned char* vs = ks + half_bytes;
             uint32_t kw[2][NG], ksz[NT][2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                const unsigned char* at = ks + k_codes + 16 * y * R + h * kHalfRow;
+                const unsigned char* at = ks + k_codes + h * kHalfRow;
                 if constexpr (NG == 4) {
                     const uint4 w = *reinterpret_cast<const uint4*>(at);
                     kw[h][0] = w.x; kw[h][1] = w.y; kw[h][NG - 2] = w.z; kw[h][NG - 1] = w.w;
@@ -626,8 +624,8 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 }
 #pragma unroll
                 for (int j = 0; j < NT; ++j) {
-                    ksz[j][h] = *reinterpret_cast<const uint32_t*>(ks + k_scale + 16 * y * R +
-                                                                   h * kHalfRow + 4 * CPT * j);
+                    ksz[j][h] = *reinterpret_cast<const uint32_t*>(ks + k_scale + h * kHalfRow +
+                                                                   4 * CPT * j);
                     if (!k_live) ksz[j][h] = 0u;
                 }
             }
@@ -636,10 +634,10 @@ q4_split_kernel(const Q4DecodeArgs a) {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     vsz[y][j][i] = *reinterpret_cast<const uint32_t*>(
-                        vs + v_scale + 16 * y * R + output_key<NG>(0, i) * R + 4 * CPT * j);
+                        vs + v_scale + output_key<NG>(0, i) * R + 4 * CPT * j);
                     if (!v_live) vsz[y][j][i] = 0u;
                 }
-            float sc[NT][4], alt[4];
+            float sc[NT][4];
 #pragma unroll
             for (int w = 0; w < NG; ++w) {
                 uint32_t x[2];
@@ -655,16 +653,13 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 for (int st = 0; st < 2; ++st) {
                     const uint32_t af[4] = {codes<F32>(x[0], 2 * st), codes<F32>(x[1], 2 * st),
                                             codes<F32>(x[0], 2 * st + 1), codes<F32>(x[1], 2 * st + 1)};
-                    // one tile: two chains
-                    float* to = NT == 1 && st ? alt : sc[j];
 #pragma unroll
                     for (int part = 0; part < PARTS; ++part) {
                         const uint32_t b0 = qf[part][w][2 * st], b1 = qf[part][w][2 * st + 1];
-                        if (opens && part == 0 && (st == 0 || NT == 1)) {
-                            const bool at = st == 0 && !F32;
-                            mma_from(to, af, b0, b1, at ? start[j][0] : 0.f, at ? start[j][1] : 0.f);
+                        if (opens && part == 0 && st == 0) {
+                            mma_from(sc[j], af, b0, b1, start[j][0], start[j][1]);
                         } else {
-                            mma(to, af, b0, b1);
+                            mma(sc[j], af, b0, b1);
                         }
                     }
                 }
@@ -678,8 +673,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
                     v[h][i] = 0.f;
 #pragma unroll
                     for (int j = 0; j < NT; ++j) {
-                        const float x = NT == 1 ? sc[j][2 * h + i] + alt[2 * h + i] : sc[j][2 * h + i];
-                        v[h][i] = fmaf(bf16lo(ksz[j][h]), x, v[h][i]);
+                        v[h][i] = fmaf(bf16lo(ksz[j][h]), sc[j][2 * h + i], v[h][i]);
                         v[h][i] = fmaf(bf16hi(ksz[j][h]), qs[j][i], v[h][i]);
                     }
                 }
@@ -714,37 +708,29 @@ q4_split_kernel(const Q4DecodeArgs a) {
     const int32_t n_tiles = t1 - t0;
     uint32_t full_bar = smem_u32(full), empty_bar = smem_u32(empty);
     asm volatile("" : "+r"(full_bar), "+r"(empty_bar));  // (keep them)
-    // this warp's keys in stage 0 (one step per tile)
-    const unsigned char* keys0 = ring + ((size_t)hc * T + rank * KEYS) * R;
-    const uint32_t stage_bytes = 2 * (uint32_t)half_bytes;
+    // this warp's keys in stage 0
+    const unsigned char* keys0 = ring + (hc * T + rank * KEYS) * R;
     float p[KS][NV][NP];
     uint32_t vsz[KS][NT][4];
-    if (!wait_phase(full_bar, 0, a.err)) return;
-    Tag tag = tags[0];
-    load_queries(tag.seq);
     clear();
-    scores(keys0, keys0 + half_bytes, p, vsz);
 
-    // Tile k's weights and output products run beside tile k + 1's scores, which
-    // need nothing of them: the two fill each other's latencies.
-    int s = 0, sn = 0;        // stages of tile k and of the next
-    uint32_t phase = 0;       // of stage sn
+    int s = 0;
+    uint32_t phase = 0;  // of stage s
     for (int32_t k = 0; k < n_tiles; ++k) {
-        if (k + 1 < n_tiles) {  // (after the last tile: itself again, unused)
-            if (++sn == S) {
-                sn = 0;
-                phase ^= 1;
-            }
-            if (!wait_phase(full_bar + 8 * sn, phase, a.err)) break;
-        }
-        const Tag next = tags[sn];
-        const int base = rank * KEYS;
-        if (base + KEYS > tag.rows || tag.bad >= 0) {  // keys that do not count
+        if (!wait_phase(full_bar + 8 * s, phase, a.err)) break;
+        const uint32_t flags = tags[s].flags;
+        if (__builtin_expect(flags & kTagFirst, 0)) load_queries(tags[s].seq);
+        const unsigned char* tile = keys0 + s * stage_bytes;
+        scores(tile, p, vsz);
+        if (__builtin_expect(flags & kTagPartial, 0)) {
+            // keys that do not count: scores of -inf, scales of 0
+            const Tag tag = tags[s];
             auto valid = [&](int key) {
-                if (base + key >= tag.rows) return false;
+                const int at = rank * KEYS + key;
+                if (at >= tag.rows) return false;
                 if (tag.bad < 0) return true;
                 const int32_t id = __ldg(a.table + (int64_t)tag.seq * a.max_blocks +
-                                         (tag.bad + base + key) / a.block_size);
+                                         (tag.bad + at) / a.block_size);
                 return id >= 0 && id < a.num_blocks;
             };
 #pragma unroll
@@ -778,7 +764,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 for (int i = 0; i < NP; ++i) grow |= p[y][h][i] > lim[i];
         }
         grow |= smax > slim;
-        if (__any_sync(0xffffffffu, grow)) {  // move the reference to the running maximum
+        if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {  // move the reference to the running maximum
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1)
                 smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, off));
@@ -834,13 +820,6 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 o[i][3] *= f1;
             }
         }
-        if (next.seq != tag.seq) load_queries(next.seq);
-
-        float pn[KS][NV][NP];
-        uint32_t vszn[KS][NT][4];
-        const unsigned char* kn = keys0 + sn * stage_bytes;
-        scores(kn, kn + half_bytes, pn, vszn);
-        const unsigned char* vs = keys0 + s * stage_bytes + half_bytes + v_codes;
 #pragma unroll
         for (int y = 0; y < KS; ++y) {
 #pragma unroll
@@ -867,7 +846,8 @@ q4_split_kernel(const Q4DecodeArgs a) {
             uint32_t vw[4][2];
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const unsigned char* vr = vs + (16 * y + output_key<NG>(0, i)) * R;
+                const unsigned char* vr =
+                    tile + half_bytes + v_codes + (16 * y + output_key<NG>(0, i)) * R;
                 if constexpr (NG == 4) {
                     const uint2 x = *reinterpret_cast<const uint2*>(vr);
                     vw[i][0] = x.x;
@@ -890,12 +870,12 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 }
                 if constexpr (PAIR) {
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        float lo = ws[i] * even, hi = ws[i] * odd;
+                    for (int part = 0; part < PARTS; ++part)
 #pragma unroll
-                        for (int part = 0; part < PARTS; ++part)
-                            pf[part][j][i] = take_f16x2<F32>(lo, hi);
-                    }
+                        for (int i = 0; i < 4; ++i) {
+                            float none = 0.f;
+                            pf[part][j][i] = take_f16x2<F32>(ws[i], none) << half_shift;
+                        }
                 } else {
 #pragma unroll
                     for (int part = 0; part < PARTS; ++part) {
@@ -942,27 +922,16 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 }
             }
         }
-        if (!F32 && ++held == kHold) {
-            held = 0;
-            settle();
-        }
+        if (!F32 && k % (kHold / KS) == 0) settle();
+        const bool ends = flags & kTagLast;
+        const int seq = ends ? tags[s].seq : 0;  // (before the stage is given back)
         __syncwarp();
         if (lane == 0) arrive(empty_bar + 8 * s);
-        s = sn;
-        const Tag cur = tag;
-        tag = next;
-#pragma unroll
-        for (int y = 0; y < KS; ++y) {
-#pragma unroll
-            for (int h = 0; h < NV; ++h)
-#pragma unroll
-                for (int i = 0; i < NP; ++i) p[y][h][i] = pn[y][h][i];
-#pragma unroll
-            for (int j = 0; j < NT; ++j)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) vsz[y][j][i] = vszn[y][j][i];
+        if (++s == S) {
+            s = 0;
+            phase ^= 1;
         }
-        if (!cur.last) continue;
+        if (!ends) continue;
 
         // ---- end of the piece: this warp's state, in output layout: dims 32 g +
         // 4 r .. + 3 of queries 2c, 2c + 1 (mod QN) for g = j CPT + 2c / QN
@@ -1057,7 +1026,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
             ++merges;
         }
         if (rank != 0) continue;
-        const int64_t slot = (int64_t)blockIdx.x + cur.seq;
+        const int64_t slot = (int64_t)blockIdx.x + seq;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int qi = (2 * c + i) % QN;
@@ -1182,7 +1151,7 @@ cudaError_t launch_split(const Q4DecodePlan& p, const Q4DecodeArgs& a, cudaStrea
                                                (int)p.smem_bytes);
     if (e != cudaSuccess) return e;
     return launch_dependent(kern, dim3(p.ctas, p.head_groups),
-                            dim3(threads<QN, F32>()), p.smem_bytes, stream, a);
+                            dim3(kThreads), p.smem_bytes, stream, a);
 }
 
 }  // namespace
@@ -1190,13 +1159,15 @@ cudaError_t launch_split(const Q4DecodePlan& p, const Q4DecodeArgs& a, cudaStrea
 bool plan_q4_decode(const DeviceInfo& dev, int32_t batch, int32_t max_blocks, int hq, int hkv,
                     int d, int block_size, int q_dtype, Q4DecodePlan* p) {
     if ((d != 64 && d != 128) || batch > kDecodeMaxBatch) return false;
+    // positions, and a tile beyond, in 32 bits
+    if ((double)max_blocks * block_size > 2147483647.0 - 4096) return false;
     // rows of 40 bytes: copies of a page piece start on 16 bytes when pages
     // hold an even number of rows
     if (d == 64 && block_size % 2) return false;
     const bool f32 = q_dtype == PKV_F32;
     const int G = hq / hkv;
     p->qn = G <= 2 ? 2 : (G <= 4 ? 4 : 8);
-    const int wc = f32 || p->qn == 8 ? consumers<8, true>() : consumers<2, false>();
+    const int wc = kConsumers;
     p->no = (G + p->qn - 1) / p->qn;
     if (p->no > wc) return false;
     p->hc = 1;  // the most KV heads whose queries the consumer warps hold
@@ -1206,7 +1177,7 @@ bool plan_q4_decode(const DeviceInfo& dev, int32_t batch, int32_t max_blocks, in
     if (p->head_groups > 65535) return false;
     const int units = p->hc * p->no;
     p->wh = wc / units;
-    p->tile = 16 * (f32 || p->qn == 8 ? key_steps<8, true>() : key_steps<2, false>()) * p->wh;
+    p->tile = 16 * (p->qn == 8 ? key_steps<8, false>() : key_steps<2, false>()) * p->wh;
     const int R = q4_row_bytes(d);
     const int nt = std::max(1, d / kQ4Group * p->qn / 8);
     const size_t stage = (size_t)2 * p->hc * p->tile * R;
@@ -1257,7 +1228,7 @@ cudaError_t launch_q4_decode(const Q4DecodePlan& p, const void* q, const void* k
     a.hc = p.hc;
     a.no = p.no;
     a.wh = p.wh;
-    a.tile = p.tile;
+    a.block = FastDiv((uint32_t)block_size);
     a.stages = p.stages;
     const bool f32 = q_dtype == PKV_F32;
     cudaError_t e = cudaErrorInvalidValue;
