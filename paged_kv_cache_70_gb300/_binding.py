@@ -669,7 +669,54 @@ def paged_mixed_step(k_cache: torch.Tensor, v_cache: torch.Tensor, scale: float,
     return pout, dout
 
 
-# ---- 4-bit pools ---------------------------------------------------------------
+# ---- 4-bit pools and compaction -------------------------------------------------
+# These are called once per layer and step on a few sequences as often as on many,
+# so what a call costs on the host is kept short: one pass over its tensors, the
+# geometry and workspace sizes looked up, the device switched only when it differs.
+
+try:  # the raw handle, without building a Stream object
+    from torch._C import _cuda_getCurrentRawStream as _raw_stream
+except ImportError:  # pragma: no cover - a torch build without it
+    def _raw_stream(index: int) -> int:
+        return torch.cuda.current_stream(index).cuda_stream
+
+_geoms: dict = {}
+_sizes: dict = {}
+
+
+def _geom(*key):
+    """pkv_geom by reference, built once per geometry."""
+    g = _geoms.get(key)
+    if g is None:
+        if len(_geoms) > 1000:
+            _geoms.clear()
+        g = _geoms[key] = Geom(*key)
+    return ctypes.byref(g)
+
+
+def _arg(name: str, t: torch.Tensor, index: int, dtype=None) -> int:
+    """The address of a contiguous tensor on device `index`."""
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor" if not t.is_cuda else
+                         f"{name} must be on the device of the other tensors")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    return t.data_ptr()
+
+
+def _launch(func: str, index: int, *args) -> None:
+    """The library's `func` on the current stream of device `index`."""
+    fn = getattr(_lib, func)
+    if torch.cuda.current_device() == index:
+        st = fn(*args, _raw_stream(index))
+    else:
+        with torch.cuda.device(index):
+            st = fn(*args, _raw_stream(index))
+    if st:
+        _check(func, st)
+
 
 def q4_cache_shape(num_blocks: int, block_size: int, num_kv_heads: int,
                    head_dim: int) -> tuple[int, int, int, int]:
@@ -680,35 +727,36 @@ def q4_cache_shape(num_blocks: int, block_size: int, num_kv_heads: int,
     return num_blocks, num_kv_heads, block_size, head_dim * 5 // 8
 
 
-def q4_geom_of(k_cache: torch.Tensor, num_heads: int) -> Geom:
-    """pkv_geom of a 4-bit pool [num_blocks, num_kv_heads, block_size, 5 d / 8]."""
+def _q4_shape(k_cache: torch.Tensor):
+    """(num_blocks, num_kv_heads, block_size, head_dim) of a 4-bit pool."""
     if k_cache.dtype != torch.uint8 or k_cache.dim() != 4 or k_cache.shape[3] not in (40, 80):
         raise ValueError("a 4-bit pool is uint8 [num_blocks, Hkv, block_size, 5 * head_dim / 8]")
     nb, hkv, bs, r = k_cache.shape
-    return Geom(num_heads, hkv, r * 8 // 5, bs, nb, PKV_Q4)
+    return nb, hkv, bs, r * 8 // 5
+
+
+def q4_geom_of(k_cache: torch.Tensor, num_heads: int) -> Geom:
+    """pkv_geom of a 4-bit pool [num_blocks, num_kv_heads, block_size, 5 d / 8]."""
+    nb, hkv, bs, d = _q4_shape(k_cache)
+    return Geom(num_heads, hkv, d, bs, nb, PKV_Q4)
 
 
 def paged_kv_write_q4(k: torch.Tensor, v: torch.Tensor, slot_mapping: torch.Tensor,
                       k_cache: torch.Tensor, v_cache: torch.Tensor) -> None:
     """In-place write of k/v [N, Hkv, d] rows (fp32 or bf16) into 4-bit pools
     (q4_cache_shape) at slot_mapping; negative slots are skipped."""
-    _cuda_contig("k", k)
-    _cuda_contig("v", v, k.dtype)
-    _cuda_contig("slot_mapping", slot_mapping, torch.int32)
-    _cuda_contig("k_cache", k_cache)
-    _cuda_contig("v_cache", v_cache, torch.uint8)
-    g = q4_geom_of(k_cache, k_cache.shape[1])
+    index = k.get_device()
+    nb, hkv, bs, d = _q4_shape(k_cache)
     n = k.shape[0]
-    if k.shape != v.shape or k.shape[1:] != (g.num_kv_heads, g.head_dim) or \
-            v_cache.shape != k_cache.shape:
+    if k.shape != v.shape or k.shape[1:] != (hkv, d) or v_cache.shape != k_cache.shape:
         raise ValueError("shape mismatch between k/v rows and the pools")
     if slot_mapping.numel() != n:
         raise ValueError("slot_mapping must have one entry per token row")
-    with torch.cuda.device(k.device):
-        st = load_library().paged_kv_write_q4(
-            _ptr(k), _ptr(v), _dtype_code(k), _ptr(slot_mapping), n, _ptr(k_cache), _ptr(v_cache),
-            ctypes.byref(g), _stream(k))
-    _check("paged_kv_write_q4", st)
+    load_library()
+    _launch("paged_kv_write_q4", index, _arg("k", k, index), _arg("v", v, index, k.dtype),
+            _dtype_code(k), _arg("slot_mapping", slot_mapping, index, torch.int32), n,
+            _arg("k_cache", k_cache, index), _arg("v_cache", v_cache, index, torch.uint8),
+            _geom(hkv, hkv, d, bs, nb, PKV_Q4))
 
 
 def paged_kv_read_q4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping: torch.Tensor,
@@ -716,36 +764,45 @@ def paged_kv_read_q4(k_cache: torch.Tensor, v_cache: torch.Tensor, slot_mapping:
                      v_out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """The values [N, Hkv, d] that 4-bit pools hold at slot_mapping [N], in
     ``dtype`` (fp32 or bf16); rows of zeros at negative slots."""
-    _cuda_contig("slot_mapping", slot_mapping, torch.int32)
-    _cuda_contig("k_cache", k_cache)
-    _cuda_contig("v_cache", v_cache, torch.uint8)
-    g = q4_geom_of(k_cache, k_cache.shape[1])
+    index = k_cache.get_device()
+    nb, hkv, bs, d = _q4_shape(k_cache)
     if v_cache.shape != k_cache.shape:
         raise ValueError("shape mismatch between the pools")
     n = slot_mapping.numel()
-    shape = (n, g.num_kv_heads, g.head_dim)
+    shape = (n, hkv, d)
     if k_out is None:
         k_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
     if v_out is None:
         v_out = torch.empty(shape, dtype=k_out.dtype, device=k_cache.device)
-    _cuda_contig("k_out", k_out)
-    _cuda_contig("v_out", v_out, k_out.dtype)
     if k_out.shape != shape or v_out.shape != shape:
         raise ValueError("k_out / v_out must be [N, Hkv, d]")
-    with torch.cuda.device(k_cache.device):
-        st = load_library().paged_kv_read_q4(
-            _ptr(k_cache), _ptr(v_cache), _ptr(slot_mapping), n, _ptr(k_out), _ptr(v_out),
-            _dtype_code(k_out), ctypes.byref(g), _stream(k_cache))
-    _check("paged_kv_read_q4", st)
+    load_library()
+    _launch("paged_kv_read_q4", index, _arg("k_cache", k_cache, index),
+            _arg("v_cache", v_cache, index, torch.uint8),
+            _arg("slot_mapping", slot_mapping, index, torch.int32), n,
+            _arg("k_out", k_out, index), _arg("v_out", v_out, index, k_out.dtype),
+            _dtype_code(k_out), _geom(hkv, hkv, d, bs, nb, PKV_Q4))
     return k_out, v_out
+
+
+def _decode_q4_size(index: int, batch: int, code: int, *geom) -> int:
+    """paged_decode_q4_workspace_size on device `index`, looked up after the first."""
+    key = (index, batch, code) + geom
+    need = _sizes.get(key)
+    if need is None:
+        if len(_sizes) > 1000:
+            _sizes.clear()
+        with torch.cuda.device(index):
+            need = _sizes[key] = int(load_library().paged_decode_q4_workspace_size(
+                batch, code, _geom(*geom)))
+    return need
 
 
 def paged_decode_q4_workspace_size(batch: int, q_heads: int, q_dtype: torch.dtype,
                                    k_cache: torch.Tensor) -> int:
-    g = q4_geom_of(k_cache, q_heads)
+    nb, hkv, bs, d = _q4_shape(k_cache)
     code = _dtype_code(torch.empty(0, dtype=q_dtype))
-    with torch.cuda.device(k_cache.device):
-        return int(load_library().paged_decode_q4_workspace_size(batch, code, ctypes.byref(g)))
+    return _decode_q4_size(k_cache.get_device(), batch, code, q_heads, hkv, d, bs, nb, PKV_Q4)
 
 
 def paged_decode_q4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -754,34 +811,28 @@ def paged_decode_q4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                     workspace: torch.Tensor | None = None) -> torch.Tensor:
     """One query token per sequence (q [batch, Hq, d], fp32 or bf16) over its
     cache_seqlens[b] keys in 4-bit pools."""
-    _cuda_contig("q", q)
-    _cuda_contig("k_cache", k_cache)
-    _cuda_contig("v_cache", v_cache, torch.uint8)
-    _cuda_contig("block_table", block_table, torch.int32)
-    _cuda_contig("cache_seqlens", cache_seqlens, torch.int32)
+    index = q.get_device()
     batch, hq, d = q.shape
-    g = q4_geom_of(k_cache, hq)
-    if d != g.head_dim or v_cache.shape != k_cache.shape or block_table.shape[0] < batch or \
-            cache_seqlens.numel() < batch:
+    nb, hkv, bs, dk = _q4_shape(k_cache)
+    rows, width = block_table.shape
+    if d != dk or v_cache.shape != k_cache.shape or rows < batch or cache_seqlens.numel() < batch:
         raise ValueError("shape mismatch")
     if out is None:
         out = torch.empty_like(q)
-    _cuda_contig("out", out, q.dtype)
-    if out.shape != q.shape:
+    elif out.shape != q.shape:
         raise ValueError("out must have q's shape")
-    scale = 1.0 / math.sqrt(d) if scale is None else float(scale)
     code = _dtype_code(q)
-    lib = load_library()
-    with torch.cuda.device(q.device):
-        need = int(lib.paged_decode_q4_workspace_size(batch, code, ctypes.byref(g)))
-        if workspace is None and need:
-            workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-        st = lib.paged_decode_q4(_ptr(q), code, _ptr(k_cache), _ptr(v_cache), _ptr(block_table),
-                                 block_table.shape[1], _ptr(cache_seqlens), batch, scale,
-                                 _ptr(out), _ptr(workspace),
-                                 0 if workspace is None else workspace.numel(), ctypes.byref(g),
-                                 _stream(q))
-    _check("paged_decode_q4", st)
+    args = (_arg("q", q, index), code, _arg("k_cache", k_cache, index),
+            _arg("v_cache", v_cache, index, torch.uint8),
+            _arg("block_table", block_table, index, torch.int32), width,
+            _arg("cache_seqlens", cache_seqlens, index, torch.int32), batch,
+            1.0 / math.sqrt(d) if scale is None else scale, _arg("out", out, index, q.dtype))
+    if workspace is None:
+        need = _decode_q4_size(index, batch, code, hq, hkv, d, bs, nb, PKV_Q4)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    load_library()
+    _launch("paged_decode_q4", index, *args, _arg("workspace", workspace, index),
+            workspace.numel() * workspace.element_size(), _geom(hq, hkv, d, bs, nb, PKV_Q4))
     return out
 
 
@@ -792,22 +843,25 @@ def paged_kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: 
     """Keep the positions keep[cu_keep[b]:cu_keep[b + 1]] of every sequence b
     (and those below start[b]), moved together in place from start[b] on; pools
     in fp32, bf16 or 4 bits.  seqlens_out receives the new lengths."""
-    _cuda_contig("k_cache", k_cache)
-    _cuda_contig("v_cache", v_cache, k_cache.dtype)
-    for n, t in (("block_table", block_table), ("keep", keep), ("cu_keep", cu_keep),
-                 ("start", start), ("seqlens_out", seqlens_out)):
-        if t is not None:
-            _cuda_contig(n, t, torch.int32)
+    index = k_cache.get_device()
     batch = cu_keep.numel() - 1
-    if k_cache.shape != v_cache.shape or batch < 0 or block_table.shape[0] < batch or \
+    rows, width = block_table.shape
+    if k_cache.shape != v_cache.shape or batch < 0 or rows < batch or \
             (start is not None and start.numel() < batch) or \
             (seqlens_out is not None and seqlens_out.numel() < batch):
         raise ValueError("shape mismatch")
-    g = q4_geom_of(k_cache, k_cache.shape[1]) if k_cache.dtype == torch.uint8 \
-        else geom_of(k_cache, k_cache.shape[2])
-    with torch.cuda.device(k_cache.device):
-        st = load_library().paged_kv_compact(
-            _ptr(k_cache), _ptr(v_cache), _ptr(block_table), block_table.shape[1], _ptr(start),
-            _ptr(keep), keep.numel(), _ptr(cu_keep), batch, _ptr(seqlens_out), ctypes.byref(g),
-            _stream(k_cache))
-    _check("paged_kv_compact", st)
+    if k_cache.dtype == torch.uint8:
+        nb, hkv, bs, d = _q4_shape(k_cache)
+        code = PKV_Q4
+    else:
+        nb, bs, hkv, d = k_cache.shape
+        code = _dtype_code(k_cache)
+    i32 = torch.int32
+    load_library()
+    _launch("paged_kv_compact", index, _arg("k_cache", k_cache, index),
+            _arg("v_cache", v_cache, index, k_cache.dtype),
+            _arg("block_table", block_table, index, i32), width,
+            None if start is None else _arg("start", start, index, i32),
+            _arg("keep", keep, index, i32), keep.numel(), _arg("cu_keep", cu_keep, index, i32),
+            batch, None if seqlens_out is None else _arg("seqlens_out", seqlens_out, index, i32),
+            _geom(hkv, hkv, d, bs, nb, code))

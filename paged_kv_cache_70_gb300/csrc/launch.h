@@ -253,7 +253,7 @@ struct Q4DecodePlan {
 bool plan_q4_decode(const DeviceInfo& dev, int32_t batch, int32_t max_blocks, int hq, int hkv,
                     int d, int block_size, int q_dtype, Q4DecodePlan* plan);
 
-cudaError_t launch_q4_decode(const Q4DecodePlan& plan, const void* q, const void* k_cache,
+cudaError_t launch_q4_decode(const DeviceInfo& dev, const Q4DecodePlan& plan, const void* q, const void* k_cache,
                              const void* v_cache, const int32_t* table, int32_t max_blocks,
                              const int32_t* seqlens, int32_t batch, float scale, void* out,
                              void* workspace, int hq, int hkv, int d, int block_size,

@@ -100,7 +100,7 @@ int paged_decode_q4(const void* q, int32_t q_dtype, const void* k_cache, const v
         (!workspace || workspace_bytes < plan.ws_bytes || !aligned(workspace, 256)))
         return PKV_ERR_WORKSPACE;
     return cuda_status(pkv::launch_q4_decode(
-        plan, q, k_cache, v_cache, block_table, max_blocks_per_seq, cache_seqlens, batch, scale,
+        dev, plan, q, k_cache, v_cache, block_table, max_blocks_per_seq, cache_seqlens, batch, scale,
         out, workspace, geom->num_heads, geom->num_kv_heads, geom->head_dim, geom->block_size,
         geom->num_blocks, q_dtype, dev.err, stream));
 }

@@ -49,6 +49,7 @@
 #include <cuda_fp16.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "launch.h"
@@ -67,6 +68,7 @@ constexpr int kProducers = 4;
 constexpr int kThreads = (kConsumers + kProducers) * 32;
 constexpr int kMaxStages = 8;
 constexpr int kHeader = 512;  // barriers and stage tags
+constexpr size_t kStaticSmem = 1024;  // left for static shared memory
 
 // 16-key products that a warp runs side by side (its share of a tile)
 template <int QN, bool F32>
@@ -1145,11 +1147,19 @@ __global__ void __launch_bounds__(kCombineMost * 32) q4_combine_kernel(const Q4C
 }
 
 template <int NG, int QN, bool F32>
-cudaError_t launch_split(const Q4DecodePlan& p, const Q4DecodeArgs& a, cudaStream_t stream) {
+cudaError_t launch_split(const DeviceInfo& dev, const Q4DecodePlan& p, const Q4DecodeArgs& a,
+                         cudaStream_t stream) {
     auto kern = q4_split_kernel<NG, QN, F32>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                               (int)p.smem_bytes);
-    if (e != cudaSuccess) return e;
+    // the most shared memory a CTA may have, set once per device
+    static std::atomic<uint64_t> set{0};
+    const uint64_t bit = 1ull << dev.device;
+    if (!(set.load(std::memory_order_relaxed) & bit)) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            (int)(dev.max_smem_optin - kStaticSmem));
+        if (e != cudaSuccess) return e;
+        set.fetch_or(bit, std::memory_order_relaxed);
+    }
     return launch_dependent(kern, dim3(p.ctas, p.head_groups),
                             dim3(kThreads), p.smem_bytes, stream, a);
 }
@@ -1183,7 +1193,7 @@ bool plan_q4_decode(const DeviceInfo& dev, int32_t batch, int32_t max_blocks, in
     const size_t stage = (size_t)2 * p->hc * p->tile * R;
     const size_t fixed = kHeader + up((size_t)(batch + 1) * 4, 128) +
                          (size_t)units * (p->wh - 1) * state_bytes(nt);
-    const size_t room = dev.max_smem_optin - 1024;  // static shared memory, alignment
+    const size_t room = dev.max_smem_optin - kStaticSmem;
     if (room < fixed + 2 * stage) return false;
     p->stages = (int)std::min<size_t>(kMaxStages, (room - fixed) / stage);
     p->smem_bytes = fixed + p->stages * stage;
@@ -1197,7 +1207,7 @@ bool plan_q4_decode(const DeviceInfo& dev, int32_t batch, int32_t max_blocks, in
     return true;
 }
 
-cudaError_t launch_q4_decode(const Q4DecodePlan& p, const void* q, const void* k_cache,
+cudaError_t launch_q4_decode(const DeviceInfo& dev, const Q4DecodePlan& p, const void* q, const void* k_cache,
                              const void* v_cache, const int32_t* table, int32_t max_blocks,
                              const int32_t* seqlens, int32_t batch, float scale, void* out,
                              void* workspace, int hq, int hkv, int d, int block_size,
@@ -1233,7 +1243,7 @@ cudaError_t launch_q4_decode(const Q4DecodePlan& p, const void* q, const void* k
     const bool f32 = q_dtype == PKV_F32;
     cudaError_t e = cudaErrorInvalidValue;
 #define PKV_Q4_CASE(NN, QQ, FF) \
-    if (d == NN * kQ4Group && p.qn == QQ && f32 == FF) e = launch_split<NN, QQ, FF>(p, a, stream);
+    if (d == NN * kQ4Group && p.qn == QQ && f32 == FF) e = launch_split<NN, QQ, FF>(dev, p, a, stream);
     PKV_Q4_CASE(4, 2, false) PKV_Q4_CASE(4, 4, false) PKV_Q4_CASE(4, 8, false)
     PKV_Q4_CASE(4, 2, true) PKV_Q4_CASE(4, 4, true) PKV_Q4_CASE(4, 8, true)
     PKV_Q4_CASE(2, 2, false) PKV_Q4_CASE(2, 4, false) PKV_Q4_CASE(2, 8, false)
