@@ -12,23 +12,31 @@
 // only need the order "a round's loads before its stores", and bytes of different
 // columns of a row need no order at all: the rows are cut into column slices
 // and one CTA walks one sequence's tokens for one slice of one pool, in rounds.
-// Within a round all loads come before a barrier and all stores after it; the
-// next round's loads are issued before this round's stores, so that they are
-// in flight together.  No flags, no waits between CTAs, and the result does
-// not depend on the order in which they run.
+// No flags, no waits between CTAs, and the result does not depend on the order in
+// which they run.
+//
 // HBM-bound: each moved row is read and written once; rows that stay where they
-// are (p_i = start + i) are neither read nor written.
+// are (p_i = start + i) are neither read nor written.  A round is a chain of four
+// memory latencies (list entry, table entry, row, store), so a CTA keeps five
+// rounds of rows in flight (cp.async into shared memory, each thread its own
+// vectors), the list two rounds further ahead and the table entries one: 85 KB of
+// loads per CTA, two CTAs per SM.
 #include <algorithm>
+#include <atomic>
 
 #include "common.cuh"
 #include "launch.h"
+#include "q4.cuh"
 
 namespace pkv {
 
 namespace {
 
-constexpr int kCompactThreads = 256;
-constexpr int kCompactUnroll = 4;  // rows in flight per thread and round
+constexpr int kCompactThreads = 512;
+constexpr int kCompactUnroll = 2;  // rows of a round per thread
+constexpr int kDepth = 5;          // rounds in flight
+constexpr int kIndexRing = kDepth + 2;
+constexpr int kMaxTokens = 128;    // tokens per round, at most
 
 struct CompactArgs {
     unsigned char* pool[2];
@@ -40,97 +48,173 @@ struct CompactArgs {
     unsigned int* err;
     int64_t page_bytes, token_bytes, head_bytes;  // strides of page, token, head
     int64_t num_blocks;
-    int32_t max_blocks, block_size, total;
+    FastDiv block;          // by the page size
+    int32_t max_blocks, total;
     int32_t vec_per_head;   // vectors that lie together; a token's row has `vecs` of them
     int32_t vecs;
     int32_t slice;          // vectors per slice
+    int32_t tokens;         // side by side: threads / slice
 };
 
-// one kept token of a round: byte offsets in the pool, -1 when nothing moves
+// one kept token: byte offsets in the pool, -1 when nothing moves
 struct Move {
     int64_t src, dst;
 };
 
-__device__ __forceinline__ Move find_move(const CompactArgs& a, const int32_t* row,
-                                          const int32_t* list, int32_t i, int32_t n,
-                                          int32_t start, bool report) {
-    Move m{-1, -1};
-    if (i >= n) return m;
-    const int32_t p = list[i], to = start + i;
-    if (p == to) return m;  // stays
-    if (p < to || p >= (int64_t)a.max_blocks * a.block_size) {
-        if (report) flag_error(a.err, PKV_FLAG_BAD_LENGTH);
-        return m;
+template <typename Vec>
+__device__ __forceinline__ void copy_async(Vec* dst, const void* src) {
+    if constexpr (sizeof(Vec) == 16) {
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src)
+                     : "memory");
+    } else if constexpr (sizeof(Vec) >= 4) {
+        asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src),
+                     "n"(sizeof(Vec) >= 4 ? sizeof(Vec) : 4)
+                     : "memory");
+    } else {
+        *dst = __ldcg(static_cast<const Vec*>(src));  // (no such copy of 2 bytes)
     }
-    const int32_t sp = p / a.block_size, dp = to / a.block_size;
-    const int32_t sb = row[sp], db = row[dp];
-    if (sb < 0 || sb >= a.num_blocks || db < 0 || db >= a.num_blocks) {
-        if (report) flag_error(a.err, PKV_FLAG_BAD_BLOCK);
-        return m;
-    }
-    m.src = sb * a.page_bytes + (p - sp * a.block_size) * a.token_bytes;
-    m.dst = db * a.page_bytes + (to - dp * a.block_size) * a.token_bytes;
-    return m;
+}
+
+constexpr size_t compact_smem() {
+    return (size_t)kDepth * kCompactUnroll * kCompactThreads * 16 +
+           (size_t)kIndexRing * kMaxTokens * sizeof(Move);
 }
 
 // grid (slices, batch, 2 pools)
 template <typename Vec>
-__global__ void __launch_bounds__(kCompactThreads) compact_kernel(const CompactArgs a) {
+__global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(const CompactArgs a) {
     PKV_DEPENDENT_PROLOGUE();
-    const int b = blockIdx.y;
+    extern __shared__ __align__(16) unsigned char smem[];
+    const int tid = threadIdx.x, b = blockIdx.y;
     const int32_t c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
     int32_t start = a.start ? __ldg(a.start + b) : 0;
-    const bool first = blockIdx.x == 0 && blockIdx.z == 0;
+    const bool report = blockIdx.x == 0 && blockIdx.z == 0;
+    const int32_t cap = a.max_blocks * (int32_t)a.block.d;
     int32_t n = c1 - c0;
-    if (c0 < 0 || c1 < c0 || c1 > a.total || start < 0 ||
-        (int64_t)start + n > (int64_t)a.max_blocks * a.block_size) {
-        if (first && threadIdx.x == 0) flag_error(a.err, PKV_FLAG_BAD_LENGTH);
-        start = min(max(start, 0), a.max_blocks * a.block_size);
+    if (c0 < 0 || c1 < c0 || c1 > a.total || start < 0 || (int64_t)start + n > cap) {
+        if (report && tid == 0) flag_error(a.err, PKV_FLAG_BAD_LENGTH);
+        start = min(max(start, 0), cap);
         n = 0;
     }
-    if (first && threadIdx.x == 0 && a.seqlens_out) a.seqlens_out[b] = start + n;
+    if (report && tid == 0 && a.seqlens_out) a.seqlens_out[b] = start + n;
     if (n == 0) return;
     const int32_t* list = a.keep + c0;
     const int32_t* row = a.table + (int64_t)b * a.max_blocks;
     unsigned char* pool = a.pool[blockIdx.z];
+    Vec* ring = reinterpret_cast<Vec*>(smem);  // [round][u][thread]
+    Move* moves = reinterpret_cast<Move*>(smem + (size_t)kDepth * kCompactUnroll * kCompactThreads * 16);
     // this thread's column of the slice and its first token of a round
-    const int tokens = kCompactThreads / a.slice;  // tokens side by side
-    const int tok = threadIdx.x / a.slice;
-    const int32_t col = blockIdx.x * a.slice + threadIdx.x % a.slice;
-    const bool live = tok < tokens && col < a.vecs;
+    const int tok = tid / a.slice;
+    const int32_t col = blockIdx.x * a.slice + tid % a.slice;
+    const bool live = tok < a.tokens && col < a.vecs;
     const int64_t off = live ? (int64_t)(col / a.vec_per_head) * a.head_bytes +
                                    (int64_t)(col % a.vec_per_head) * sizeof(Vec)
                              : 0;
-    const int32_t step = tokens * kCompactUnroll;
-    int64_t dst[kCompactUnroll], dst_next[kCompactUnroll];
-    Vec x[kCompactUnroll], x_next[kCompactUnroll];
-    auto load = [&](int32_t i0, int64_t* d, Vec* v) {
-#pragma unroll
-        for (int u = 0; u < kCompactUnroll; ++u) {
-            d[u] = -1;
-            if (!live) continue;
-            const Move m = find_move(a, row, list, i0 + u * tokens + tok, n, start, first);
-            if (m.src < 0) continue;
-            d[u] = m.dst + off;
-            v[u] = __ldcg(reinterpret_cast<const Vec*>(pool + m.src + off));
+    const int step = a.tokens * kCompactUnroll;  // tokens per round
+    const int rounds = (n + step - 1) / step;
+    const bool indexer = tid < step;  // looks up token tid of each round
+
+    // Three steps of a token's lookup, in rounds of their own: the list entry (-1:
+    // nothing moves), the two table entries, the offsets.
+    auto entry = [&](int r) {
+        const int64_t i = (int64_t)r * step + tid;
+        if (!indexer || i >= n) return -1;
+        const int32_t p = __ldg(list + i), to = start + (int32_t)i;
+        if (p == to) return -1;  // stays
+        if (p < to || p >= cap) {
+            if (report) flag_error(a.err, PKV_FLAG_BAD_LENGTH);
+            return -1;
         }
+        return p;
     };
-    load(0, dst, x);
-    for (int32_t i0 = 0; i0 < n; i0 += step) {
-        __syncthreads();  // every thread has read its rows of this round
-        load(i0 + step, dst_next, x_next);
-#pragma unroll
-        for (int u = 0; u < kCompactUnroll; ++u) {
-            if (dst[u] >= 0) *reinterpret_cast<Vec*>(pool + dst[u]) = x[u];
-            dst[u] = dst_next[u];
-            x[u] = x_next[u];
+    struct Pages {
+        int32_t src, dst;
+    };
+    auto pages = [&](int r, int32_t p) {
+        Pages g{-1, -1};
+        if (p < 0) return g;
+        const int32_t to = start + r * step + tid;
+        g.src = __ldg(row + a.block.quot((uint32_t)p));
+        g.dst = __ldg(row + a.block.quot((uint32_t)to));
+        return g;
+    };
+    auto offsets = [&](int r, int32_t p, const Pages& g) {
+        if (!indexer) return;
+        Move m{-1, -1};
+        if (p >= 0) {
+            const int32_t to = start + r * step + tid, B = (int32_t)a.block.d;
+            if (g.src < 0 || g.src >= a.num_blocks || g.dst < 0 || g.dst >= a.num_blocks) {
+                if (report) flag_error(a.err, PKV_FLAG_BAD_BLOCK);
+            } else {
+                const int32_t sp = (int32_t)a.block.quot((uint32_t)p), dp = (int32_t)a.block.quot((uint32_t)to);
+                m.src = g.src * a.page_bytes + (int64_t)(p - sp * B) * a.token_bytes;
+                m.dst = g.dst * a.page_bytes + (int64_t)(to - dp * B) * a.token_bytes;
+            }
         }
+        moves[r % kIndexRing * kMaxTokens + tid] = m;
+    };
+    auto load = [&](int r) {  // (a group is closed for every round, also past the last)
+        if (live && r < rounds) {
+#pragma unroll
+            for (int u = 0; u < kCompactUnroll; ++u) {
+                const int64_t src = moves[r % kIndexRing * kMaxTokens + u * a.tokens + tok].src;
+                if (src >= 0)
+                    copy_async(&ring[(r % kDepth * kCompactUnroll + u) * kCompactThreads + tid],
+                               pool + src + off);
+            }
+        }
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+
+    int32_t p[kDepth + 2];
+    Pages g[kDepth + 1];
+#pragma unroll
+    for (int r = 0; r < kDepth + 2; ++r) p[r] = entry(r);
+#pragma unroll
+    for (int r = 0; r < kDepth + 1; ++r) g[r] = pages(r, p[r]);
+#pragma unroll
+    for (int r = 0; r < kDepth; ++r) offsets(r, p[r], g[r]);
+    int32_t p1 = p[kDepth], p2 = p[kDepth + 1];  // of rounds r + kDepth, + 1
+    Pages g1 = g[kDepth];                        // of round r + kDepth
+    __syncthreads();
+#pragma unroll
+    for (int r = 0; r < kDepth; ++r) load(r);
+    for (int r = 0; r < rounds; ++r) {
+        offsets(r + kDepth, p1, g1);
+        p1 = p2;
+        g1 = pages(r + kDepth + 1, p1);
+        p2 = entry(r + kDepth + 2);
+        asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
+        __syncthreads();  // every thread has read its rows of this round
+        if (live) {
+#pragma unroll
+            for (int u = 0; u < kCompactUnroll; ++u) {
+                const int64_t dst = moves[r % kIndexRing * kMaxTokens + u * a.tokens + tok].dst;
+                if (dst >= 0)
+                    *reinterpret_cast<Vec*>(pool + dst + off) =
+                        ring[(r % kDepth * kCompactUnroll + u) * kCompactThreads + tid];
+            }
+        }
+        load(r + kDepth);
     }
+}
+
+template <typename Vec>
+cudaError_t launch_typed(int device, dim3 grid, const CompactArgs& a, cudaStream_t stream) {
+    auto kern = compact_kernel<Vec>;
+    static std::atomic<uint64_t> set{0};
+    if (!(set.load(std::memory_order_relaxed) & (1ull << device))) {
+        const cudaError_t e = cudaFuncSetAttribute(
+            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)compact_smem());
+        if (e != cudaSuccess) return e;
+        set.fetch_or(1ull << device, std::memory_order_relaxed);
+    }
+    return launch_dependent(kern, grid, dim3(kCompactThreads), compact_smem(), stream, a);
 }
 
 }  // namespace
 
-cudaError_t launch_compact(const CompactLaunch& c, unsigned int* err, cudaStream_t stream) {
+cudaError_t launch_compact(const DeviceInfo& dev, const CompactLaunch& c, cudaStream_t stream) {
     CompactArgs a{};
     a.pool[0] = static_cast<unsigned char*>(c.k_cache);
     a.pool[1] = static_cast<unsigned char*>(c.v_cache);
@@ -139,13 +223,13 @@ cudaError_t launch_compact(const CompactLaunch& c, unsigned int* err, cudaStream
     a.keep = c.keep;
     a.cu = c.cu_keep;
     a.seqlens_out = c.seqlens_out;
-    a.err = err;
+    a.err = dev.err;
     a.page_bytes = c.page_bytes;
     a.token_bytes = c.token_bytes;
     a.head_bytes = c.head_bytes;
     a.num_blocks = c.num_blocks;
+    a.block = FastDiv((uint32_t)c.block_size);
     a.max_blocks = c.max_blocks;
-    a.block_size = c.block_size;
     a.total = c.total;
     // the widest vector that divides the pieces and the pools' alignment
     int vec = 16;
@@ -153,13 +237,19 @@ cudaError_t launch_compact(const CompactLaunch& c, unsigned int* err, cudaStream
         vec /= 2;
     a.vec_per_head = (int32_t)(c.piece_bytes / vec);
     a.vecs = (int32_t)(a.vec_per_head * c.pieces);
-    a.slice = std::min(a.vecs, 4);
+    // Short lists (a draft's accepted tokens) take whole rows, so that a round is not
+    // larger than the list; long ones slices of 8 vectors, a round of 128 tokens.
+    const int64_t mean = (c.total + c.batch - 1) / c.batch;
+    const int want = (int)std::min<int64_t>(kMaxTokens, std::max<int64_t>(mean, 8));
+    a.slice = std::min(a.vecs, kCompactThreads * kCompactUnroll / want);
+    a.slice = std::max(a.slice, kCompactThreads * kCompactUnroll / kMaxTokens);
+    a.slice = std::min(a.slice, kCompactThreads);
+    a.tokens = std::min(kCompactThreads / a.slice, kMaxTokens / kCompactUnroll);
     const dim3 grid((unsigned)((a.vecs + a.slice - 1) / a.slice), (unsigned)c.batch, 2);
-    auto kern = vec == 16 ? compact_kernel<uint4>
-                          : (vec == 8 ? compact_kernel<uint2>
-                                      : (vec == 4 ? compact_kernel<uint32_t>
-                                                  : compact_kernel<uint16_t>));
-    return launch_dependent(kern, grid, dim3(kCompactThreads), 0, stream, a);
+    if (vec == 16) return launch_typed<uint4>(dev.device, grid, a, stream);
+    if (vec == 8) return launch_typed<uint2>(dev.device, grid, a, stream);
+    if (vec == 4) return launch_typed<uint32_t>(dev.device, grid, a, stream);
+    return launch_typed<uint16_t>(dev.device, grid, a, stream);
 }
 
 }  // namespace pkv

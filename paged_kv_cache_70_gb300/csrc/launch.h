@@ -275,6 +275,6 @@ struct CompactLaunch {
     int64_t num_blocks;
     int32_t max_blocks, block_size, batch, total;
 };
-cudaError_t launch_compact(const CompactLaunch& c, unsigned int* err, cudaStream_t stream);
+cudaError_t launch_compact(const DeviceInfo& dev, const CompactLaunch& c, cudaStream_t stream);
 
 }  // namespace pkv

@@ -150,7 +150,7 @@ int paged_kv_compact(void* k_cache, void* v_cache, const int32_t* block_table,
     }
     c.page_bytes = c.pieces * c.piece_bytes * geom->block_size;
     if (c.pieces * c.piece_bytes > (1 << 24)) return PKV_ERR_UNSUPPORTED;
-    return cuda_status(pkv::launch_compact(c, dev.err, stream));
+    return cuda_status(pkv::launch_compact(dev, c, stream));
 }
 
 }  // extern "C"

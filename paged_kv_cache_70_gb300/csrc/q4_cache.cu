@@ -113,6 +113,16 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(a), "f"(b));
     return y;
 }
+__device__ __forceinline__ float min_nan(float a, float b, float c) {
+    float y;
+    asm("min.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
+__device__ __forceinline__ float max_nan(float a, float b, float c) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(y) : "f"(a), "f"(b), "f"(c));
+    return y;
+}
 
 template <int NG, bool F32>
 __global__ void __launch_bounds__(kQ4Warps * 32)
@@ -154,10 +164,12 @@ q4_write_kernel(const void* __restrict__ k, const void* __restrict__ v, const Q4
             widen8<F32>(raw[u], x);
             float lo = x[0], hi = x[0];
 #pragma unroll
-            for (int i = 1; i < 8; ++i) {
-                lo = min_nan(lo, x[i]);
-                hi = max_nan(hi, x[i]);
+            for (int i = 1; i < 7; i += 2) {
+                lo = min_nan(lo, x[i], x[i + 1]);
+                hi = max_nan(hi, x[i], x[i + 1]);
             }
+            lo = min_nan(lo, x[7]);
+            hi = max_nan(hi, x[7]);
 #pragma unroll
             for (int off = 1; off < 4; off <<= 1) {
                 lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
@@ -174,11 +186,15 @@ q4_write_kernel(const void* __restrict__ k, const void* __restrict__ v, const Q4
                 __fadd_rn(__fadd_rn(0.5f * lo, 0.5f * hi), 0.5f * s));
             const float z = __uint_as_float(zb << 16);
             const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-            uint32_t w = 0;
+            // rint and the conversion by an addition: 2^23 + 2^22 + 8 + t rounds t to
+            // a whole number, ties to even, and leaves code t + 8 in the low bits.
+            // Clamped first (a NaN becomes -8: code 0), which rounding does not
+            // change.  The bits above the codes add up to a constant.
+            uint32_t w = 0u - 0x4B400000u * 0x11111111u;
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
-                const float t = rintf(__fmul_rn(__fsub_rn(x[i], z), inv)) + 8.f;
-                w |= (uint32_t)fminf(fmaxf(t, 0.f), 15.f) << (4 * i);
+                const float t = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], z), inv), -8.f), 7.f);
+                w += __float_as_uint(__fadd_rn(t, 12582920.f)) << (4 * i);
             }
             w = units_to_words<NG>(w, lane, g);
             if (vec < vecs) {
