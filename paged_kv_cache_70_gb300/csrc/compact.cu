@@ -32,11 +32,17 @@ namespace pkv {
 
 namespace {
 
-constexpr int kCompactThreads = 512;
 constexpr int kCompactUnroll = 2;  // rows of a round per thread
-constexpr int kDepth = 5;          // rounds in flight
-constexpr int kIndexRing = kDepth + 2;
-constexpr int kMaxTokens = 128;    // tokens per round, at most
+// A CTA's shape: threads, rounds in flight, tokens per round at most.  Short lists
+// are one round, and many small CTAs start sooner.
+struct LongLists {
+    static constexpr int kThreads = 512, kDepth = 5, kTokens = 128, kCtas = 2;
+};
+struct ShortLists {
+    static constexpr int kThreads = 128, kDepth = 1, kTokens = 32, kCtas = 8;
+};
+constexpr int32_t kNone = -0x7fffffff - 1;
+constexpr int kAhead = 1;          // rounds between the steps of a lookup
 
 struct CompactArgs {
     unsigned char* pool[2];
@@ -75,15 +81,22 @@ __device__ __forceinline__ void copy_async(Vec* dst, const void* src) {
     }
 }
 
+// row ring, then lookup ring
+template <typename Shape>
+constexpr size_t ring_bytes() {
+    return (size_t)Shape::kDepth * kCompactUnroll * Shape::kThreads * 16;
+}
+template <typename Shape>
 constexpr size_t compact_smem() {
-    return (size_t)kDepth * kCompactUnroll * kCompactThreads * 16 +
-           (size_t)kIndexRing * kMaxTokens * sizeof(Move);
+    return ring_bytes<Shape>() + (size_t)(Shape::kDepth + 2) * Shape::kTokens * sizeof(Move);
 }
 
 // grid (slices, batch, 2 pools)
-template <typename Vec>
-__global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(const CompactArgs a) {
+template <typename Vec, typename Shape>
+__global__ void __launch_bounds__(Shape::kThreads, Shape::kCtas) compact_kernel(const CompactArgs a) {
     PKV_DEPENDENT_PROLOGUE();
+    constexpr int kDepth = Shape::kDepth, kThreads = Shape::kThreads, kTokens = Shape::kTokens;
+    constexpr int kIndexRing = kDepth + 2;
     extern __shared__ __align__(16) unsigned char smem[];
     const int tid = threadIdx.x, b = blockIdx.y;
     const int32_t c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
@@ -102,7 +115,7 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(const Compa
     const int32_t* row = a.table + (int64_t)b * a.max_blocks;
     unsigned char* pool = a.pool[blockIdx.z];
     Vec* ring = reinterpret_cast<Vec*>(smem);  // [round][u][thread]
-    Move* moves = reinterpret_cast<Move*>(smem + (size_t)kDepth * kCompactUnroll * kCompactThreads * 16);
+    Move* moves = reinterpret_cast<Move*>(smem + ring_bytes<Shape>());
     // this thread's column of the slice and its first token of a round
     const int tok = tid / a.slice;
     const int32_t col = blockIdx.x * a.slice + tid % a.slice;
@@ -114,26 +127,25 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(const Compa
     const int rounds = (n + step - 1) / step;
     const bool indexer = tid < step;  // looks up token tid of each round
 
-    // Three steps of a token's lookup, in rounds of their own: the list entry (-1:
-    // nothing moves), the two table entries, the offsets.
+    // Three steps of a token's lookup, in rounds of their own so that each load has
+    // time to arrive: the list entry, the two table entries, the offsets.
     auto entry = [&](int r) {
         const int64_t i = (int64_t)r * step + tid;
-        if (!indexer || i >= n) return -1;
-        const int32_t p = __ldg(list + i), to = start + (int32_t)i;
-        if (p == to) return -1;  // stays
-        if (p < to || p >= cap) {
-            if (report) flag_error(a.err, PKV_FLAG_BAD_LENGTH);
-            return -1;
-        }
-        return p;
+        return indexer && i < n ? __ldg(list + i) : kNone;
     };
     struct Pages {
         int32_t src, dst;
     };
-    auto pages = [&](int r, int32_t p) {
+    auto pages = [&](int r, int32_t& p) {  // p: kNone where nothing moves
         Pages g{-1, -1};
-        if (p < 0) return g;
         const int32_t to = start + r * step + tid;
+        if (p == to) p = kNone;  // stays
+        if (p == kNone) return g;
+        if (p < to || p >= cap) {
+            if (report) flag_error(a.err, PKV_FLAG_BAD_LENGTH);
+            p = kNone;
+            return g;
+        }
         g.src = __ldg(row + a.block.quot((uint32_t)p));
         g.dst = __ldg(row + a.block.quot((uint32_t)to));
         return g;
@@ -141,7 +153,7 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(const Compa
     auto offsets = [&](int r, int32_t p, const Pages& g) {
         if (!indexer) return;
         Move m{-1, -1};
-        if (p >= 0) {
+        if (p != kNone) {
             const int32_t to = start + r * step + tid, B = (int32_t)a.block.d;
             if (g.src < 0 || g.src >= a.num_blocks || g.dst < 0 || g.dst >= a.num_blocks) {
                 if (report) flag_error(a.err, PKV_FLAG_BAD_BLOCK);
@@ -151,65 +163,92 @@ __global__ void __launch_bounds__(kCompactThreads, 2) compact_kernel(const Compa
                 m.dst = g.dst * a.page_bytes + (int64_t)(to - dp * B) * a.token_bytes;
             }
         }
-        moves[r % kIndexRing * kMaxTokens + tid] = m;
+        moves[r % kIndexRing * kTokens + tid] = m;
     };
     auto load = [&](int r) {  // (a group is closed for every round, also past the last)
         if (live && r < rounds) {
 #pragma unroll
             for (int u = 0; u < kCompactUnroll; ++u) {
-                const int64_t src = moves[r % kIndexRing * kMaxTokens + u * a.tokens + tok].src;
+                const int64_t src = moves[r % kIndexRing * kTokens + u * a.tokens + tok].src;
                 if (src >= 0)
-                    copy_async(&ring[(r % kDepth * kCompactUnroll + u) * kCompactThreads + tid],
+                    copy_async(&ring[(r % kDepth * kCompactUnroll + u) * kThreads + tid],
                                pool + src + off);
             }
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
 
-    int32_t p[kDepth + 2];
-    Pages g[kDepth + 1];
+    // rounds ahead of the row loads: a table entry is looked up kAhead rounds
+    // before its offsets are formed, a list entry kAhead before that
+    int32_t p[kDepth + 2 * kAhead];
+    Pages g[kDepth + kAhead];
 #pragma unroll
-    for (int r = 0; r < kDepth + 2; ++r) p[r] = entry(r);
+    for (int r = 0; r < kDepth + 2 * kAhead; ++r) p[r] = entry(r);
 #pragma unroll
-    for (int r = 0; r < kDepth + 1; ++r) g[r] = pages(r, p[r]);
+    for (int r = 0; r < kDepth + kAhead; ++r) g[r] = pages(r, p[r]);
 #pragma unroll
     for (int r = 0; r < kDepth; ++r) offsets(r, p[r], g[r]);
-    int32_t p1 = p[kDepth], p2 = p[kDepth + 1];  // of rounds r + kDepth, + 1
-    Pages g1 = g[kDepth];                        // of round r + kDepth
+    int32_t pn[2 * kAhead];  // list entries of rounds r + kDepth ..
+    Pages gn[kAhead];        // table entries of rounds r + kDepth ..
+#pragma unroll
+    for (int i = 0; i < 2 * kAhead; ++i) pn[i] = p[kDepth + i];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) gn[i] = g[kDepth + i];
     __syncthreads();
 #pragma unroll
     for (int r = 0; r < kDepth; ++r) load(r);
     for (int r = 0; r < rounds; ++r) {
-        offsets(r + kDepth, p1, g1);
-        p1 = p2;
-        g1 = pages(r + kDepth + 1, p1);
-        p2 = entry(r + kDepth + 2);
+        offsets(r + kDepth, pn[0], gn[0]);
+#pragma unroll
+        for (int i = 0; i + 1 < kAhead; ++i) gn[i] = gn[i + 1];
+        gn[kAhead - 1] = pages(r + kDepth + kAhead, pn[kAhead]);
+#pragma unroll
+        for (int i = 0; i + 1 < 2 * kAhead; ++i) pn[i] = pn[i + 1];
+        pn[2 * kAhead - 1] = entry(r + kDepth + 2 * kAhead);
         asm volatile("cp.async.wait_group %0;" ::"n"(kDepth - 1) : "memory");
         __syncthreads();  // every thread has read its rows of this round
         if (live) {
 #pragma unroll
             for (int u = 0; u < kCompactUnroll; ++u) {
-                const int64_t dst = moves[r % kIndexRing * kMaxTokens + u * a.tokens + tok].dst;
+                const int64_t dst = moves[r % kIndexRing * kTokens + u * a.tokens + tok].dst;
                 if (dst >= 0)
                     *reinterpret_cast<Vec*>(pool + dst + off) =
-                        ring[(r % kDepth * kCompactUnroll + u) * kCompactThreads + tid];
+                        ring[(r % kDepth * kCompactUnroll + u) * kThreads + tid];
             }
         }
         load(r + kDepth);
     }
 }
 
-template <typename Vec>
-cudaError_t launch_typed(int device, dim3 grid, const CompactArgs& a, cudaStream_t stream) {
-    auto kern = compact_kernel<Vec>;
-    static std::atomic<uint64_t> set{0};
+template <typename Vec, typename Shape>
+cudaError_t launch_shaped(int device, int64_t mean, int32_t batch, CompactArgs& a,
+                          cudaStream_t stream) {
+    // a slice as wide as lets a round hold the mean list, up to kTokens
+    constexpr int kRow = Shape::kThreads * kCompactUnroll;
+    const int want = (int)std::min<int64_t>(Shape::kTokens, std::max<int64_t>(mean, 8));
+    a.slice = std::max(std::min(a.vecs, kRow / want), kRow / Shape::kTokens);
+    a.tokens = std::min(Shape::kThreads / a.slice, Shape::kTokens / kCompactUnroll);
+    const dim3 grid((unsigned)((a.vecs + a.slice - 1) / a.slice), (unsigned)batch, 2);
+    auto kern = compact_kernel<Vec, Shape>;
+    static std::atomic<uint64_t> set{0};  // the shared memory limit, once per device
     if (!(set.load(std::memory_order_relaxed) & (1ull << device))) {
-        const cudaError_t e = cudaFuncSetAttribute(
-            kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)compact_smem());
+        const cudaError_t e =
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 (int)compact_smem<Shape>());
         if (e != cudaSuccess) return e;
         set.fetch_or(1ull << device, std::memory_order_relaxed);
     }
-    return launch_dependent(kern, grid, dim3(kCompactThreads), compact_smem(), stream, a);
+    return launch_dependent(kern, grid, dim3(Shape::kThreads), compact_smem<Shape>(), stream, a);
+}
+// Lists of up to 32 tokens on average take the small CTAs: the accepted tokens of
+// 64 drafts take 3.5 us (bf16) against 3.8; half of long contexts 187 us with the
+// large ones, 246 with half their size.
+template <typename Vec>
+cudaError_t launch_typed(int device, int64_t mean, int32_t batch, CompactArgs& a,
+                         cudaStream_t stream) {
+    return mean <= ShortLists::kTokens
+               ? launch_shaped<Vec, ShortLists>(device, mean, batch, a, stream)
+               : launch_shaped<Vec, LongLists>(device, mean, batch, a, stream);
 }
 
 }  // namespace
@@ -237,19 +276,11 @@ cudaError_t launch_compact(const DeviceInfo& dev, const CompactLaunch& c, cudaSt
         vec /= 2;
     a.vec_per_head = (int32_t)(c.piece_bytes / vec);
     a.vecs = (int32_t)(a.vec_per_head * c.pieces);
-    // Short lists (a draft's accepted tokens) take whole rows, so that a round is not
-    // larger than the list; long ones slices of 8 vectors, a round of 128 tokens.
     const int64_t mean = (c.total + c.batch - 1) / c.batch;
-    const int want = (int)std::min<int64_t>(kMaxTokens, std::max<int64_t>(mean, 8));
-    a.slice = std::min(a.vecs, kCompactThreads * kCompactUnroll / want);
-    a.slice = std::max(a.slice, kCompactThreads * kCompactUnroll / kMaxTokens);
-    a.slice = std::min(a.slice, kCompactThreads);
-    a.tokens = std::min(kCompactThreads / a.slice, kMaxTokens / kCompactUnroll);
-    const dim3 grid((unsigned)((a.vecs + a.slice - 1) / a.slice), (unsigned)c.batch, 2);
-    if (vec == 16) return launch_typed<uint4>(dev.device, grid, a, stream);
-    if (vec == 8) return launch_typed<uint2>(dev.device, grid, a, stream);
-    if (vec == 4) return launch_typed<uint32_t>(dev.device, grid, a, stream);
-    return launch_typed<uint16_t>(dev.device, grid, a, stream);
+    if (vec == 16) return launch_typed<uint4>(dev.device, mean, c.batch, a, stream);
+    if (vec == 8) return launch_typed<uint2>(dev.device, mean, c.batch, a, stream);
+    if (vec == 4) return launch_typed<uint32_t>(dev.device, mean, c.batch, a, stream);
+    return launch_typed<uint16_t>(dev.device, mean, c.batch, a, stream);
 }
 
 }  // namespace pkv

@@ -124,6 +124,17 @@ __device__ __forceinline__ float max_nan(float a, float b, float c) {
     return y;
 }
 
+// x / 15 rounded to nearest, x >= 0: from a quotient that is off by an ulp at most,
+// one step with the exact remainder and the rounded reciprocal gives the rounded
+// quotient (Markstein, "Computation of elementary functions on the IBM RISC
+// System/6000 processor", 1990, theorem on division).  An infinity stays.
+__device__ __forceinline__ float div15(float x) {
+    constexpr float kInv = 1.f / 15.f;
+    const float q = __fmul_rn(x, kInv);
+    const float y = __fmaf_rn(__fmaf_rn(-15.f, q, x), kInv, q);
+    return q == INFINITY ? q : y;
+}
+
 template <int NG, bool F32>
 __global__ void __launch_bounds__(kQ4Warps * 32)
 q4_write_kernel(const void* __restrict__ k, const void* __restrict__ v, const Q4Rows a,
@@ -137,7 +148,19 @@ q4_write_kernel(const void* __restrict__ k, const void* __restrict__ v, const Q4
     unsigned char* pool = blockIdx.y ? vc : kc;
     const int vecs = a.hkv * (D / 8);  // lanes' worth of dims in a token's row
     const int64_t e0 = n * a.hkv * D;
+    Raw8<F32> raw[kQ4Unroll];
+    auto load = [&](int v0) {
+#pragma unroll
+        for (int u = 0; u < kQ4Unroll; ++u) {
+            const int vec = v0 + 32 * u + lane;
+            raw[u].a = make_uint4(0, 0, 0, 0);
+            raw[u].b = make_uint4(0, 0, 0, 0);
+            if (vec < vecs) load8<F32>(src, e0 + (int64_t)vec * 8, raw[u]);
+        }
+    };
+    // the row before its slot is known (a row that is not written wastes the load)
     const int32_t slot = __ldg(a.slots + n);
+    load(0);
     if (slot < 0) return;
     if (slot >= a.num_slots) {
         if (lane == 0) flag_error(a.err, PKV_FLAG_BAD_SLOT);
@@ -146,14 +169,7 @@ q4_write_kernel(const void* __restrict__ k, const void* __restrict__ v, const Q4
     const int32_t page = (int32_t)a.block.quot((uint32_t)slot);
     const int32_t at = slot - page * (int32_t)a.block.d;
     for (int v0 = 0; v0 < vecs; v0 += 32 * kQ4Unroll) {
-        Raw8<F32> raw[kQ4Unroll];
-#pragma unroll
-        for (int u = 0; u < kQ4Unroll; ++u) {
-            const int vec = v0 + 32 * u + lane;
-            raw[u].a = make_uint4(0, 0, 0, 0);
-            raw[u].b = make_uint4(0, 0, 0, 0);
-            if (vec < vecs) load8<F32>(src, e0 + (int64_t)vec * 8, raw[u]);
-        }
+        if (v0 > 0) load(v0);
 #pragma unroll
         for (int u = 0; u < kQ4Unroll; ++u) {
             const int vec = v0 + 32 * u + lane;
@@ -176,7 +192,7 @@ q4_write_kernel(const void* __restrict__ k, const void* __restrict__ v, const Q4
                 hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
             }
             // one rounding per operation (no contraction): the codes are the format's
-            uint32_t sb = f32_to_bf16_bits(__fdiv_rn(__fsub_rn(hi, lo), 15.f));
+            uint32_t sb = f32_to_bf16_bits(div15(__fsub_rn(hi, lo)));
             float s = __uint_as_float(sb << 16);
             if (s < 1.17549435e-38f) {  // 2^-126; a NaN stays
                 s = 0.f;
