@@ -29,7 +29,6 @@ namespace pkv {
 namespace {
 
 constexpr int kQ4Warps = 4;   // tokens per CTA
-constexpr int kQ4Unroll = 4;  // 32-lane steps of a row in flight per warp
 
 struct Q4Rows {
     const int32_t* slots;
@@ -90,15 +89,17 @@ __device__ __forceinline__ void load8(const void* base, int64_t elem, Raw8<F32>&
 }
 
 template <bool F32>
-__device__ __forceinline__ void widen8(const Raw8<F32>& r, float* x) {
+__device__ __forceinline__ void widen8(const Raw8<F32>& r, float2* x) {
     if constexpr (F32) {
-        x[0] = __uint_as_float(r.a.x); x[1] = __uint_as_float(r.a.y);
-        x[2] = __uint_as_float(r.a.z); x[3] = __uint_as_float(r.a.w);
-        x[4] = __uint_as_float(r.b.x); x[5] = __uint_as_float(r.b.y);
-        x[6] = __uint_as_float(r.b.z); x[7] = __uint_as_float(r.b.w);
+        x[0] = make_float2(__uint_as_float(r.a.x), __uint_as_float(r.a.y));
+        x[1] = make_float2(__uint_as_float(r.a.z), __uint_as_float(r.a.w));
+        x[2] = make_float2(__uint_as_float(r.b.x), __uint_as_float(r.b.y));
+        x[3] = make_float2(__uint_as_float(r.b.z), __uint_as_float(r.b.w));
     } else {
-        x[0] = bf16lo(r.a.x); x[1] = bf16hi(r.a.x); x[2] = bf16lo(r.a.y); x[3] = bf16hi(r.a.y);
-        x[4] = bf16lo(r.a.z); x[5] = bf16hi(r.a.z); x[6] = bf16lo(r.a.w); x[7] = bf16hi(r.a.w);
+        x[0] = make_float2(bf16lo(r.a.x), bf16hi(r.a.x));
+        x[1] = make_float2(bf16lo(r.a.y), bf16hi(r.a.y));
+        x[2] = make_float2(bf16lo(r.a.z), bf16hi(r.a.z));
+        x[3] = make_float2(bf16lo(r.a.w), bf16hi(r.a.w));
     }
 }
 
@@ -135,7 +136,17 @@ __device__ __forceinline__ float div15(float x) {
     return q == INFINITY ? q : y;
 }
 
-template <int NG, bool F32>
+// 1 / s rounded to nearest, for a bf16 s whose reciprocal is a normal number: the
+// approximate instruction is off by an ulp at most, and one Newton step with the
+// exact remainder gives the rounded reciprocal of any s whose significand is not all
+// ones (Markstein, as above); eight bits followed by zeros are not.
+__device__ __forceinline__ float reciprocal(float s) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(s));
+    return __fmaf_rn(y, __fmaf_rn(-s, y, 1.f), y);
+}
+
+template <int NG, bool F32, int U>
 __global__ void __launch_bounds__(kQ4Warps * 32)
 q4_write_kernel(const void* __restrict__ k, const void* __restrict__ v, const Q4Rows a,
                 unsigned char* __restrict__ kc, unsigned char* __restrict__ vc) {
@@ -148,10 +159,10 @@ q4_write_kernel(const void* __restrict__ k, const void* __restrict__ v, const Q4
     unsigned char* pool = blockIdx.y ? vc : kc;
     const int vecs = a.hkv * (D / 8);  // lanes' worth of dims in a token's row
     const int64_t e0 = n * a.hkv * D;
-    Raw8<F32> raw[kQ4Unroll];
+    Raw8<F32> raw[U];
     auto load = [&](int v0) {
 #pragma unroll
-        for (int u = 0; u < kQ4Unroll; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int vec = v0 + 32 * u + lane;
             raw[u].a = make_uint4(0, 0, 0, 0);
             raw[u].b = make_uint4(0, 0, 0, 0);
@@ -168,61 +179,73 @@ q4_write_kernel(const void* __restrict__ k, const void* __restrict__ v, const Q4
     }
     const int32_t page = (int32_t)a.block.quot((uint32_t)slot);
     const int32_t at = slot - page * (int32_t)a.block.d;
-    for (int v0 = 0; v0 < vecs; v0 += 32 * kQ4Unroll) {
+    // a lane keeps its group and chunk; each step is 8 / NG heads further
+    int head, g, c;
+    lane_place<NG>(lane, &head, &g, &c);
+    unsigned char* row = pool + row_offset<NG>(a, page, at, head);
+    const int64_t row_step = (int64_t)(8 / NG) * a.block.d * q4_row_bytes(D);
+    for (int v0 = 0; v0 < vecs; v0 += 32 * U) {
         if (v0 > 0) load(v0);
 #pragma unroll
-        for (int u = 0; u < kQ4Unroll; ++u) {
-            const int vec = v0 + 32 * u + lane;
-            if (v0 + 32 * u >= vecs) break;  // warp-uniform
-            int head, g, c;
-            lane_place<NG>(vec, &head, &g, &c);
-            float x[8];
+        for (int u = 0; u < U; ++u, row += row_step) {
+            float2 x[4];
             widen8<F32>(raw[u], x);
-            float lo = x[0], hi = x[0];
+            float lo = min_nan(x[0].x, x[0].y), hi = max_nan(x[0].x, x[0].y);
 #pragma unroll
-            for (int i = 1; i < 7; i += 2) {
-                lo = min_nan(lo, x[i], x[i + 1]);
-                hi = max_nan(hi, x[i], x[i + 1]);
+            for (int i = 1; i < 4; ++i) {
+                lo = min_nan(lo, x[i].x, x[i].y);
+                hi = max_nan(hi, x[i].x, x[i].y);
             }
-            lo = min_nan(lo, x[7]);
-            hi = max_nan(hi, x[7]);
 #pragma unroll
             for (int off = 1; off < 4; off <<= 1) {
                 lo = min_nan(lo, __shfl_xor_sync(0xffffffffu, lo, off));
                 hi = max_nan(hi, __shfl_xor_sync(0xffffffffu, hi, off));
             }
             // one rounding per operation (no contraction): the codes are the format's
-            uint32_t sb = f32_to_bf16_bits(div15(__fsub_rn(hi, lo)));
-            float s = __uint_as_float(sb << 16);
-            if (s < 1.17549435e-38f) {  // 2^-126; a NaN stays
-                s = 0.f;
-                sb = 0;
-            }
-            const uint32_t zb = f32_to_bf16_bits(
-                __fadd_rn(__fadd_rn(0.5f * lo, 0.5f * hi), 0.5f * s));
-            const float z = __uint_as_float(zb << 16);
-            const float inv = s > 0.f ? __frcp_rn(s) : 0.f;
-            // rint and the conversion by an addition: 2^23 + 2^22 + 8 + t rounds t to
-            // a whole number, ties to even, and leaves code t + 8 in the low bits.
-            // Clamped first (a NaN becomes -8: code 0), which rounding does not
-            // change.  The bits above the codes add up to a constant.
-            uint32_t w = 0u - 0x4B400000u * 0x11111111u;
+            uint32_t sb = pack_bf16x2(div15(__fsub_rn(hi, lo)), 0.f);
+            const bool usual = sb - 0x80u < 0x7F80u - 0x80u;  // 2^-126 <= s < infinity
+            if (sb < 0x80u) sb = 0;
+            const float s = __uint_as_float(sb << 16);
+            const uint32_t zb =
+                pack_bf16x2(0.f, __fadd_rn(__fadd_rn(0.5f * lo, 0.5f * hi), 0.5f * s));
+            const float z = __uint_as_float(zb);
+            const float inv = usual ? reciprocal(s) : 0.f;
+            // (x - z) / s lies in about -8 .. 7 unless the rounding of s and z moved
+            // an end by half a step: every operation is monotonic, so the ends tell
+            // for the group.  rint(-8.5) is -8 and rint(7.5) is 8.
+            const bool inside = __fmul_rn(__fsub_rn(lo, z), inv) >= -8.5f &&
+                                __fmul_rn(__fsub_rn(hi, z), inv) < 7.5f;
+            float2 q[4];
+            const float2 z2 = make_float2(-z, -z), i2 = make_float2(inv, inv);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float t = fminf(fmaxf(__fmul_rn(__fsub_rn(x[i], z), inv), -8.f), 7.f);
-                w += __float_as_uint(__fadd_rn(t, 12582920.f)) << (4 * i);
+            for (int i = 0; i < 4; ++i) q[i] = fmul2(fadd2(x[i], z2), i2);
+            if (!__all_sync(0xffffffffu, inside)) {  // (a NaN becomes code 0)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    q[i] = make_float2(fminf(fmaxf(q[i].x, -8.f), 7.f),
+                                       fminf(fmaxf(q[i].y, -8.f), 7.f));
+            }
+            // rint and the conversion by an addition: 2^23 + 2^22 + 8 + t rounds t to
+            // a whole number, ties to even, and leaves code t + 8 in the low bits
+            // (clamping to -8 .. 7 before it changes no code).  The bits above the
+            // codes add up to a constant.
+            uint32_t w = 0u - 0x4B400000u * 0x11111111u;
+            const float2 magic = make_float2(12582920.f, 12582920.f);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                q[i] = fadd2(q[i], magic);
+                w += (__float_as_uint(q[i].x) << (8 * i)) + (__float_as_uint(q[i].y) << (8 * i + 4));
             }
             w = units_to_words<NG>(w, lane, g);
-            if (vec < vecs) {
-                unsigned char* row = pool + row_offset<NG>(a, page, at, head);
+            if (v0 + 32 * u + lane < vecs) {
                 *reinterpret_cast<uint32_t*>(row + c * (4 * NG) + g * 4) = w;
-                if (c == 0) *reinterpret_cast<uint32_t*>(row + D / 2 + g * 4) = sb | (zb << 16);
+                if (c == 0) *reinterpret_cast<uint32_t*>(row + D / 2 + g * 4) = sb | zb;
             }
         }
     }
 }
 
-template <int NG, bool F32>
+template <int NG, bool F32, int U>
 __global__ void __launch_bounds__(kQ4Warps * 32)
 q4_read_kernel(const unsigned char* __restrict__ kc, const unsigned char* __restrict__ vc,
                const Q4Rows a, void* __restrict__ k, void* __restrict__ v) {
@@ -240,10 +263,10 @@ q4_read_kernel(const unsigned char* __restrict__ kc, const unsigned char* __rest
     if (slot >= a.num_slots && lane == 0) flag_error(a.err, PKV_FLAG_BAD_SLOT);
     const int32_t page = real ? (int32_t)a.block.quot((uint32_t)slot) : 0;
     const int32_t at = real ? slot - page * (int32_t)a.block.d : 0;
-    for (int v0 = 0; v0 < vecs; v0 += 32 * kQ4Unroll) {
-        uint32_t words[kQ4Unroll], sz[kQ4Unroll];
+    for (int v0 = 0; v0 < vecs; v0 += 32 * U) {
+        uint32_t words[U], sz[U];
 #pragma unroll
-        for (int u = 0; u < kQ4Unroll; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int vec = v0 + 32 * u + lane;
             words[u] = sz[u] = 0;
             if (vec < vecs && real) {
@@ -255,9 +278,8 @@ q4_read_kernel(const unsigned char* __restrict__ kc, const unsigned char* __rest
             }
         }
 #pragma unroll
-        for (int u = 0; u < kQ4Unroll; ++u) {
+        for (int u = 0; u < U; ++u) {
             const int vec = v0 + 32 * u + lane;
-            if (v0 + 32 * u >= vecs) break;  // warp-uniform
             const uint32_t w = words_to_units<NG>(words[u], lane, (vec / 4) % NG);
             const float s = bf16lo(sz[u]), z = bf16hi(sz[u]);
             float x[8];
@@ -279,6 +301,14 @@ q4_read_kernel(const unsigned char* __restrict__ kc, const unsigned char* __rest
     }
 }
 
+// the kernel `name` for a head dim, row type and 32-lane steps in flight per warp
+// (as many as a row has, up to 4)
+#define PKV_Q4_KERNEL(name, d, f32, vecs)                                               \
+    ((d) == 128 ? ((f32) ? PKV_Q4_STEPS(name, 4, true, vecs) : PKV_Q4_STEPS(name, 4, false, vecs)) \
+                : ((f32) ? PKV_Q4_STEPS(name, 2, true, vecs) : PKV_Q4_STEPS(name, 2, false, vecs)))
+#define PKV_Q4_STEPS(name, ng, f32, vecs) \
+    ((vecs) <= 32 ? name<ng, f32, 1> : ((vecs) <= 64 ? name<ng, f32, 2> : name<ng, f32, 4>))
+
 }  // namespace
 
 cudaError_t launch_q4_write(const void* k, const void* v, int src_dtype, const int32_t* slots,
@@ -289,8 +319,7 @@ cudaError_t launch_q4_write(const void* k, const void* v, int src_dtype, const i
     const Q4Rows a{slots, num_tokens, num_slots, FastDiv((uint32_t)block_size), hkv, err};
     const dim3 grid((unsigned)((num_tokens + kQ4Warps - 1) / kQ4Warps), 2);
     const bool f32 = src_dtype == PKV_F32;
-    auto kern = d == 128 ? (f32 ? q4_write_kernel<4, true> : q4_write_kernel<4, false>)
-                         : (f32 ? q4_write_kernel<2, true> : q4_write_kernel<2, false>);
+    auto kern = PKV_Q4_KERNEL(q4_write_kernel, d, f32, hkv * (d / 8));
     return launch_dependent(kern, grid, dim3(kQ4Warps * 32), 0, stream, k, v, a,
                             static_cast<unsigned char*>(k_cache),
                             static_cast<unsigned char*>(v_cache));
@@ -304,8 +333,7 @@ cudaError_t launch_q4_read(const void* k_cache, const void* v_cache, const int32
     const Q4Rows a{slots, num_tokens, num_slots, FastDiv((uint32_t)block_size), hkv, err};
     const dim3 grid((unsigned)((num_tokens + kQ4Warps - 1) / kQ4Warps), 2);
     const bool f32 = dst_dtype == PKV_F32;
-    auto kern = d == 128 ? (f32 ? q4_read_kernel<4, true> : q4_read_kernel<4, false>)
-                         : (f32 ? q4_read_kernel<2, true> : q4_read_kernel<2, false>);
+    auto kern = PKV_Q4_KERNEL(q4_read_kernel, d, f32, hkv * (d / 8));
     return launch_dependent(kern, grid, dim3(kQ4Warps * 32), 0, stream,
                             static_cast<const unsigned char*>(k_cache),
                             static_cast<const unsigned char*>(v_cache), a, k, v);
