@@ -61,8 +61,16 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kHold = 16;         // 16-key products between additions of the offsets' sums
-constexpr float kGrow = 8.f;       // rescale when a score passes the reference by 2^8
-constexpr float kScaleGrow = 4.f;  // or a V scale its bound by 2^4: weights stay below 2^12
+// The reference moves when a score passes it by 2^grow_by() or a V scale its bound by
+// 2^scale_grow(): weights stay below 2^12 (bf16 queries; fp16 holds 11 bits of those
+// down to 2^-14), or, moved up by 2^bias(), below 2^15 (fp32 queries, whose second
+// part then has its bits for weights down to 2^-14 of the largest).
+template <bool F32>
+__host__ __device__ constexpr float grow_by() { return F32 ? 2.f : 8.f; }
+template <bool F32>
+__host__ __device__ constexpr float scale_grow() { return F32 ? 1.f : 4.f; }
+template <bool F32>
+__host__ __device__ constexpr float bias() { return F32 ? 12.f : 0.f; }
 constexpr int kConsumers = 8;  // 12 warps in all leave 168 registers a thread
 constexpr int kProducers = 4;
 constexpr int kThreads = (kConsumers + kProducers) * 32;
@@ -144,20 +152,29 @@ __device__ __forceinline__ void mma_from(float* d, const uint32_t* a, uint32_t b
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 
-// Codes i of both halves of x as two fp16.  A code in the low bits of the
-// mantissa is a subnormal, u 2^-24, and one four bits up is 16 u 2^-24: no
-// conversion, one logic operation per pair of codes and a shift for every other
-// pair.  The factor 16 is taken out of the other operand (scores) or of the
-// result (output), 2^24 at the end.
-// With CENTRED 8 is subtracted (exactly; subnormals again).
-template <bool CENTRED>
+// Codes i of both halves of x as two fp16, in units of code_unit(), those of odd i 16
+// times as large; the factor 16 is taken out of the other operand (scores) or of
+// the result (output).
+//  * bf16 queries: a code in the low bits of the mantissa is a subnormal, u 2^-24, and
+//    one four bits up is 16 u 2^-24: one logic operation per pair of codes and a
+//    shift for every other pair.  The products are aligned by the operands'
+//    exponent fields, which overstate a subnormal by up to 2^10, and cut 25 bits
+//    below the largest: about 2^-15 of the largest weight, under the 2^-12 that
+//    the weights' own rounding leaves.
+//  * EXACT (fp32 queries): 1024 + u, then minus 1024 + 8, gives the normal number
+//    u - 8 (odd i: 1024 + 16 u and 1024 + 128); the second parts of queries and
+//    weights keep their bits.
+template <bool EXACT>
 __device__ __forceinline__ uint32_t codes(uint32_t x, int i) {
     uint32_t y = (i & 2 ? x >> 8 : x) & (i & 1 ? 0x00F000F0u : 0x000F000Fu);
-    if constexpr (CENTRED)
-        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(y) : "r"(i & 1 ? 0x00800080u : 0x00080008u));
+    if constexpr (EXACT) {
+        y |= 0x64006400u;
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(y) : "r"(i & 1 ? 0x64806480u : 0x64086408u));
+    }
     return y;
 }
-constexpr float kUnit = 1.f / 16777216.f;  // 2^-24
+template <bool EXACT>
+__host__ __device__ constexpr float code_unit() { return EXACT ? 1.f : 1.f / 16777216.f; }
 
 __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     uint32_t y;
@@ -463,7 +480,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
     constexpr bool PAIR = QN < 8;
     const uint32_t half_shift = (r / QN) & 1 ? 16 : 0;  // this column's half
     uint32_t qf[PARTS][NG][4];  // score product's columns: 2 k-steps of 2 words per code word
-    float qs[NT][2];            // 2^-24 sum of q over the group of columns 2c, 2c + 1
+    float qs[NT][2];            // sum of q over the group of columns 2c, 2c + 1, in units of code_unit()
     float start[NT][2];         // -8 times those: where a score product starts
     float cq[NP];               // from a product to log2 units, for this lane's queries
     constexpr int OT = PAIR ? NG : 2 * NG;  // output tiles of 16 rows
@@ -541,7 +558,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
         const int ex = (int)(__float_as_uint(mx) >> 23);
         const float up_q = __uint_as_float((uint32_t)min(max(265 - ex, 1), 252) << 23);
-        const float down = a.qscale / kUnit / up_q;
+        const float down = a.qscale / code_unit<F32>() / up_q;
         if constexpr (QN == 2) {
             cq[0] = __shfl_sync(0xffffffffu, down, 4 * (c & 1));
         } else {
@@ -562,7 +579,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
 #pragma unroll
             for (int e = 0; e < 8; ++e) x[e] *= up_q;
             float sum = ((x[0] + x[1]) + (x[2] + x[3])) + ((x[4] + x[5]) + (x[6] + x[7]));
-            sum *= kUnit;
+            sum *= code_unit<F32>();
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
             sum += __shfl_xor_sync(0xffffffffu, sum, 2);
             qs[j][0] = __shfl_sync(0xffffffffu, sum, 8 * c);
@@ -774,7 +791,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
             const int se = min(max((int)(__float_as_uint(smax) >> 23) - 126, -60), 100);
             const float sold = sref;
             sref = fmaxf(sref, (float)se);
-            slim = exp2f(sref + kScaleGrow);
+            slim = exp2f(sref + scale_grow<F32>());
             float f[NP];
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
@@ -786,11 +803,11 @@ q4_split_kernel(const Q4DecodeArgs a) {
 #pragma unroll
                 for (int off = QN == 8 ? 4 : 2; off < 32; off <<= 1)
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                const float mn = fmaxf(m[i] - sold, mx) + sref;
+                const float mn = fmaxf(m[i] - sold + bias<F32>(), mx) + sref - bias<F32>();
                 f[i] = m[i] == -INFINITY ? 0.f : ex2(m[i] - mn);
                 m[i] = mn;
                 mr[i] = mn == -INFINITY ? 0.f : mn;
-                lim[i] = mn - sref + kGrow;
+                lim[i] = mn - sref + bias<F32>() + grow_by<F32>();
                 l[i] *= f[i];
             }
             // factors of this lane's columns 2c, 2c + 1 and of column r
@@ -972,7 +989,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 if (g >= NG || gi != 2 * c / QN) continue;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float u = e & 1 ? 1.f / (16.f * kUnit) : 1.f / kUnit;
+                    const float u = 1.f / code_unit<F32>() / (e & 1 ? 16.f : 1.f);
                     const float* x = o[(PAIR ? g >> 1 : g) * 2 + (e >> 1)] + 2 * (e & 1);
                     val[j][0][e] = fmaf(x[0], u, z0);
                     val[j][1][e] = fmaf(x[1], u, z1);
