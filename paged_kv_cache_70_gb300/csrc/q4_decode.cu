@@ -152,26 +152,30 @@ __device__ __forceinline__ void mma_from(float* d, const uint32_t* a, uint32_t b
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1), "f"(c0), "f"(c1));
 }
 
-// Codes i of both halves of x as two fp16, in units of code_unit(), those of odd i 16
-// times as large; the factor 16 is taken out of the other operand (scores) or of
-// the result (output).
-//  * bf16 queries: a code in the low bits of the mantissa is a subnormal, u 2^-24, and
-//    one four bits up is 16 u 2^-24: one logic operation per pair of codes and a
-//    shift for every other pair.  The products are aligned by the operands'
-//    exponent fields, which overstate a subnormal by up to 2^10, and cut 25 bits
-//    below the largest: about 2^-15 of the largest weight, under the 2^-12 that
-//    the weights' own rounding leaves.
+// Codes 2i and 2i + 1 of both halves of x as operands, in units of code_unit().
+//  * bf16 queries: a code in the low bits of an fp16's mantissa is a subnormal, so
+//    fields of the word are operands as they are.  `low` is code 2i, u0, and
+//    `both` the byte of the two, u0 + 16 u1: two logic operations per pair of codes,
+//    no shift (the upper bytes come by a permutation).  The other operand or the
+//    result takes u1 out again: q0 u0 + q1 u1 = (q0 - q1 / 16) u0 + (q1 / 16) both.
+//    The products are aligned by the operands' exponent fields, which overstate a
+//    subnormal by up to 2^10, and cut 25 bits below the largest: about 2^-15 of the
+//    largest weight, under the 2^-12 that the weights' own rounding leaves.
 //  * EXACT (fp32 queries): 1024 + u, then minus 1024 + 8, gives the normal number
-//    u - 8 (odd i: 1024 + 16 u and 1024 + 128); the second parts of queries and
-//    weights keep their bits.
+//    u0 - 8, and 1024 + 16 u, minus 1024 + 128, 16 (u1 - 8) for `both`; the second
+//    parts of queries and weights keep their bits.
 template <bool EXACT>
-__device__ __forceinline__ uint32_t codes(uint32_t x, int i) {
-    uint32_t y = (i & 2 ? x >> 8 : x) & (i & 1 ? 0x00F000F0u : 0x000F000Fu);
+__device__ __forceinline__ void code_pair(uint32_t x, int i, uint32_t& low, uint32_t& both) {
     if constexpr (EXACT) {
-        y |= 0x64006400u;
-        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(y) : "r"(i & 1 ? 0x64806480u : 0x64086408u));
+        const uint32_t y = i ? x >> 8 : x;
+        low = (y & 0x000F000Fu) | 0x64006400u;
+        both = (y & 0x00F000F0u) | 0x64006400u;
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(low) : "r"(0x64086408u));
+        asm("sub.rn.f16x2 %0, %0, %1;" : "+r"(both) : "r"(0x64806480u));
+    } else {
+        both = i ? __byte_perm(x, 0u, 0x4341) : x & 0x00FF00FFu;
+        low = both & 0x000F000Fu;
     }
-    return y;
 }
 template <bool EXACT>
 __host__ __device__ constexpr float code_unit() { return EXACT ? 1.f : 1.f / 16777216.f; }
@@ -586,8 +590,12 @@ q4_split_kernel(const Q4DecodeArgs a) {
             qs[j][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
             start[j][0] = F32 ? 0.f : -8.f * qs[j][0];
             start[j][1] = F32 ? 0.f : -8.f * qs[j][1];
+            // (codes of odd dims count 16 times, and bring their even neighbours')
 #pragma unroll
-            for (int e = 1; e < 8; e += 2) x[e] *= 0.0625f;  // its codes count 16 times
+            for (int e = 0; e < 8; e += 2) {
+                x[e + 1] *= 0.0625f;
+                if constexpr (!F32) x[e] -= x[e + 1];
+            }
             if constexpr (PAIR) {
                 // word (unit u of 2, pair of groups gp): dims 4u .. 4u + 3 of the
                 // chunk, k-step e / 2, word e % 2
@@ -670,8 +678,9 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 const bool opens = PAIR ? w < NG / 2 && (NT > 1 || w == 0) : true;  // tile j's first
 #pragma unroll
                 for (int st = 0; st < 2; ++st) {
-                    const uint32_t af[4] = {codes<F32>(x[0], 2 * st), codes<F32>(x[1], 2 * st),
-                                            codes<F32>(x[0], 2 * st + 1), codes<F32>(x[1], 2 * st + 1)};
+                    uint32_t af[4];
+                    code_pair<F32>(x[0], st, af[0], af[2]);
+                    code_pair<F32>(x[1], st, af[1], af[3]);
 #pragma unroll
                     for (int part = 0; part < PARTS; ++part) {
                         const uint32_t b0 = qf[part][w][2 * st], b1 = qf[part][w][2 * st + 1];
@@ -903,8 +912,8 @@ q4_split_kernel(const Q4DecodeArgs a) {
                     }
                 }
                 if constexpr (!F32) {
-                    // -8 in the units of rows r (codes 0, 2) and r + 8 (codes 1, 3)
-                    const uint32_t off[4] = {0x80088008u, 0x80808080u, 0x80088008u, 0x80808080u};
+                    // -8 in rows r (u0), -8 - 128 in rows r + 8 (u0 + 16 u1)
+                    const uint32_t off[4] = {0x80088008u, 0x80888088u, 0x80088008u, 0x80888088u};
 #pragma unroll
                     for (int i = 0; i < PW; i += 2) mma(ct[j], off, pf[0][j][i], pf[0][j][i + 1]);
                 }
@@ -916,9 +925,9 @@ q4_split_kernel(const Q4DecodeArgs a) {
                     for (int h = 0; h < 2; ++h)
 #pragma unroll
                         for (int u = 0; u < 4; u += 2) {
-                            const uint32_t af[4] = {
-                                codes<F32>(vw[u][gp], 2 * h), codes<F32>(vw[u][gp], 2 * h + 1),
-                                codes<F32>(vw[u + 1][gp], 2 * h), codes<F32>(vw[u + 1][gp], 2 * h + 1)};
+                            uint32_t af[4];
+                            code_pair<F32>(vw[u][gp], h, af[0], af[1]);
+                            code_pair<F32>(vw[u + 1][gp], h, af[2], af[3]);
                             const int j = 2 * gp / CPT;
 #pragma unroll
                             for (int part = 0; part < PARTS; ++part)
@@ -932,8 +941,9 @@ q4_split_kernel(const Q4DecodeArgs a) {
                     const uint32_t xb = __byte_perm(vw[2][g >> 1], vw[3][g >> 1], sel);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const uint32_t af[4] = {codes<F32>(xa, 2 * h), codes<F32>(xa, 2 * h + 1),
-                                                codes<F32>(xb, 2 * h), codes<F32>(xb, 2 * h + 1)};
+                        uint32_t af[4];
+                        code_pair<F32>(xa, h, af[0], af[1]);
+                        code_pair<F32>(xb, h, af[2], af[3]);
 #pragma unroll
                         for (int part = 0; part < PARTS; ++part)
                             mma(o[2 * g + h], af, pf[part][g][0], pf[part][g][1]);
@@ -991,8 +1001,9 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 for (int e = 0; e < 4; ++e) {
                     const float u = 1.f / code_unit<F32>() / (e & 1 ? 16.f : 1.f);
                     const float* x = o[(PAIR ? g >> 1 : g) * 2 + (e >> 1)] + 2 * (e & 1);
-                    val[j][0][e] = fmaf(x[0], u, z0);
-                    val[j][1][e] = fmaf(x[1], u, z1);
+                    const bool mixed = !F32 && (e & 1);  // holds its even neighbour too
+                    val[j][0][e] = fmaf(x[0] - (mixed ? x[-2] : 0.f), u, z0);
+                    val[j][1][e] = fmaf(x[1] - (mixed ? x[-1] : 0.f), u, z1);
                 }
             }
         }
