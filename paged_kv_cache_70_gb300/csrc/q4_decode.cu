@@ -74,6 +74,8 @@ __host__ __device__ constexpr float bias() { return F32 ? 12.f : 0.f; }
 constexpr int kConsumers = 8;  // 12 warps in all leave 168 registers a thread
 constexpr int kProducers = 4;
 constexpr int kThreads = (kConsumers + kProducers) * 32;
+// KV heads per CTA: 4 with two warps each take larger copies than 8 with one
+constexpr int kMaxHeads = 4;
 constexpr int kMaxStages = 8;
 constexpr int kHeader = 512;  // barriers and stage tags
 constexpr size_t kStaticSmem = 1024;  // left for static shared memory
@@ -261,6 +263,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
     constexpr int NP = QN == 2 ? 1 : 2;            // queries a lane takes exponentials for
     constexpr int NV = QN == 8 ? 2 : 1;            // score rows a lane takes them for
     constexpr int KS = key_steps<QN, F32>();       // 16-key products side by side
+    constexpr bool EARLY = QN > 2;                 // a stage is given back after its loads
     extern __shared__ __align__(128) unsigned char smem[];
     uint64_t* full = reinterpret_cast<uint64_t*>(smem);
     uint64_t* empty = full + kMaxStages;
@@ -324,8 +327,11 @@ q4_split_kernel(const Q4DecodeArgs a) {
         __syncthreads();
     }
     const int32_t total = tstart[a.batch];
+    // (the combine, let start here, reads the tile starts before it waits)
     if (first_cta) {
         for (int b = tid; b <= a.batch; b += blockDim.x) a.tstart[b] = tstart[b];
+        __threadfence();
+        __syncthreads();
     }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int32_t len = share_len(total, a.batch, gridDim.x);
@@ -777,6 +783,33 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 }
             }
         }
+        // The V words, and the stage is given back: with 4 or 8 queries a step computes
+        // for so long that holding it until its end leaves the ring short (8 long
+        // contexts, 4 queries 66.8 us against 69.0; with 2 queries 59.2 against 57.5,
+        // for the registers that the words wait in).
+        uint32_t vw[KS][4][2];
+        auto load_v = [&](int y) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const unsigned char* vr =
+                    tile + half_bytes + v_codes + (16 * y + output_key<NG>(0, i)) * R;
+                if constexpr (NG == 4) {
+                    const uint2 x = *reinterpret_cast<const uint2*>(vr);
+                    vw[y][i][0] = x.x;
+                    vw[y][i][1] = x.y;
+                } else {
+                    vw[y][i][0] = *reinterpret_cast<const uint32_t*>(vr);
+                }
+            }
+        };
+        const bool ends = flags & kTagLast;
+        const int seq = ends ? tags[s].seq : 0;  // (before the stage is given back)
+        if constexpr (EARLY) {
+#pragma unroll
+            for (int y = 0; y < KS; ++y) load_v(y);
+            __syncwarp();
+            if (lane == 0) arrive(empty_bar + 8 * s);
+        }
         float smax = 0.f;
         bool grow = false;
 #pragma unroll
@@ -871,19 +904,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
                     w[i] = (my_q & 1) ? x1 : x0;
                 }
             }
-            uint32_t vw[4][2];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const unsigned char* vr =
-                    tile + half_bytes + v_codes + (16 * y + output_key<NG>(0, i)) * R;
-                if constexpr (NG == 4) {
-                    const uint2 x = *reinterpret_cast<const uint2*>(vr);
-                    vw[i][0] = x.x;
-                    vw[i][1] = x.y;
-                } else {
-                    vw[i][0] = *reinterpret_cast<const uint32_t*>(vr);
-                }
-            }
+            if constexpr (!EARLY) load_v(y);
             // columns: a word per key (its weight in this column's half), or per two
             // keys
             constexpr int PW = PAIR ? 4 : 2;
@@ -926,8 +947,8 @@ q4_split_kernel(const Q4DecodeArgs a) {
 #pragma unroll
                         for (int u = 0; u < 4; u += 2) {
                             uint32_t af[4];
-                            code_pair<F32>(vw[u][gp], h, af[0], af[1]);
-                            code_pair<F32>(vw[u + 1][gp], h, af[2], af[3]);
+                            code_pair<F32>(vw[y][u][gp], h, af[0], af[1]);
+                            code_pair<F32>(vw[y][u + 1][gp], h, af[2], af[3]);
                             const int j = 2 * gp / CPT;
 #pragma unroll
                             for (int part = 0; part < PARTS; ++part)
@@ -937,8 +958,8 @@ q4_split_kernel(const Q4DecodeArgs a) {
 #pragma unroll
                 for (int g = 0; g < NG; ++g) {
                     const uint32_t sel = (g & 1) ? 0x7632 : 0x5410;
-                    const uint32_t xa = __byte_perm(vw[0][g >> 1], vw[1][g >> 1], sel);
-                    const uint32_t xb = __byte_perm(vw[2][g >> 1], vw[3][g >> 1], sel);
+                    const uint32_t xa = __byte_perm(vw[y][0][g >> 1], vw[y][1][g >> 1], sel);
+                    const uint32_t xb = __byte_perm(vw[y][2][g >> 1], vw[y][3][g >> 1], sel);
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         uint32_t af[4];
@@ -952,10 +973,10 @@ q4_split_kernel(const Q4DecodeArgs a) {
             }
         }
         if (!F32 && k % (kHold / KS) == 0) settle();
-        const bool ends = flags & kTagLast;
-        const int seq = ends ? tags[s].seq : 0;  // (before the stage is given back)
-        __syncwarp();
-        if (lane == 0) arrive(empty_bar + 8 * s);
+        if constexpr (!EARLY) {
+            __syncwarp();
+            if (lane == 0) arrive(empty_bar + 8 * s);
+        }
         if (++s == S) {
             s = 0;
             phase ^= 1;
@@ -1106,7 +1127,6 @@ __device__ __forceinline__ void join(float& M, float& L, float* acc, float mo, f
 
 template <int D, bool F32>
 __global__ void __launch_bounds__(kCombineMost * 32) q4_combine_kernel(const Q4CombineArgs a) {
-    PKV_DEPENDENT_PROLOGUE();
     constexpr int E = D / 32;
     __shared__ float part[kCombineMost][32 * E + 2];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
@@ -1115,9 +1135,13 @@ __global__ void __launch_bounds__(kCombineMost * 32) q4_combine_kernel(const Q4C
     const int64_t id = (int64_t)blockIdx.x * per_cta + warp / a.w;
     const bool live = id < (int64_t)a.batch * a.hq;
     const int b = live ? (int)(id / a.hq) : 0, h = live ? (int)(id % a.hq) : 0;
-    const int32_t ta = a.tstart[b], tb = a.tstart[b + 1];
-    const int32_t len = share_len(a.tstart[a.batch], a.batch, a.ctas);
+    // The tile starts: stored and fenced by the split's first block before it lets
+    // this kernel start, which therefore needs not wait for them.
+    const int32_t ta = __ldcg(a.tstart + b), tb = __ldcg(a.tstart + b + 1);
+    const int32_t len = share_len(__ldcg(a.tstart + a.batch), a.batch, a.ctas);
     const int c0 = (ta + b + 1) / len, c1 = tb > ta && live ? (tb + b) / len : c0 - 1;
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     float M = -INFINITY, L = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
@@ -1210,7 +1234,7 @@ bool plan_q4_decode(const DeviceInfo& dev, int32_t batch, int32_t max_blocks, in
     if (p->no > wc) return false;
     p->hc = 1;  // the most KV heads whose queries the consumer warps hold
     for (int h = 1; h * p->no <= wc && h <= hkv; ++h)
-        if (hkv % h == 0) p->hc = h;
+        if (hkv % h == 0 && h <= kMaxHeads) p->hc = h;
     p->head_groups = hkv / p->hc;
     if (p->head_groups > 65535) return false;
     const int units = p->hc * p->no;
