@@ -71,14 +71,16 @@ template <bool F32>
 __host__ __device__ constexpr float scale_grow() { return F32 ? 1.f : 4.f; }
 template <bool F32>
 __host__ __device__ constexpr float bias() { return F32 ? 12.f : 0.f; }
-constexpr int kConsumers = 8;  // 12 warps in all leave 168 registers a thread
 constexpr int kProducers = 4;
-constexpr int kThreads = (kConsumers + kProducers) * 32;
-// KV heads per CTA: 4 with two warps each take larger copies than 8 with one
-constexpr int kMaxHeads = 4;
 constexpr int kMaxStages = 8;
 constexpr int kHeader = 512;  // barriers and stage tags
 constexpr size_t kStaticSmem = 1024;  // left for static shared memory
+
+// Consumer warps: 12 with the 128 registers that 16 warps leave a thread, or 8 with
+// 168 where 8 queries keep four column tiles (8 long contexts, 2 queries per KV head
+// 53.8 us with 12 and 57.2 with 8; 8 queries 128 and 96, for spilled registers).
+__host__ __device__ constexpr int consumers(int qn) { return qn == 8 ? 8 : 12; }
+__host__ __device__ constexpr int threads(int qn) { return (consumers(qn) + kProducers) * 32; }
 
 // 16-key products that a warp runs side by side (its share of a tile)
 template <int QN, bool F32>
@@ -253,9 +255,9 @@ __device__ __forceinline__ void score_row(int key, int* r, int* half) {
 }
 
 template <int NG, int QN, bool F32>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(threads(QN), 1)
 q4_split_kernel(const Q4DecodeArgs a) {
-    constexpr int WC = kConsumers;
+    constexpr int WC = consumers(QN);
     constexpr int D = NG * kQ4Group, R = q4_row_bytes(D);
     constexpr int CPT = 8 / QN;                    // groups per column tile
     constexpr int NT = NG > CPT ? NG / CPT : 1;    // column tiles
@@ -263,7 +265,6 @@ q4_split_kernel(const Q4DecodeArgs a) {
     constexpr int NP = QN == 2 ? 1 : 2;            // queries a lane takes exponentials for
     constexpr int NV = QN == 8 ? 2 : 1;            // score rows a lane takes them for
     constexpr int KS = key_steps<QN, F32>();       // 16-key products side by side
-    constexpr bool EARLY = QN > 2;                 // a stage is given back after its loads
     extern __shared__ __align__(128) unsigned char smem[];
     uint64_t* full = reinterpret_cast<uint64_t*>(smem);
     uint64_t* empty = full + kMaxStages;
@@ -273,7 +274,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
     unsigned char* scratch = smem + kHeader + up((size_t)(a.batch + 1) * 4, 128);
     const int units = a.hc * a.no;  // (head, queries) of the CTA
     unsigned char* ring = scratch + (size_t)units * (a.wh - 1) * state_bytes(NT);
-    __shared__ int32_t warp_sum[kThreads / 32];
+    __shared__ int32_t warp_sum[threads(QN) / 32];
 
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     // A tile is the next T = KEYS * wh keys of a sequence: KEYS for each of the
@@ -285,7 +286,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
     const int active = units * a.wh;  // consumer warps at work
     if (tid == 0) {
         for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&full[s], 2);  // a K and a V producer
             mbar_init(&empty[s], active);
         }
         mbar_init(&merge_bar[0], units * (a.wh - 1) + 1);
@@ -298,7 +299,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
     const int64_t cap = (int64_t)a.max_blocks * a.block_size;
     const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0;
     {
-        constexpr int N = kThreads;
+        constexpr int N = threads(QN);
         const int per = (a.batch + N - 1) / N;
         const int lo = tid * per, hi = min(lo + per, a.batch);
         int32_t sum = 0;
@@ -342,17 +343,18 @@ q4_split_kernel(const Q4DecodeArgs a) {
 
     if (warp >= WC) {
         // ------------------------------ producers -----------------------------
-        // Warp w prepares tiles t0 + w, t0 + w + 4, ..: one tile costs a chain of
-        // ~2000 cycles (slot, table entry, address, barrier) whatever its size.
-        // No more warps than stages: a warp then has seen its stage's last but one
-        // contents consumed (with its own previous tile) before it waits for the
-        // last, which a wait on the phase's parity alone could not tell apart.
-        const int prods = min(kProducers, S);
-        if (warp - WC >= prods) return;
+        // Two pairs of warps take the tiles in turn, one warp of a pair K and the other
+        // V: one tile costs a chain of ~2000 cycles (table entry, address, slot) and
+        // ~60 more for each copy, whatever its size.  No more pairs than stages: a
+        // warp then has seen its stage's last but one contents consumed (with its own
+        // previous tile) before it waits for the last, which a wait on the phase's
+        // parity alone could not tell apart.
+        const bool is_v = (warp - WC) & 1;
+        constexpr int prods = kProducers / 2;
         const uint64_t pol = l2_evict_first_policy();
         const uint32_t inv_hc = 65536u / a.hc + 1;  // i / hc for i < 512, hc <= 16
         const int64_t head_bytes = (int64_t)a.block_size * R;
-        const int32_t tf = t0 + warp - WC;
+        const int32_t tf = t0 + (warp - WC) / 2;
         if (tf >= t1) return;
         int b = 0;  // the sequence of tile t
         {
@@ -407,13 +409,13 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 }
             }
             bad = __any_sync(0xffffffffu, bad);
-            bytes = __reduce_add_sync(0xffffffffu, bytes) * 2 * a.hc;
+            bytes = __reduce_add_sync(0xffffffffu, bytes) * a.hc;
             bool ok = true;
             if (lane == 0) {
                 ok = mbar_wait(&empty[s], (fills & 1) ^ 1, a.err);
                 if (ok) {
                     if (bad) flag_error(a.err, PKV_FLAG_BAD_BLOCK);
-                    tags[s] = Tag{(last ? kTagLast : 0u) |
+                    if (!is_v) tags[s] = Tag{(last ? kTagLast : 0u) |
                                       (k == 0 || t == tstart[seq] ? kTagFirst : 0u) |
                                       (bad || q1 - q0 < T ? kTagPartial : 0u),
                                   q1 - q0, seq, bad ? q0 : -1};
@@ -441,8 +443,8 @@ q4_split_kernel(const Q4DecodeArgs a) {
                                         (int64_t)(lo - pg * a.block_size) * R;
                     unsigned char* dst = kd + ((size_t)h * T + (lo - q0)) * R;
                     const uint32_t n16 = (uint32_t)up((size_t)(hi - lo) * R, 16);
-                    bulk_g2s(dst, a.kc + src, n16, &full[s], pol);
-                    bulk_g2s(dst + half_bytes, a.vc + src, n16, &full[s], pol);
+                    bulk_g2s(is_v ? dst + half_bytes : dst, (is_v ? a.vc : a.kc) + src, n16,
+                             &full[s], pol);
                 }
             }
             __syncwarp();
@@ -783,12 +785,11 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 }
             }
         }
-        // The V words, and the stage is given back: with 4 or 8 queries a step computes
-        // for so long that holding it until its end leaves the ring short (8 long
-        // contexts, 4 queries 66.8 us against 69.0; with 2 queries 59.2 against 57.5,
-        // for the registers that the words wait in).
+        // The V words, and the stage is given back: it is held for its loads, not for
+        // the arithmetic, which keeps the ring of three stages full.
         uint32_t vw[KS][4][2];
-        auto load_v = [&](int y) {
+#pragma unroll
+        for (int y = 0; y < KS; ++y)
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const unsigned char* vr =
@@ -801,15 +802,10 @@ q4_split_kernel(const Q4DecodeArgs a) {
                     vw[y][i][0] = *reinterpret_cast<const uint32_t*>(vr);
                 }
             }
-        };
         const bool ends = flags & kTagLast;
         const int seq = ends ? tags[s].seq : 0;  // (before the stage is given back)
-        if constexpr (EARLY) {
-#pragma unroll
-            for (int y = 0; y < KS; ++y) load_v(y);
-            __syncwarp();
-            if (lane == 0) arrive(empty_bar + 8 * s);
-        }
+        __syncwarp();
+        if (lane == 0) arrive(empty_bar + 8 * s);
         float smax = 0.f;
         bool grow = false;
 #pragma unroll
@@ -904,7 +900,6 @@ q4_split_kernel(const Q4DecodeArgs a) {
                     w[i] = (my_q & 1) ? x1 : x0;
                 }
             }
-            if constexpr (!EARLY) load_v(y);
             // columns: a word per key (its weight in this column's half), or per two
             // keys
             constexpr int PW = PAIR ? 4 : 2;
@@ -973,10 +968,6 @@ q4_split_kernel(const Q4DecodeArgs a) {
             }
         }
         if (!F32 && k % (kHold / KS) == 0) settle();
-        if constexpr (!EARLY) {
-            __syncwarp();
-            if (lane == 0) arrive(empty_bar + 8 * s);
-        }
         if (++s == S) {
             s = 0;
             phase ^= 1;
@@ -1213,7 +1204,7 @@ cudaError_t launch_split(const DeviceInfo& dev, const Q4DecodePlan& p, const Q4D
         set.fetch_or(bit, std::memory_order_relaxed);
     }
     return launch_dependent(kern, dim3(p.ctas, p.head_groups),
-                            dim3(kThreads), p.smem_bytes, stream, a);
+                            dim3(threads(QN)), p.smem_bytes, stream, a);
 }
 
 }  // namespace
@@ -1229,12 +1220,16 @@ bool plan_q4_decode(const DeviceInfo& dev, int32_t batch, int32_t max_blocks, in
     const bool f32 = q_dtype == PKV_F32;
     const int G = hq / hkv;
     p->qn = G <= 2 ? 2 : (G <= 4 ? 4 : 8);
-    const int wc = kConsumers;
+    const int wc = consumers(p->qn);
     p->no = (G + p->qn - 1) / p->qn;
     if (p->no > wc) return false;
-    p->hc = 1;  // the most KV heads whose queries the consumer warps hold
-    for (int h = 1; h * p->no <= wc && h <= hkv; ++h)
-        if (hkv % h == 0 && h <= kMaxHeads) p->hc = h;
+    // KV heads per CTA: the most, up to 6 warps' worth, that keep four fifths of the
+    // consumers at work; the warps left over share a head's keys.  (8 heads: 4 with
+    // 3 warps each.  Fewer heads take larger copies, more heads fewer merges.)
+    p->hc = 1;
+    auto at_work = [&](int h) { return wc / (h * p->no) * (h * p->no); };
+    for (int h = 1; h <= hkv && h * p->no <= std::max(6, p->no); ++h)
+        if (hkv % h == 0 && (5 * at_work(h) >= 4 * wc || at_work(h) > at_work(p->hc))) p->hc = h;
     p->head_groups = hkv / p->hc;
     if (p->head_groups > 65535) return false;
     const int units = p->hc * p->no;
