@@ -349,6 +349,9 @@ q4_split_kernel(const Q4DecodeArgs a) {
         // warp then has seen its stage's last but one contents consumed (with its own
         // previous tile) before it waits for the last, which a wait on the phase's
         // parity alone could not tell apart.
+#ifdef PKV_TEST_SPLIT_PRODUCER_IDLE
+        return;  // test-only build: issue nothing, so the consumers' first wait runs out
+#endif
         const bool is_v = (warp - WC) & 1;
         constexpr int prods = kProducers / 2;
         const uint64_t pol = l2_evict_first_policy();

@@ -181,6 +181,14 @@ DECODE = [  # lens, Hq, Hkv, d, B, dtype
     ([20000, 9000, 1], 16, 8, 128, 256, "bf16"),
     ([12345], 2, 1, 128, 16, "bf16"),
     ([40] * 200 + [1500], 16, 8, 128, 16, "bf16"),
+    ([500, 33], 10, 5, 128, 16, "bf16"),
+    ([77, 410], 28, 7, 64, 32, "bf16"),
+    ([96, 97, 95], 20, 10, 128, 16, "bf16"),
+    ([385, 383], 24, 12, 128, 8, "f32"),
+    ([1000, 20], 64, 1, 128, 16, "bf16"),
+    ([700], 128, 2, 64, 16, "f32"),
+    ([100, 3], 18, 6, 64, 64, "f32"),
+    ([50] * 3, 32, 32, 128, 16, "bf16"),
 ]
 
 
@@ -342,6 +350,56 @@ def test_decode_workspace_and_shape_refusals():
         pkv.paged_decode_q4(dev[0].half(), *dev[1:])
     with pytest.raises(pkv.PagedKVError):
         pkv.paged_decode_q4(dev[0][:, :12].contiguous(), *dev[1:])  # 12 % 8
+    for hq, hkv, d, block in ((65, 1, 128, 16), (130, 2, 64, 16), (4, 2, 64, 7)):
+        q = torch.zeros(2, hq, d, device="cuda", dtype=torch.bfloat16)
+        kc = torch.zeros(pkv.q4_cache_shape(4, block, hkv, d), dtype=torch.uint8, device="cuda")
+        t = torch.zeros(2, 2, dtype=torch.int32, device="cuda")
+        with pytest.raises(pkv.PagedKVError) as e:
+            pkv.paged_decode_q4(q, kc, kc, t, dev[4])
+        assert e.value.status == -2
+
+
+def test_pages_past_four_gigabytes():
+    """Pages at the end of a pool whose byte offsets pass 32 bits: write, read,
+    decode and copy."""
+    hq, hkv, d, block, lens = 16, 8, 128, 16, [300, 41]
+    page = hkv * block * 80
+    total = (5 << 30) // page
+    if torch.cuda.mem_get_info()[0] < 4 * total * page:
+        pytest.skip("needs 20 GB of device memory")
+    rng = np.random.default_rng(5)
+    table, used = pages(rng, lens, block, extra=0)
+    far = np.where(table < 0, -1, total - 1 - table).astype(np.int32)  # the last pages
+    kd, vd = (torch.empty(pkv.q4_cache_shape(total, block, hkv, d), dtype=torch.uint8,
+                          device="cuda") for _ in range(2))
+    seq = np.concatenate([np.full(n, i) for i, n in enumerate(lens)]).astype(np.int32)
+    pos = np.concatenate([np.arange(n) for n in lens]).astype(np.int32)
+    slots = slots_of(far, seq, pos, block).astype(np.int32)
+    x = [rng.standard_normal((len(seq), hkv, d)).astype(np.float32) for _ in range(2)]
+    pkv.paged_kv_write_q4(to_dev(x[0]), to_dev(x[1]), to_dev(slots), kd, vd)
+    k, v = pkv.paged_kv_read_q4(kd, vd, to_dev(slots), torch.float32)
+    rows = [Q.quantise(a) for a in x]
+    assert np.array_equal(to_host(k), Q.values(rows[0]).astype(np.float32))
+    assert np.array_equal(to_host(v), Q.values(rows[1]).astype(np.float32))
+    near = [np.zeros((used, hkv, block, 80), np.uint8) for _ in x]
+    for pool, r in zip(near, rows):
+        pool[table[seq, pos // block], :, pos % block] = r
+    q = rng.standard_normal((2, hq, d)).astype(np.float32)
+    out = pkv.paged_decode_q4(to_dev(q), kd, vd, to_dev(far), to_dev(np.asarray(lens, np.int32)))
+    want, tol = Q.decode(q, near[0], near[1], table, lens, d ** -0.5)
+    check(out, want, tol)
+    src, dst = int(far[0, 0]), 3
+    pkv.paged_copy_blocks(kd, vd, to_dev(np.asarray([src], np.int32)),
+                          to_dev(np.asarray([dst], np.int32)))
+    assert torch.equal(kd[src], kd[dst]) and torch.equal(vd[src], vd[dst])
+    # the last page's tokens kept every other one, in place
+    keep = np.arange(0, lens[0], 2, dtype=np.int32)[1:]
+    keep = np.concatenate([[0], keep]).astype(np.int32)
+    pkv.paged_kv_compact(kd, vd, to_dev(far[:1]), to_dev(keep),
+                         to_dev(np.asarray([0, len(keep)], np.int32)))
+    k, _ = pkv.paged_kv_read_q4(kd, vd, to_dev(slots[:len(keep)]), torch.float32)
+    assert np.array_equal(to_host(k), Q.values(rows[0][keep]).astype(np.float32))
+    assert pkv.paged_error_flags() == 0
 
 
 # ---------------------------------------------------------------------------
