@@ -444,6 +444,24 @@ int paged_bm_fork(pkv_block_manager* bm, int64_t seq, int64_t* child_out);
 int paged_bm_append(pkv_block_manager* bm, int64_t seq, int64_t token, int32_t* cow_src_out,
                     int32_t* cow_dst_out);
 
+/* The bookkeeping of paged_kv_compact for `seq`: it keeps its tokens below
+ * `start` and, of the others, those at the positions keep[0 .. n_keep)
+ * (strictly ascending, in [start, length)).  Blocks behind the new end are
+ * released, in reverse order.  A shared block that rows move into is replaced
+ * by a new block: the *n_cow_out pairs (cow_src_out[i], cow_dst_out[i]) must be
+ * copied first (paged_copy_blocks).  table_out [table_capacity, at least the
+ * present table's length] receives the present table with those replacements:
+ * pass it to paged_kv_compact, in stream order before any write into the
+ * released blocks.  Blocks that rows move into leave the prefix cache and never
+ * enter it again (their tokens no longer say what they hold), nor do the
+ * sequence's later blocks; a last block that is partial now leaves it too.
+ * PKV_ERR_INVALID (a capacity too small: *n_cow_out says how many pairs there
+ * are) and PKV_ERR_NO_SPACE change nothing. */
+int paged_bm_compact(pkv_block_manager* bm, int64_t seq, int64_t start, const int32_t* keep,
+                     int64_t n_keep, int32_t* table_out, int32_t table_capacity,
+                     int32_t* cow_src_out, int32_t* cow_dst_out, int32_t cow_capacity,
+                     int32_t* n_cow_out);
+
 /* Release a sequence: its blocks in reverse order, refs -1 each; a block at 0
  * leaves the cache and is pushed on the free stack. */
 int paged_bm_free(pkv_block_manager* bm, int64_t seq);
@@ -529,12 +547,18 @@ int paged_kv_read_q4(const void* k_cache, const void* v_cache, const int32_t* sl
  * each, read through block_table row b; 0 when cache_seqlens[b] == 0.  The
  * values are used as stored (4-bit codes, bf16 scales); scores, softmax
  * statistics and sums are fp32.
- * Supported: any Hq / Hkv; head_dim 64 or 128; any block_size; batch <= 4096.
+ * Supported: any Hq / Hkv up to 64; head_dim 128 with any block_size, 64 with an
+ * even one; batch <= 4096; max_blocks_per_seq * block_size up to 2^31 - 4097.
+ * Rounding: with bf16 queries each weight is multiplied by its V scale and
+ * rounded to fp16 (11 bits; those below 2^-14 of the largest to 2^-25 of it),
+ * below the output's own rounding; with fp32 queries, queries and weights keep
+ * 22 bits or more.  Values of V past 1e33 in magnitude may give infinities.  A NaN
+ * or infinite query, or a NaN key, makes its own heads' output NaN.
  * workspace: paged_decode_q4_workspace_size(batch, q_dtype, geom) bytes, 256-byte
- * aligned, contents irrelevant on entry, as for paged_decode (may be NULL when
- * that size is 0).  A length below 0 or past the table counts as the nearest
- * valid one (PKV_FLAG_BAD_LENGTH); keys of a bad page are skipped
- * (PKV_FLAG_BAD_BLOCK).
+ * aligned, contents irrelevant on entry, as for paged_decode; it must not be used
+ * by another call that runs concurrently.  A length below 0 or past the table
+ * counts as the nearest valid one (PKV_FLAG_BAD_LENGTH); keys of a bad page are
+ * skipped (PKV_FLAG_BAD_BLOCK).
  */
 size_t paged_decode_q4_workspace_size(int32_t batch, int32_t q_dtype, const pkv_geom* geom);
 int paged_decode_q4(const void* q, int32_t q_dtype, const void* k_cache, const void* v_cache,

@@ -59,6 +59,7 @@ EXPORTED = (
     "paged_decode_q4_workspace_size",
     "paged_decode_q4",
     "paged_kv_compact",
+    "paged_bm_compact",
 )
 PKV_ERR_NO_SPACE = -5
 
@@ -153,8 +154,9 @@ def load_library(path: str | None = None):
         lib.paged_bm_seq_len.argtypes = [vp, i64, i64p]
         lib.paged_bm_ref_count.argtypes = [vp, i32, i32p]
         lib.paged_bm_free_blocks.argtypes = [vp, vp, i64, i64p]
+        lib.paged_bm_compact.argtypes = [vp, i64, i64, vp, i64, vp, i32, vp, vp, i32, i32p]
         for f in ("create", "destroy", "allocate", "fork", "append", "free", "block_table",
-                  "seq_len", "ref_count", "free_blocks"):
+                  "seq_len", "ref_count", "free_blocks", "compact"):
             getattr(lib, "paged_bm_" + f).restype = ctypes.c_int
         lib.paged_decode_shared_prefix_workspace_size.argtypes = [i32, gp]
         lib.paged_decode_shared_prefix_workspace_size.restype = sz
@@ -539,6 +541,24 @@ class BlockManager:
 
     def free(self, seq: int) -> None:
         _check("paged_bm_free", self._lib.paged_bm_free(self._h, seq))
+
+    def compact(self, seq: int, keep, start: int = 0) -> tuple[list[int], list[int], list[int]]:
+        """Keep the tokens below ``start`` and at the positions ``keep`` (ascending).
+        Returns (src, dst, table): the block copies to make first and the table
+        to pass to paged_kv_compact; the blocks behind the new end are released."""
+        keep = [int(p) for p in keep]
+        if any(not -(2**31) <= p < 2**31 for p in keep):
+            raise ValueError("keep must hold 32-bit positions")
+        table = self.table(seq)
+        arr = (ctypes.c_int32 * max(1, len(keep)))(*keep)
+        rows = (ctypes.c_int32 * max(1, len(table)))()
+        src, dst = ((ctypes.c_int32 * max(1, len(table)))() for _ in range(2))
+        n = ctypes.c_int32()
+        vp = ctypes.c_void_p
+        _check("paged_bm_compact", self._lib.paged_bm_compact(
+            self._h, seq, start, ctypes.cast(arr, vp), len(keep), ctypes.cast(rows, vp), len(table),
+            ctypes.cast(src, vp), ctypes.cast(dst, vp), len(table), ctypes.byref(n)))
+        return list(src[: n.value]), list(dst[: n.value]), list(rows[: len(table)])
 
     def table(self, seq: int) -> list[int]:
         n = ctypes.c_int32()

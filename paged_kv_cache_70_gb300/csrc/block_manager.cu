@@ -49,6 +49,9 @@ struct KeyHash {
 struct Seq {
     std::vector<int32_t> table;
     std::vector<int64_t> tokens;
+    // Blocks from this index on hold rows that were moved (paged_bm_compact): their
+    // tokens no longer say what they hold, so they never enter the cache.
+    size_t moved_from = SIZE_MAX;
 };
 
 }  // namespace
@@ -71,13 +74,15 @@ struct pkv_block_manager {
     }
     void release(int32_t b) {
         if (--ref[b] == 0) {
-            if (keyed[b]) {
-                cache.erase(key_of[b]);
-                keyed[b] = 0;
-                key_of[b].tokens.clear();
-            }
+            uncache(b);
             free_stack.push_back(b);
         }
+    }
+    void uncache(int32_t b) {
+        if (!keyed[b]) return;
+        cache.erase(key_of[b]);
+        keyed[b] = 0;
+        key_of[b].tokens.clear();
     }
     void enter(int32_t b, Key&& k) {
         Key copy = k;
@@ -194,10 +199,12 @@ int paged_bm_append(pkv_block_manager* bm, int64_t seq, int64_t token, int32_t* 
             s.table.back() = nb;
             src = last;
             dst = nb;
+        } else {
+            bm->uncache(last);  // a block cut by paged_bm_compact is written anew from here
         }
     }
     s.tokens.push_back(token);
-    if ((L + 1) % B == 0) {  // the last block just filled: cache it
+    if ((L + 1) % B == 0 && s.table.size() <= s.moved_from) {  // the last block just filled
         Key k;
         k.parent = s.table.size() >= 2 ? s.table[s.table.size() - 2] : -1;
         k.tokens.assign(s.tokens.end() - B, s.tokens.end());
@@ -207,6 +214,66 @@ int paged_bm_append(pkv_block_manager* bm, int64_t seq, int64_t token, int32_t* 
     *cow_src_out = src;
     *cow_dst_out = dst;
     return PKV_OK;
+}
+
+int paged_bm_compact(pkv_block_manager* bm, int64_t seq, int64_t start, const int32_t* keep,
+                     int64_t n_keep, int32_t* table_out, int32_t table_capacity,
+                     int32_t* cow_src_out, int32_t* cow_dst_out, int32_t cow_capacity,
+                     int32_t* n_cow_out) try {
+    if (!bm || !n_cow_out || n_keep < 0 || (n_keep > 0 && !keep) || start < 0 ||
+        table_capacity < 0 || cow_capacity < 0)
+        return PKV_ERR_INVALID;
+    auto it = bm->seqs.find(seq);
+    if (it == bm->seqs.end()) return PKV_ERR_INVALID;
+    Seq& s = it->second;
+    const int64_t B = bm->B, L = (int64_t)s.tokens.size();
+    if (start > L || n_keep > L - start) return PKV_ERR_INVALID;
+    const int64_t end = start + n_keep;
+    if ((int64_t)s.table.size() > table_capacity || (!s.table.empty() && !table_out))
+        return PKV_ERR_INVALID;
+    int64_t first = end;  // the first position whose row changes
+    for (int64_t i = n_keep; i-- > 0;) {
+        if (keep[i] < start + i || keep[i] >= L || (i > 0 && keep[i - 1] >= keep[i]))
+            return PKV_ERR_INVALID;
+        if (keep[i] != start + i) first = start + i;
+    }
+    // blocks written: those of positions first .. end - 1; shared ones are copied
+    const size_t b0 = (size_t)(first / B), b1 = (size_t)((end + B - 1) / B);
+    int32_t n_cow = 0;
+    for (size_t i = b0; first < end && i < b1; ++i) n_cow += bm->ref[s.table[i]] > 1;
+    *n_cow_out = n_cow;
+    if (n_cow > cow_capacity || (n_cow > 0 && (!cow_src_out || !cow_dst_out)))
+        return PKV_ERR_INVALID;
+    if (n_cow > (int64_t)bm->free_stack.size()) return PKV_ERR_NO_SPACE;
+    std::vector<int64_t> tokens(s.tokens.begin(), s.tokens.begin() + start);
+    tokens.reserve((size_t)end);
+    for (int64_t i = 0; i < n_keep; ++i) tokens.push_back(s.tokens[(size_t)keep[i]]);
+    bm->free_stack.reserve(bm->ref.size());
+    // from here on nothing can fail
+    int32_t c = 0;
+    for (size_t i = b0; first < end && i < b1; ++i) {
+        const int32_t old = s.table[i];
+        if (bm->ref[old] > 1) {
+            const int32_t nb = bm->take();
+            bm->release(old);
+            s.table[i] = nb;
+            cow_src_out[c] = old;
+            cow_dst_out[c++] = nb;
+        } else {
+            bm->uncache(old);
+        }
+    }
+    if (first < end) s.moved_from = std::min(s.moved_from, b0);
+    if (!s.table.empty()) std::memcpy(table_out, s.table.data(), s.table.size() * sizeof(int32_t));
+    for (size_t i = s.table.size(); i-- > b1;) bm->release(s.table[i]);
+    s.table.resize(b1);
+    s.tokens.swap(tokens);
+    // a last block that is partial now will be written into (a shared one is copied
+    // first, by paged_bm_append)
+    if (end % B && bm->ref[s.table.back()] == 1) bm->uncache(s.table.back());
+    return PKV_OK;
+} catch (...) {  // out of host memory: before anything changed
+    return PKV_ERR_NO_SPACE;
 }
 
 int paged_bm_free(pkv_block_manager* bm, int64_t seq) {
