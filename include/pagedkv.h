@@ -548,11 +548,13 @@ int paged_kv_read_q4(const void* k_cache, const void* v_cache, const int32_t* sl
  * values are used as stored (4-bit codes, bf16 scales); scores, softmax
  * statistics and sums are fp32.
  * Supported: any Hq / Hkv up to 64; head_dim 128 with any block_size, 64 with an
- * even one; batch <= 4096; max_blocks_per_seq * block_size up to 2^31 - 4097.
+ * even one; batch <= 4096; max_blocks_per_seq * block_size up to 2^31 - 4097, and
+ * below 2^34 for the whole batch.
  * Rounding: with bf16 queries each weight is multiplied by its V scale and
  * rounded to fp16 (11 bits; those below 2^-14 of the largest to 2^-25 of it),
  * below the output's own rounding; with fp32 queries, queries and weights keep
- * 22 bits or more.  Values of V past 1e33 in magnitude may give infinities.  A NaN
+ * 22 bits or more.  Values of V past 1e33 in magnitude may give infinities; scales of
+ * V count to 2^-85 absolutely, so that groups of V that span less lose them.  A NaN
  * or infinite query, or a NaN key, makes its own heads' output NaN.
  * workspace: paged_decode_q4_workspace_size(batch, q_dtype, geom) bytes, 256-byte
  * aligned, contents irrelevant on entry, as for paged_decode; it must not be used
@@ -578,7 +580,8 @@ int paged_decode_q4(const void* q, int32_t q_dtype, const void* k_cache, const v
  * must be >= start[b] + i, which any ascending list is.  cu_keep [batch + 1]
  * starts at 0 and ends at total_keep, the length of keep.  seqlens_out [batch] (may be
  * NULL) receives start[b] + (number kept), for the next decode; it may be the
- * lengths' own array (no lengths are read).
+ * lengths' own array (no lengths are read), or `start` itself (which then moves
+ * on in place), but may overlap no input otherwise.
  * Rows at and behind the new end keep their old contents.  The pages written
  * must belong to one sequence only (copy shared ones first, paged_copy_blocks).
  * An entry below start[b] + i or past the table sets PKV_FLAG_BAD_LENGTH, and a

@@ -81,6 +81,32 @@ __device__ __forceinline__ void copy_async(Vec* dst, const void* src) {
     }
 }
 
+// A sequence's list and start: the number kept; nothing (flagged by `report`) and a
+// start within the table where they are out of range.
+__device__ __forceinline__ int32_t kept(const CompactArgs& a, int b, bool report, int32_t& c0,
+                                        int32_t& start) {
+    c0 = __ldg(a.cu + b);
+    const int32_t c1 = __ldg(a.cu + b + 1);
+    start = a.start ? a.start[b] : 0;
+    const int32_t cap = a.max_blocks * (int32_t)a.block.d;
+    if (c0 >= 0 && c1 >= c0 && c1 <= a.total && start >= 0 && (int64_t)start + (c1 - c0) <= cap)
+        return c1 - c0;
+    if (report) flag_error(a.err, PKV_FLAG_BAD_LENGTH);
+    start = min(max(start, 0), cap);
+    return 0;
+}
+
+// The new lengths, after every CTA has read the starts: launched only where both are
+// one array (a draft's lengths, moved on in place), one thread per sequence.
+__global__ void __launch_bounds__(128) compact_lengths_kernel(const CompactArgs a, int32_t batch) {
+    PKV_DEPENDENT_PROLOGUE();
+    const int b = blockIdx.x * blockDim.x + threadIdx.x;
+    if (b >= batch) return;
+    int32_t c0, start;
+    const int32_t n = kept(a, b, false, c0, start);
+    a.seqlens_out[b] = start + n;
+}
+
 // row ring, then lookup ring
 template <typename Shape>
 constexpr size_t ring_bytes() {
@@ -99,16 +125,10 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kCtas) compact_kernel(
     constexpr int kIndexRing = kDepth + 2;
     extern __shared__ __align__(16) unsigned char smem[];
     const int tid = threadIdx.x, b = blockIdx.y;
-    const int32_t c0 = __ldg(a.cu + b), c1 = __ldg(a.cu + b + 1);
-    int32_t start = a.start ? __ldg(a.start + b) : 0;
     const bool report = blockIdx.x == 0 && blockIdx.z == 0;
     const int32_t cap = a.max_blocks * (int32_t)a.block.d;
-    int32_t n = c1 - c0;
-    if (c0 < 0 || c1 < c0 || c1 > a.total || start < 0 || (int64_t)start + n > cap) {
-        if (report && tid == 0) flag_error(a.err, PKV_FLAG_BAD_LENGTH);
-        start = min(max(start, 0), cap);
-        n = 0;
-    }
+    int32_t c0, start;
+    const int32_t n = kept(a, b, report && tid == 0, c0, start);
     if (report && tid == 0 && a.seqlens_out) a.seqlens_out[b] = start + n;
     if (n == 0) return;
     const int32_t* list = a.keep + c0;
@@ -276,11 +296,19 @@ cudaError_t launch_compact(const DeviceInfo& dev, const CompactLaunch& c, cudaSt
         vec /= 2;
     a.vec_per_head = (int32_t)(c.piece_bytes / vec);
     a.vecs = (int32_t)(a.vec_per_head * c.pieces);
-    const int64_t mean = (c.total + c.batch - 1) / c.batch;
-    if (vec == 16) return launch_typed<uint4>(dev.device, mean, c.batch, a, stream);
-    if (vec == 8) return launch_typed<uint2>(dev.device, mean, c.batch, a, stream);
-    if (vec == 4) return launch_typed<uint32_t>(dev.device, mean, c.batch, a, stream);
-    return launch_typed<uint16_t>(dev.device, mean, c.batch, a, stream);
+    // the starts' own array takes the lengths once every CTA has read it
+    const bool in_place = c.seqlens_out && c.seqlens_out == c.start;
+    CompactArgs lengths = a;
+    if (in_place) a.seqlens_out = nullptr;
+    const int64_t mean = ((int64_t)c.total + c.batch - 1) / c.batch;
+    cudaError_t e;
+    if (vec == 16) e = launch_typed<uint4>(dev.device, mean, c.batch, a, stream);
+    else if (vec == 8) e = launch_typed<uint2>(dev.device, mean, c.batch, a, stream);
+    else if (vec == 4) e = launch_typed<uint32_t>(dev.device, mean, c.batch, a, stream);
+    else e = launch_typed<uint16_t>(dev.device, mean, c.batch, a, stream);
+    if (e != cudaSuccess || !in_place) return e;
+    return launch_dependent(compact_lengths_kernel, dim3((unsigned)((c.batch + 127) / 128)),
+                            dim3(128), 0, stream, lengths, c.batch);
 }
 
 }  // namespace pkv

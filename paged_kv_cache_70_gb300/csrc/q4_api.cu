@@ -10,6 +10,12 @@ using pkv::elt_size;
 
 namespace {
 
+// batch int32 values at a and at b share some, but are not one array
+bool straddle(const int32_t* a, const int32_t* b, int64_t n) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && x != y && (x < y ? y - x : x - y) < (uintptr_t)n * sizeof(int32_t);
+}
+
 int cuda_status(cudaError_t e) { return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA; }
 
 // the geometry of a call on 4-bit pools (geom->dtype PKV_Q4)
@@ -115,6 +121,7 @@ int paged_kv_compact(void* k_cache, void* v_cache, const int32_t* block_table,
     if (batch < 0 || max_blocks_per_seq < 0 || total_keep < 0) return PKV_ERR_INVALID;
     if (batch == 0) return PKV_OK;
     if (batch > 65535) return PKV_ERR_UNSUPPORTED;  // one grid row per sequence
+    if (straddle(start, seqlens_out, batch)) return PKV_ERR_INVALID;
     if (!cu_keep || (total_keep > 0 && (!keep || !block_table || !k_cache || !v_cache)))
         return PKV_ERR_INVALID;
     // positions are int32

@@ -104,6 +104,81 @@ def test_lists_need_not_ascend():
     run("bf16", [16], [0], keep, np.asarray([0, 8], np.int32), 4, 2, 64, 1, use_start=False)
 
 
+@pytest.mark.parametrize("dtype,block,hkv,d", [("bf16", 16, 8, 128), ("q4", 16, 2, 64), ("f32", 4, 40, 128)])
+def test_the_starts_own_array_takes_the_new_lengths(dtype, block, hkv, d):
+    """Lengths before a draft, moved on in place by its accepted tokens (every CTA of
+    a sequence has to read the start before it changes)."""
+    rng = np.random.default_rng(hkv)
+    lens = [int(n) for n in rng.integers(0, 90, 300)] + [3000]
+    starts = np.asarray([rng.integers(0, n + 1) for n in lens], np.int32)
+    t, total = tables(rng, lens, block)
+    k, v = (make(rng, dtype, total, block, hkv, d) for _ in range(2))
+    keep, cu = lists_of(rng, lens, starts, 0.4)
+    at = to_dev(starts)
+    kd, vd = to_dev(k), to_dev(v)
+    pkv.paged_kv_compact(kd, vd, to_dev(t), to_dev(keep), to_dev(cu), at, at)
+    for got, was in ((kd, k), (vd, v)):
+        assert np.array_equal(to_host(got).view(np.uint8),
+                              Q.compact(was, t, keep, cu, starts, dtype == "q4").view(np.uint8))
+    assert np.array_equal(to_host(at), starts + np.diff(cu))
+    # starts out of range are flagged and brought into the table
+    far = to_dev(np.asarray([-5, block * t.shape[1] + 9] + [0] * (len(lens) - 2), np.int32))
+    pkv.paged_kv_compact(kd, vd, to_dev(t), to_dev(keep[:0]), to_dev(np.zeros_like(cu)), far, far)
+    assert to_host(far).tolist() == [0, block * t.shape[1]] + [0] * (len(lens) - 2)
+    assert pkv.paged_error_flags() == pkv.PKV_FLAG_BAD_LENGTH
+
+
+def test_the_most_sequences():
+    """65,535 of them, two tokens each, the second kept."""
+    n = 65535
+    k = torch.arange(2 * n, device="cuda", dtype=torch.float32).reshape(n, 2, 1, 1)
+    kd, vd = k.clone(), -k
+    i32 = dict(dtype=torch.int32, device="cuda")
+    new = torch.full((n,), -1, **i32)
+    pkv.paged_kv_compact(kd, vd, torch.arange(n, **i32)[:, None], torch.ones(n, **i32),
+                         torch.arange(n + 1, **i32), None, new)
+    want = k.clone()
+    want[:, 0] = k[:, 1]
+    assert torch.equal(kd, want) and torch.equal(vd, -want)
+    assert bool((new == 1).all()) and pkv.paged_error_flags() == 0
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "q4"])
+def test_with_the_block_managers_bookkeeping(dtype):
+    """Forked sequences: the copies and the table that BlockManager.compact names, then
+    the move; each sequence reads back its own rows."""
+    rng = np.random.default_rng(9)
+    block, hkv, d, total = 16, 2, 64, 40
+    k, v = (make(rng, dtype, total, block, hkv, d) for _ in range(2))
+    kd, vd = to_dev(k), to_dev(v)
+    bm = pkv.BlockManager(total, block)
+    a, _ = bm.allocate(range(100))
+    b = bm.fork(a)
+    c, _ = bm.allocate(range(1000, 1070))
+
+    def rows(seq, x):
+        t, n = np.asarray(bm.table(seq)), bm.seq_len(seq)
+        pos = np.arange(n)
+        x = to_host(x)
+        return x[t[pos // block], :, pos % block] if dtype == "q4" else x[t[pos // block], pos % block]
+
+    want = {s: [rows(s, x) for x in (kd, vd)] for s in (a, b, c)}
+    for seq, start, keep in ((b, 20, [30, 31, 50, 77, 99]), (c, 0, list(range(3, 70, 2))),
+                             (a, 90, [95]), (b, 25, [])):
+        src, dst, table = bm.compact(seq, keep, start)
+        if src:
+            pkv.paged_copy_blocks(kd, vd, *(to_dev(np.asarray(x, np.int32)) for x in (src, dst)))
+        one = lambda *x: to_dev(np.asarray(x, np.int32))  # noqa: E731
+        at = one(start)
+        pkv.paged_kv_compact(kd, vd, one(*table)[None], one(*keep), one(0, len(keep)), at, at)
+        want[seq] = [np.concatenate([x[:start], x[keep]]) if keep else x[:start] for x in want[seq]]
+        assert at.tolist() == [bm.seq_len(seq)]
+        for s, w in want.items():
+            for x, y in zip((kd, vd), w):
+                assert np.array_equal(rows(s, x), y)
+    assert pkv.paged_error_flags() == 0
+
+
 def test_bad_entries_are_flagged_and_left_out():
     rng = np.random.default_rng(0)
     t, total = tables(rng, [32, 32, 32], 8)

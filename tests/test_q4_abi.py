@@ -79,6 +79,10 @@ def test_compact_refusals(lib):
         assert f(P, P, P, 4, P, P, 3, P, 70000, P, g, None) == -2
         assert f(P, P, P, 1 << 28, P, P, 3, P, 2, P, g, None) == -2  # positions > int32
         assert f(None, None, None, 4, None, None, 0, None, 0, None, g, None) == 0
+        # the new lengths share a part of the starts (the whole of them is a call)
+        for by in (4, -4, 36):
+            at, new = ctypes.c_void_p(1024), ctypes.c_void_p(1024 + by)
+            assert f(P, P, P, 4, at, P, 3, P, 10, new, g, None) == -1
     assert f(P, P, P, 4, P, P, 3, P, 2, P, None, None) == -1
     assert f(P, P, P, 4, P, P, 3, P, 2, P, geom(dtype=7), None) == -1
     assert f(ODD, P, P, 4, P, P, 3, P, 2, P, geom(), None) == -1
