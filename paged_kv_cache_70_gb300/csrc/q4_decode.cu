@@ -1250,6 +1250,7 @@ bool plan_q4_decode(const DeviceInfo& dev, int32_t batch, int32_t max_blocks, in
     // one CTA per SM, no more than there can be tiles
     const int64_t tiles = ((int64_t)max_blocks * block_size + p->tile - 1) / p->tile * batch;
     const int64_t most = std::max(1, dev.num_sms / p->head_groups);
+    if (tiles + batch > 0x7fffffffLL - most) return false;  // the line of tiles is 32 bits long
     p->ctas = (int)std::max<int64_t>(1, std::min(most, tiles));
     const size_t slots = (size_t)most + batch;  // whatever the table's width is
     p->ws_bytes = up((size_t)(batch + 1) * 4, 256) + up(slots * hq * 2 * 4, 256) +

@@ -328,6 +328,66 @@ def test_decode_in_two_graphs_that_share_a_workspace_and_on_other_streams():
         check(out, want, tol)
 
 
+def test_the_largest_batch_and_one_more():
+    rng = np.random.default_rng(8)
+    lens = rng.integers(0, 20, 4096).tolist()
+    lens[77] = 3000
+    q, kc, vc, table = decode_case(lens, 2, 1, 64, 16, "bf16", 8)
+    dev = [to_dev(x) for x in (q, kc, vc, table, np.asarray(lens, np.int32))]
+    want, tol = Q.decode(q, kc, vc, table, lens, 0.125)
+    check(pkv.paged_decode_q4(*dev), want, tol)
+    with pytest.raises(pkv.PagedKVError) as e:
+        pkv.paged_decode_q4(torch.cat([dev[0], dev[0][:1]]), dev[1], dev[2],
+                            torch.cat([dev[3], dev[3][:1]]), torch.cat([dev[4], dev[4][:1]]))
+    assert e.value.status == -2
+    # more keys in all than the split can number: refused, whatever the lengths are
+    wide = torch.zeros(4096, 5000, dtype=torch.int32, device="cuda")
+    pool = torch.zeros(pkv.q4_cache_shape(2, 400000, 1, 64), dtype=torch.uint8, device="cuda")
+    with pytest.raises(pkv.PagedKVError) as e:
+        pkv.paged_decode_q4(dev[0], pool, pool, wide, dev[4])
+    assert e.value.status == -2
+    assert pkv.paged_error_flags() == 0
+
+
+def test_a_step_in_one_graph_replayed_as_the_lengths_move_on():
+    """Slots, write, decode and lengths + 1, captured once and replayed; then the same
+    rows evicted by a captured compaction."""
+    rng = np.random.default_rng(6)
+    hq, hkv, d, block, first, steps = 8, 4, 64, 16, [14, 0, 200], 5
+    table, total = pages(rng, [n + steps for n in first], block, width=14)
+    kc = make_pool(rng, total, hkv, block, d, table, first)
+    vc = make_pool(rng, total, hkv, block, d, table, first)
+    kd, vd, td = to_dev(kc), to_dev(vc), to_dev(table)
+    lens = to_dev(np.asarray(first, np.int32))
+    seq = to_dev(np.arange(3, dtype=np.int32))
+    q, k, v = (torch.zeros(3, h, d, device="cuda", dtype=torch.bfloat16) for h in (hq, hkv, hkv))
+    out = torch.empty_like(q)
+    slots = torch.empty(3, dtype=torch.int32, device="cuda")
+    ws = torch.empty(pkv.paged_decode_q4_workspace_size(3, hq, torch.bfloat16, kd),
+                     dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        pkv.paged_build_slot_mapping(td, seq, lens, block, slots)
+        pkv.paged_kv_write_q4(k, v, slots, kd, vd)
+        lens += 1
+        pkv.paged_decode_q4(q, kd, vd, td, lens, out=out, workspace=ws)
+    assert lens.tolist() == first
+    at = np.asarray(first)
+    for step in range(steps):
+        x = [bf16(rng.standard_normal((3, h, d))) for h in (hq, hkv, hkv)]
+        for dst, src in zip((q, k, v), x):
+            dst.copy_(to_dev(src))
+        g.replay()
+        for pool, rows in ((kc, x[1]), (vc, x[2])):
+            pool[table[np.arange(3), at // block], :, at % block] = Q.quantise(Q.bf16_value(rows))
+        at = at + 1
+        assert np.array_equal(to_host(kd), kc) and np.array_equal(to_host(vd), vc)
+        want, tol = Q.decode(x[0], kc, vc, table, at, d ** -0.5)
+        check(out, want, tol, f"replay {step}")
+    assert lens.tolist() == at.tolist() and pkv.paged_error_flags() == 0
+
+
 def test_decode_workspace_and_shape_refusals():
     lens = [300, 41]
     q, kc, vc, table = decode_case(lens, 16, 8, 128, 16, "bf16", 30)
