@@ -15,12 +15,17 @@
 // No flags, no waits between CTAs, and the result does not depend on the order in
 // which they run.
 //
-// HBM-bound: each moved row is read and written once; rows that stay where they
-// are (p_i = start + i) are neither read nor written.  A round is a chain of four
-// memory latencies (list entry, table entry, row, store), so a CTA keeps five
-// rounds of rows in flight (cp.async into shared memory, each thread its own
-// vectors), the list two rounds further ahead and the table entries one: 85 KB of
-// loads per CTA, two CTAs per SM.
+// HBM-bound where the sequences are many: each moved row is read and written once;
+// rows that stay where they are (p_i = start + i) are neither read nor written.  A round
+// is a chain of four memory latencies (list entry, table entry, row, store), so a CTA
+// keeps up to six rounds of rows in flight (cp.async into shared memory, each thread
+// its own vectors), the table entries of the next round and the list entries of the one
+// after: 80 KB of rows per CTA and two CTAs per SM.  Nothing joins the rounds of a
+// sequence but their order, which bounds few sequences: those take narrower slices and
+// more tokens per round (launch_typed).
+// Measured: half of the tokens of 8 contexts of 16 K - 41 K (bf16, 8 heads, d = 128,
+// 970.7 MB read and written) 187 us, 5180 GB/s (0.76 of the measured copy rate; the longest
+// sequence ends last); 64 contexts up to 4 K 98 us, 5630 GB/s; one of 41 K 48 us.
 #include <algorithm>
 #include <atomic>
 
@@ -33,11 +38,23 @@ namespace pkv {
 namespace {
 
 constexpr int kCompactUnroll = 2;  // rows of a round per thread
-// A CTA's shape: threads, rounds in flight, tokens per round at most.  Short lists
-// are one round, and many small CTAs start sooner.
+// A CTA's shape: threads, rounds in flight, tokens per round at most, CTAs per SM.
+// A sequence's rounds are a chain, so a sequence takes as many rounds as its list has
+// tokens per round, whatever the other SMs do: few sequences take narrow slices and
+// many tokens per round.
 struct LongLists {
     static constexpr int kThreads = 512, kDepth = 5, kTokens = 128, kCtas = 2;
 };
+struct FewLists {
+    static constexpr int kThreads = 512, kDepth = 5, kTokens = 256, kCtas = 2;
+};
+struct TwoLists {
+    static constexpr int kThreads = 512, kDepth = 3, kTokens = 512, kCtas = 2;
+};
+struct OneList {
+    static constexpr int kThreads = 512, kDepth = 6, kTokens = 512, kCtas = 1;
+};
+// Short lists are one round, and many small CTAs start sooner.
 struct ShortLists {
     static constexpr int kThreads = 128, kDepth = 1, kTokens = 32, kCtas = 8;
 };
@@ -240,13 +257,18 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kCtas) compact_kernel(
     }
 }
 
+// vectors per slice: as many as let a round hold the mean list, up to kTokens
+template <typename Shape>
+int slice_of(int vecs, int64_t mean) {
+    constexpr int kRow = Shape::kThreads * kCompactUnroll;
+    const int want = (int)std::min<int64_t>(Shape::kTokens, std::max<int64_t>(mean, 8));
+    return std::max(std::min(vecs, kRow / want), kRow / Shape::kTokens);
+}
+
 template <typename Vec, typename Shape>
 cudaError_t launch_shaped(int device, int64_t mean, int32_t batch, CompactArgs& a,
                           cudaStream_t stream) {
-    // a slice as wide as lets a round hold the mean list, up to kTokens
-    constexpr int kRow = Shape::kThreads * kCompactUnroll;
-    const int want = (int)std::min<int64_t>(Shape::kTokens, std::max<int64_t>(mean, 8));
-    a.slice = std::max(std::min(a.vecs, kRow / want), kRow / Shape::kTokens);
+    a.slice = slice_of<Shape>(a.vecs, mean);
     a.tokens = std::min(Shape::kThreads / a.slice, Shape::kTokens / kCompactUnroll);
     const dim3 grid((unsigned)((a.vecs + a.slice - 1) / a.slice), (unsigned)batch, 2);
     auto kern = compact_kernel<Vec, Shape>;
@@ -260,15 +282,31 @@ cudaError_t launch_shaped(int device, int64_t mean, int32_t batch, CompactArgs& 
     }
     return launch_dependent(kern, grid, dim3(Shape::kThreads), compact_smem<Shape>(), stream, a);
 }
-// Lists of up to 32 tokens on average take the small CTAs: the accepted tokens of
-// 64 drafts take 3.5 us (bf16) against 3.8; half of long contexts 187 us with the
-// large ones, 246 with half their size.
+
+// Lists of up to 32 tokens on average take the small CTAs: the accepted tokens of 64
+// drafts take 3.5 us (bf16) against 3.8.  Longer ones take the most tokens per round
+// whose CTAs are all resident at once, or, of 256 per round, in two turns.  Half of the
+// tokens of 1, 2, 4, 5, 6 and 8 contexts of 8 K - 40 K (bf16, 8 heads, d = 128), us:
+//   OneList 48, 65, - | TwoLists 69, 58, 96 | FewLists 73, 73, 88, 129, 144, 173
+//   LongLists 118, 96, 125, 155, 166, 181 (64 contexts up to 4 K: 98, FewLists 113)
 template <typename Vec>
-cudaError_t launch_typed(int device, int64_t mean, int32_t batch, CompactArgs& a,
+cudaError_t launch_typed(const DeviceInfo& dev, int64_t mean, int32_t batch, CompactArgs& a,
                          cudaStream_t stream) {
-    return mean <= ShortLists::kTokens
-               ? launch_shaped<Vec, ShortLists>(device, mean, batch, a, stream)
-               : launch_shaped<Vec, LongLists>(device, mean, batch, a, stream);
+    if (mean <= ShortLists::kTokens)
+        return launch_shaped<Vec, ShortLists>(dev.device, mean, batch, a, stream);
+    auto resident = [&](auto shape, int turns) {
+        using Shape = decltype(shape);
+        const int slice = slice_of<Shape>(a.vecs, mean);
+        return (int64_t)((a.vecs + slice - 1) / slice) * batch * 2 <=
+               (int64_t)dev.num_sms * Shape::kCtas * turns;
+    };
+    if (resident(OneList{}, 1))
+        return launch_shaped<Vec, OneList>(dev.device, mean, batch, a, stream);
+    if (resident(TwoLists{}, 1))
+        return launch_shaped<Vec, TwoLists>(dev.device, mean, batch, a, stream);
+    if (resident(FewLists{}, 2))
+        return launch_shaped<Vec, FewLists>(dev.device, mean, batch, a, stream);
+    return launch_shaped<Vec, LongLists>(dev.device, mean, batch, a, stream);
 }
 
 }  // namespace
@@ -302,10 +340,10 @@ cudaError_t launch_compact(const DeviceInfo& dev, const CompactLaunch& c, cudaSt
     if (in_place) a.seqlens_out = nullptr;
     const int64_t mean = ((int64_t)c.total + c.batch - 1) / c.batch;
     cudaError_t e;
-    if (vec == 16) e = launch_typed<uint4>(dev.device, mean, c.batch, a, stream);
-    else if (vec == 8) e = launch_typed<uint2>(dev.device, mean, c.batch, a, stream);
-    else if (vec == 4) e = launch_typed<uint32_t>(dev.device, mean, c.batch, a, stream);
-    else e = launch_typed<uint16_t>(dev.device, mean, c.batch, a, stream);
+    if (vec == 16) e = launch_typed<uint4>(dev, mean, c.batch, a, stream);
+    else if (vec == 8) e = launch_typed<uint2>(dev, mean, c.batch, a, stream);
+    else if (vec == 4) e = launch_typed<uint32_t>(dev, mean, c.batch, a, stream);
+    else e = launch_typed<uint16_t>(dev, mean, c.batch, a, stream);
     if (e != cudaSuccess || !in_place) return e;
     return launch_dependent(compact_lengths_kernel, dim3((unsigned)((c.batch + 127) / 128)),
                             dim3(128), 0, stream, lengths, c.batch);

@@ -98,6 +98,16 @@ def test_every_token_moves_a_fixed_way(dtype, gap):
     run(dtype, [n], [0], keep, np.asarray([0, n - gap], np.int32), 16, 4, 64, gap, use_start=False)
 
 
+@pytest.mark.parametrize("dtype,hkv,d", [("bf16", 8, 128), ("q4", 8, 128), ("f32", 1, 128)])
+@pytest.mark.parametrize("lens", [[3000], [700, 2500], [1500, 20, 900, 2100], [900, 600] * 4,
+                                  [200] * 11, [100, 300] * 12, [70] * 150])
+def test_any_number_of_sequences(dtype, hkv, d, lens):
+    """From one sequence, cut into narrow slices, to so many that each has wide ones."""
+    rng = np.random.default_rng(len(lens))
+    keep, cu = lists_of(rng, lens, [0] * len(lens), 0.6)
+    run(dtype, lens, [0] * len(lens), keep, cu, 16, hkv, d, 3, use_start=False)
+
+
 def test_lists_need_not_ascend():
     """Any order whose i-th entry is at least start + i (here also one entry twice)."""
     keep = np.asarray([9, 3, 5, 12, 12, 8, 11, 7], np.int32)
