@@ -14,11 +14,11 @@
 // the CUDA cores one query head alone would need 8 warp instructions of FMAs per
 // key plus 16 for unpacking, and the queries of a group multiply the first.  So
 // the products run on the tensor cores, from registers: a lane unpacks codes
-// straight into the operand fragments of mma.m16n8k16 (a nibble becomes the bf16
-// 128 + u with one shift and one logic operation per PAIR of codes), keys (score)
-// or dims (output) as the 16 rows and queries as the 8 columns.  tcgen05 would
-// need the unpacked operand written to shared or tensor memory first, four times
-// the bytes that came in, only to multiply it by 2 to 8 columns.
+// straight into the operand fragments of mma.m16n8k16 (one or two logic operations
+// per PAIR of codes, code_pair below), keys (score) or dims (output) as the 16 rows
+// and queries as the 8 columns.  tcgen05 would need the unpacked operand written to
+// shared or tensor memory first, four times the bytes that came in, only to multiply
+// it by 2 to 8 columns.
 //
 //  * Columns.  A group of QN = 2, 4 or 8 query heads (the next size up from
 //    Hq / Hkv; more heads: several warps) shares the 8 columns with 8 / QN groups
@@ -27,25 +27,37 @@
 //    zeros that would not have been issued anyway.  The score tile is scaled per
 //    group, summed over the groups by a reduce-scatter among the 4 lanes of a row
 //    and each lane takes the exponential of its own share.
-//  * Offsets.  sum (u - 8) x = sum (128 + u) x - 136 sum x: the score's
-//    accumulator starts at -136 sum q; for the output a second product of the
-//    constant -136 with the same weights follows each first one, so the two cancel
-//    step by step and nothing large is carried through a long sum.  With fp32
-//    queries 136 is subtracted from the operand (exactly), and queries and
-//    weights enter as three bf16 parts (24 bits), three products each.
-//  * Weights are rounded to bf16 after the V scale is multiplied in (once, 2^-9
-//    relative at most, as every bf16 attention path here does); the offsets' part
-//    sum p z and all sums stay fp32.
-//  * Reference maximum: lags.  State and output are rescaled only when a score
-//    exceeds the reference by more than 2^8 (one vote per 16 keys).
-//  * Work split as in decode.cu: the tiles of all sequences in one list, cut into
-//    equal contiguous shares, one per CTA; each (CTA, sequence) piece leaves a
-//    partial state that a second kernel merges.  A producer warp brings tiles of K
-//    and V into a ring of stages, one bulk copy per page piece and head; consumer
-//    warps own (head, 8 queries) and take 16 keys at a time.
+//  * Offsets.  sum (u - 8) x = sum u x - 8 sum x: the score's accumulator starts at
+//    -8 sum q; for the output a product of the constant -8 with the weights runs
+//    beside the others, in sums of its own that are added every kHold products, so
+//    that nothing large is carried through a long sum.  With fp32 queries 8 is taken
+//    off the operand instead (exactly), and queries and weights enter as two fp16
+//    parts (22 bits), two products each.
+//  * Weights are rounded to fp16 after the V scale is multiplied in, relative to a
+//    reference that includes log2 of the largest V scale (2^-11 at most, below the
+//    2^-8 of the bf16 output); the offsets' part sum p z and all sums stay fp32.
+//  * Reference maximum: lags.  State and output are rescaled only when a score or a
+//    V scale exceeds the reference by more than grow_by() or scale_grow() (one vote
+//    per tile).
+//  * Work split: the tiles of all sequences in one list, cut into equal contiguous
+//    shares, one per CTA; each (CTA, sequence) piece leaves a partial state that a
+//    second kernel merges.  Four producer warps bring tiles of K and V into a ring of
+//    stages, one bulk copy per page piece and head; the other 12 (8 queries: 8) own
+//    a (head, queries) and a share of the tile's keys each, and hold a stage for their
+//    loads only.
 //  * Keys of a page outside the pool are skipped and flagged; rows past the length
 //    never enter: their scales count as 0 and their scores as -inf, whatever the
 //    page holds there.  Every wait is time-limited.
+//
+// Measured (bf16 queries, device time of split and combine; of the measured copy rate):
+//   8 sequences of 16 K - 41 K keys, 16 / 8 heads, d = 128, 303 MB   53.1 us  0.84
+//   the same with 32 / 8 heads 64.4 us (issue slots), 64 / 8 heads 95.9
+//   64 sequences of 128 - 4096 keys, 16 / 8 heads, B = 16, 173 MB    37.8 us  0.68
+//   8 x 16 K - 41 K keys, 16 / 8 heads, d = 64, 152 MB               41.7 us
+//   one of 7777 keys, 32 / 4 heads, d = 64                            9.4 us
+//   fp32 queries, 8 x 8 K - 20 K keys, 16 / 8 heads, d = 128         46.1 us
+// 7 to 8 us of each are two launches, the plan, the first tile and the combine; the
+// long contexts' split alone issues in half of its cycles (profile: 50 %).
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -101,7 +113,7 @@ struct Q4DecodeArgs {
     int32_t max_blocks, batch, hq, hkv, block_size;
     int32_t hc;      // KV heads per CTA
     int32_t no;      // warps' worth of query heads per KV head
-    int32_t wh;      // warps that share a head and its queries (16 keys each)
+    int32_t wh;      // warps that share a head and its queries (part of a tile's keys each)
     int32_t stages;
     FastDiv block;   // by the page size
 };
@@ -164,7 +176,7 @@ __device__ __forceinline__ void mma_from(float* d, const uint32_t* a, uint32_t b
 //    result takes u1 out again: q0 u0 + q1 u1 = (q0 - q1 / 16) u0 + (q1 / 16) both.
 //    The products are aligned by the operands' exponent fields, which overstate a
 //    subnormal by up to 2^10, and cut 25 bits below the largest: about 2^-15 of the
-//    largest weight, under the 2^-12 that the weights' own rounding leaves.
+//    largest weight, under the 2^-11 that the weights' own rounding leaves.
 //  * EXACT (fp32 queries): 1024 + u, then minus 1024 + 8, gives the normal number
 //    u0 - 8, and 1024 + 16 u, minus 1024 + 128, 16 (u1 - 8) for `both`; the second
 //    parts of queries and weights keep their bits.
