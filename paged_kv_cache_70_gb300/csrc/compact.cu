@@ -167,17 +167,20 @@ __global__ void __launch_bounds__(Shape::kThreads, Shape::kCtas) compact_kernel(
     // Three steps of a token's lookup, in rounds of their own so that each load has
     // time to arrive: the list entry, the two table entries, the offsets.
     auto entry = [&](int r) {
-        const int64_t i = (int64_t)r * step + tid;
-        return indexer && i < n ? __ldg(list + i) : kNone;
+        const uint32_t i = (uint32_t)r * step + tid;
+        return indexer && i < (uint32_t)n ? __ldg(list + i) : 0;
     };
     struct Pages {
         int32_t src, dst;
     };
-    auto pages = [&](int r, int32_t& p) {  // p: kNone where nothing moves
+    auto pages = [&](int r, int32_t& p) {  // makes p kNone where nothing moves
         Pages g{-1, -1};
-        const int32_t to = start + r * step + tid;
-        if (p == to) p = kNone;  // stays
-        if (p == kNone) return g;
+        const uint32_t i = (uint32_t)r * step + tid;
+        const int32_t to = start + (int32_t)i;
+        if (!indexer || i >= (uint32_t)n || p == to) {  // no such token, or it stays
+            p = kNone;
+            return g;
+        }
         if (p < to || p >= cap) {
             if (report) flag_error(a.err, PKV_FLAG_BAD_LENGTH);
             p = kNone;

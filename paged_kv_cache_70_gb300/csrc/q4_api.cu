@@ -129,8 +129,6 @@ int paged_kv_compact(void* k_cache, void* v_cache, const int32_t* block_table,
     const bool q4 = geom->dtype == PKV_Q4;
     const int align = q4 ? 16 : elt_size(geom->dtype);
     if (!aligned(k_cache, align) || !aligned(v_cache, align)) return PKV_ERR_INVALID;
-    DeviceInfo dev;
-    if (pkv::current_device_info(&dev) != cudaSuccess) return PKV_ERR_CUDA;
     pkv::CompactLaunch c{};
     c.k_cache = k_cache;
     c.v_cache = v_cache;
@@ -157,6 +155,14 @@ int paged_kv_compact(void* k_cache, void* v_cache, const int32_t* block_table,
     }
     c.page_bytes = c.pieces * c.piece_bytes * geom->block_size;
     if (c.pieces * c.piece_bytes > (1 << 24)) return PKV_ERR_UNSUPPORTED;
+    // pools that share rows: K's moves and V's, in no order, would move some twice
+    const uintptr_t kp = reinterpret_cast<uintptr_t>(k_cache);
+    const uintptr_t vp = reinterpret_cast<uintptr_t>(v_cache);
+    const uintptr_t pool_bytes = (uintptr_t)(geom->num_blocks * c.page_bytes);
+    if (total_keep > 0 && (kp < vp ? vp - kp : kp - vp) < pool_bytes)
+        return PKV_ERR_INVALID;
+    DeviceInfo dev;
+    if (pkv::current_device_info(&dev) != cudaSuccess) return PKV_ERR_CUDA;
     return cuda_status(pkv::launch_compact(dev, c, stream));
 }
 

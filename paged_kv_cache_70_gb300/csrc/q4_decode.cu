@@ -94,7 +94,9 @@ constexpr size_t kStaticSmem = 1024;  // left for static shared memory
 __host__ __device__ constexpr int consumers(int qn) { return qn == 8 ? 8 : 12; }
 __host__ __device__ constexpr int threads(int qn) { return (consumers(qn) + kProducers) * 32; }
 
-// 16-key products that a warp runs side by side (its share of a tile)
+// 16-key products that a warp runs side by side (its share of a tile): two hide one
+// another's latencies (8 long contexts 66.7 us with two and 79 with one, of an earlier
+// form); with 8 queries they spill (121 us against 96).
 template <int QN, bool F32>
 __host__ __device__ constexpr int key_steps() { return QN == 8 ? 1 : 2; }
 
@@ -1239,8 +1241,10 @@ bool plan_q4_decode(const DeviceInfo& dev, int32_t batch, int32_t max_blocks, in
     p->no = (G + p->qn - 1) / p->qn;
     if (p->no > wc) return false;
     // KV heads per CTA: the most, up to 6 warps' worth, that keep four fifths of the
-    // consumers at work; the warps left over share a head's keys.  (8 heads: 4 with
-    // 3 warps each.  Fewer heads take larger copies, more heads fewer merges.)
+    // consumers at work; the warps left over share a head's keys.  (8 heads: 4 with 3
+    // warps each, 38.2 us at 64 sequences and 53.8 at 8 long contexts; 2 heads with 6
+    // warps, and more merges, 39.7 and 53.2; 8 heads with 1 warp, and 4 idle, 38.5 and
+    // 57.3.)
     p->hc = 1;
     auto at_work = [&](int h) { return wc / (h * p->no) * (h * p->no); };
     for (int h = 1; h <= hkv && h * p->no <= std::max(6, p->no); ++h)

@@ -212,6 +212,7 @@ def test_bad_entries_are_flagged_and_left_out():
     # an entry below its place, one past the table, one negative
     assert call(t, [5, 0, 7, 32, 9, -1], [0, 3, 5, 6], [0, 0, 0], L,
                 [(0, 5, 0), (0, 7, 2), (1, 9, 1)]) == [3, 2, 1]
+    assert call(t, [5, -2 ** 31, 2 ** 31 - 1], [0, 1, 2, 3], [0, 0, 0], L, [(0, 5, 0)]) == [1, 1, 1]
     # a bad source page, a bad destination page
     bad = t.copy()
     bad[0, 1], bad[1, 0] = -1, total
@@ -260,8 +261,13 @@ def test_no_lengths_out_no_tokens_other_stream_and_graph():
 
 def test_binding_refusals():
     k = torch.zeros(4, 8, 2, 64, device="cuda")
+    both = torch.zeros(5, 8, 2, 64, device="cuda")
     i = lambda *x: torch.tensor(x, dtype=torch.int32, device="cuda")  # noqa: E731
     t = i(0, 1, 2, 3).reshape(2, 2)
+    for v in (k, both[1:]):  # pools that share rows
+        with pytest.raises(pkv.PagedKVError) as e:
+            pkv.paged_kv_compact(k if v is k else both[:4], v, t, i(1), i(0, 1))
+        assert e.value.status == -1
     with pytest.raises(ValueError):
         pkv.paged_kv_compact(k, k[:2], t, i(1), i(0, 1))
     with pytest.raises(ValueError):

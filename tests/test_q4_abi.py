@@ -83,6 +83,9 @@ def test_compact_refusals(lib):
         for by in (4, -4, 36):
             at, new = ctypes.c_void_p(1024), ctypes.c_void_p(1024 + by)
             assert f(P, P, P, 4, at, P, 3, P, 10, new, g, None) == -1
+        # pools that share their rows, or some
+        assert f(P, P, P, 4, P, P, 3, P, 2, P, g, None) == -1
+        assert f(P, ctypes.c_void_p(4096), P, 4, P, P, 3, P, 2, P, g, None) == -1
     assert f(P, P, P, 4, P, P, 3, P, 2, P, None, None) == -1
     assert f(P, P, P, 4, P, P, 3, P, 2, P, geom(dtype=7), None) == -1
     assert f(ODD, P, P, 4, P, P, 3, P, 2, P, geom(), None) == -1
