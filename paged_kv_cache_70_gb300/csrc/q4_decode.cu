@@ -120,16 +120,11 @@ struct Q4DecodeArgs {
     FastDiv block;   // by the page size
 };
 
-// One stage's description, written by the producer: a word of flags and the key
-// count, which every tile reads, and what only some do.
-constexpr uint32_t kTagLast = 1;     // the piece of the sequence ends here
-constexpr uint32_t kTagFirst = 2;    // a sequence starts in this CTA: load its queries
-constexpr uint32_t kTagPartial = 4;  // fewer keys than the tile holds, or a bad page
+// One stage's description, written by the producer
 struct Tag {
-    uint32_t flags;
-    int32_t rows;  // keys
-    int32_t seq;   // sequence
-    int32_t bad;   // first key's position if a page was out of range, else -1
+    uint32_t partial;  // fewer keys than the tile holds, or a bad page
+    int32_t rows;      // keys
+    int32_t bad;       // first key's position if a page was out of range, else -1
 };
 
 // ---- the split's shares: tile t of sequence b sits at t + b + 1 on a line (a
@@ -145,6 +140,16 @@ __device__ __forceinline__ int32_t share_first(const int32_t* tstart, int batch,
     }
     if (lo >= batch) return tstart[batch];
     return (int32_t)max((int64_t)tstart[lo], x - lo - 1);
+}
+
+// the sequence of tile t
+__device__ __forceinline__ int share_seq(const int32_t* tstart, int batch, int32_t t) {
+    int lo = 0, hi = batch;
+    while (lo < hi) {
+        const int mid = (lo + hi) >> 1;
+        if (tstart[mid + 1] <= t) lo = mid + 1; else hi = mid;
+    }
+    return lo;
 }
 
 __host__ __device__ constexpr size_t up(size_t x, size_t a) { return (x + a - 1) / a * a; }
@@ -373,15 +378,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
         const int64_t head_bytes = (int64_t)a.block_size * R;
         const int32_t tf = t0 + (warp - WC) / 2;
         if (tf >= t1) return;
-        int b = 0;  // the sequence of tile t
-        {
-            int lo = 0, hi = a.batch;
-            while (lo < hi) {
-                const int mid = (lo + hi) >> 1;
-                if (tstart[mid + 1] <= tf) lo = mid + 1; else hi = mid;
-            }
-            b = lo;
-        }
+        int b = share_seq(tstart, a.batch, tf);  // the sequence of tile t
         int32_t L = (int32_t)min((int64_t)max(__ldg(a.seqlens + b), 0), cap);
         // ids of a tile's first 32 pages, one tile ahead
         auto fetch = [&](int bb, int32_t p0, int32_t p1) {
@@ -398,7 +395,6 @@ q4_split_kernel(const Q4DecodeArgs a) {
             const int seq = b;
             const int32_t q0 = p0, q1 = p1;  // this tile's keys
             int32_t page = next_page;
-            const bool last = t + 1 == tstart[b + 1] || t + 1 == t1;
             if (t + prods < t1) {  // the next tile's sequence and pages
                 if (t + prods >= tstart[b + 1]) {
                     do ++b; while (tstart[b + 1] <= t + prods);
@@ -432,10 +428,8 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 ok = mbar_wait(&empty[s], (fills & 1) ^ 1, a.err);
                 if (ok) {
                     if (bad) flag_error(a.err, PKV_FLAG_BAD_BLOCK);
-                    if (!is_v) tags[s] = Tag{(last ? kTagLast : 0u) |
-                                      (k == 0 || t == tstart[seq] ? kTagFirst : 0u) |
-                                      (bad || q1 - q0 < T ? kTagPartial : 0u),
-                                  q1 - q0, seq, bad ? q0 : -1};
+                    if (!is_v)
+                        tags[s] = Tag{bad || q1 - q0 < T, q1 - q0, bad ? q0 : -1};
                     mbar_arrive_expect_tx(&full[s], bytes);
                 }
             }
@@ -768,21 +762,27 @@ q4_split_kernel(const Q4DecodeArgs a) {
     clear();
 
     int s = 0;
-    uint32_t phase = 0;  // of stage s
+    uint32_t phase = 0;    // of stage s
+    int seq = share_seq(tstart, a.batch, t0) - 1;  // sequence of tile k
+    int32_t next = 0;      // the tile that the next one begins with
     for (int32_t k = 0; k < n_tiles; ++k) {
+        if (k == next) {  // (before the wait: the first queries come with the first tile)
+            do ++seq; while (tstart[seq + 1] <= t0 + k);
+            next = min(tstart[seq + 1] - t0, n_tiles);
+            load_queries(seq);
+        }
         if (!wait_phase(full_bar + 8 * s, phase, a.err)) break;
-        const uint32_t flags = tags[s].flags;
-        if (__builtin_expect(flags & kTagFirst, 0)) load_queries(tags[s].seq);
+        const uint32_t partial = tags[s].partial;
         const unsigned char* tile = keys0 + s * stage_bytes;
         scores(tile, p, vsz);
-        if (__builtin_expect(flags & kTagPartial, 0)) {
+        if (__builtin_expect(partial, 0)) {
             // keys that do not count: scores of -inf, scales of 0
             const Tag tag = tags[s];
             auto valid = [&](int key) {
                 const int at = rank * KEYS + key;
                 if (at >= tag.rows) return false;
                 if (tag.bad < 0) return true;
-                const int32_t id = __ldg(a.table + (int64_t)tag.seq * a.max_blocks +
+                const int32_t id = __ldg(a.table + (int64_t)seq * a.max_blocks +
                                          (tag.bad + at) / a.block_size);
                 return id >= 0 && id < a.num_blocks;
             };
@@ -819,8 +819,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
                     vw[y][i][0] = *reinterpret_cast<const uint32_t*>(vr);
                 }
             }
-        const bool ends = flags & kTagLast;
-        const int seq = ends ? tags[s].seq : 0;  // (before the stage is given back)
+        const bool ends = k + 1 == next;
         __syncwarp();
         if (lane == 0) arrive(empty_bar + 8 * s);
         float smax = 0.f;
