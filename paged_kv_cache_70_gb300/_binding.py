@@ -608,7 +608,10 @@ def paged_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, src: torch.T
         raise ValueError("shape mismatch")
     if k_cache.dtype == torch.uint8:  # a 4-bit page, moved as one row of 16-bit words
         q4_geom_of(k_cache, k_cache.shape[1])
-        g = Geom(1, 1, k_cache[0].numel() // 2 if len(k_cache) else 1, 1, len(k_cache), PKV_BF16)
+        words = k_cache[0].numel() // 2 if len(k_cache) else 1
+        if words > 2**31 - 1:
+            raise ValueError("a page holds 2^31 16-bit words at most")
+        g = Geom(1, 1, words, 1, len(k_cache), PKV_BF16)
     else:
         g = geom_of(k_cache, k_cache.shape[2])
     with torch.cuda.device(k_cache.device):

@@ -24,8 +24,8 @@
 // sequence but their order, which bounds few sequences: those take narrower slices and
 // more tokens per round (launch_typed).
 // Measured: half of the tokens of 8 contexts of 16 K - 41 K (bf16, 8 heads, d = 128,
-// 970.7 MB read and written) 187 us, 5180 GB/s (0.76 of the measured copy rate; the longest
-// sequence ends last); 64 contexts up to 4 K 98 us, 5630 GB/s; one of 41 K 48 us.
+// 970.7 MB read and written) 185.5 us, 5230 GB/s (0.77 of the measured copy rate; the longest
+// sequence ends last); 64 contexts up to 4 K 98 us, 5620 GB/s; one of 41 K 48 us.
 #include <algorithm>
 #include <atomic>
 
@@ -287,7 +287,7 @@ cudaError_t launch_shaped(int device, int64_t mean, int32_t batch, CompactArgs& 
 }
 
 // Lists of up to 32 tokens on average take the small CTAs: the accepted tokens of 64
-// drafts take 3.5 us (bf16) against 3.8.  Longer ones take the most tokens per round
+// drafts took 3.5 us (bf16) against 3.8 (3.0 now).  Longer ones take the most tokens per round
 // whose CTAs are all resident at once, or, of 256 per round, in two turns.  Half of the
 // tokens of 1, 2, 4, 5, 6 and 8 contexts of 8 K - 40 K (bf16, 8 heads, d = 128), us:
 //   OneList 48, 65, - | TwoLists 69, 58, 96 | FewLists 73, 73, 88, 129, 144, 173

@@ -50,14 +50,14 @@
 //    page holds there.  Every wait is time-limited.
 //
 // Measured (bf16 queries, device time of split and combine; of the measured copy rate):
-//   8 sequences of 16 K - 41 K keys, 16 / 8 heads, d = 128, 303 MB   53.1 us  0.84
-//   the same with 32 / 8 heads 64.4 us (issue slots), 64 / 8 heads 95.9
-//   64 sequences of 128 - 4096 keys, 16 / 8 heads, B = 16, 173 MB    37.8 us  0.68
-//   8 x 16 K - 41 K keys, 16 / 8 heads, d = 64, 152 MB               41.7 us
-//   one of 7777 keys, 32 / 4 heads, d = 64                            9.4 us
-//   fp32 queries, 8 x 8 K - 20 K keys, 16 / 8 heads, d = 128         46.1 us
-// 7 to 8 us of each are two launches, the plan, the first tile and the combine; the
-// long contexts' split alone issues in half of its cycles (profile: 50 %).
+//   8 sequences of 16 K - 41 K keys, 16 / 8 heads, d = 128, 303 MB   52.9 us  0.85
+//   the same with 32 / 8 heads 63.4 us (issue slots), 64 / 8 heads 90.7
+//   64 sequences of 128 - 4096 keys, 16 / 8 heads, B = 16, 173 MB    37.1 us  0.69
+//   8 x 16 K - 41 K keys, 16 / 8 heads, d = 64, 152 MB               39.9 us
+//   one of 7777 keys, 32 / 4 heads, d = 64                            8.8 us
+//   fp32 queries, 8 x 8 K - 20 K keys, 16 / 8 heads, d = 128         45.0 us
+// 7 us of each are two launches, the plan, the first tile and the combine; the long
+// contexts' split alone issues in half of its cycles (profile: 52 %).
 #include <cuda_fp16.h>
 
 #include <algorithm>
