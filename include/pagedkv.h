@@ -581,8 +581,8 @@ int paged_decode_q4(const void* q, int32_t q_dtype, const void* k_cache, const v
  * starts at 0 and ends at total_keep, the length of keep.  seqlens_out [batch] (may be
  * NULL) receives start[b] + (number kept), for the next decode; it may be the
  * lengths' own array (no lengths are read), or `start` itself (which then moves
- * on in place), but may overlap no input otherwise.  The two pools may not
- * overlap.
+ * on in place: with one call per layer, in the last one only), but may overlap
+ * no input otherwise.  The two pools may not overlap.
  * Rows at and behind the new end keep their old contents.  The pages written
  * must belong to one sequence only (copy shared ones first, paged_copy_blocks).
  * An entry below start[b] + i or past the table sets PKV_FLAG_BAD_LENGTH, and a

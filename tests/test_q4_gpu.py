@@ -230,6 +230,34 @@ def test_decode_scales(scale):
     check(out, want, tol)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("at", [0, 100, 299])
+def test_decode_with_a_large_value_that_no_query_looks_at(dtype, at):
+    """A V row 4096 times the others' with a weight near zero: the others keep the
+    precision that the tolerance gives them (fp16 holds weights times scales above 2^-14
+    of the largest scale in full, and the smaller ones to 2^-25 of it)."""
+    rng = np.random.default_rng(at + 1)
+    n, d, block = 300, 128, 16
+    table, total = pages(rng, [n], block)
+    q = bf16(rng.standard_normal((1, 2, d)))
+    q[0, 1] = q[0, 0]
+    qv = Q.bf16_value(q)[0, 0].astype(np.float32)
+    x = [rng.standard_normal((n, 1, d)).astype(np.float32) for _ in range(2)]
+    x[0][at, 0] = -5 * qv
+    x[1][at, 0] *= 4096
+    kc, vc = (np.full((total, 1, block, 80), 0xFF, np.uint8) for _ in range(2))
+    pos = np.arange(n)
+    for pool, rows in ((kc, x[0]), (vc, x[1])):
+        pool[table[0, pos // block], :, pos % block] = Q.quantise(rows)
+    if dtype == "f32":
+        q = Q.bf16_value(q).astype(np.float32)
+    out = pkv.paged_decode_q4(to_dev(q), to_dev(kc), to_dev(vc), to_dev(table),
+                              to_dev(np.asarray([n], np.int32)))
+    want, tol = Q.decode(q, kc, vc, table, [n], d ** -0.5)
+    assert np.abs(want).max() < 1  # (the large row is not in it)
+    check(out, want, tol)
+
+
 def test_decode_bad_lengths_and_pages():
     lens = [100, 40, 64]
     block = 16
