@@ -78,9 +78,11 @@ def decode(q, kc, vc, table, lens, scale, skip=None):
 
     Tolerance, per output value, with p the softmax weights:
       output rounding              r |out|            r = 2^-8 (bf16), 2^-24 (fp32)
-      weights rounded to bf16      2^-8 sum p |s (u - 8)|   (bf16 q; fp32 q: 2^-22)
-      scores: fp32 sums of d products of q with 128 + u (bf16 q; |.| <= 143) and
-      the start -136 sum q, each term rounded or cut (2^-23), 48 terms a group:
+      weights rounded to 8 bits or more  2^-8 sum p |s (u - 8)|   (the kernel keeps 11 with
+      bf16 q; fp32 q: 2^-22)
+      scores: fp32 sums of d products of q with whole numbers of at most 280 (the
+      kernel's codes, two to a byte, and their offset stay below), each term rounded or
+      cut (2^-23), 48 terms a group:
         e = 48 2^-23 280 sum_g s_g |q|_1,g + (2 d) 2^-23 sum |q| |k|,
       which moves every weight by a factor exp(2 scale e) at most
       exponential, sums and merges 2^-15 sum p |v| (fp32 q: 2^-19): thousands of
