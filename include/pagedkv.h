@@ -553,9 +553,10 @@ int paged_kv_read_q4(const void* k_cache, const void* v_cache, const int32_t* sl
  * Rounding: with bf16 queries each weight is multiplied by its V scale and
  * rounded to fp16 (11 bits; those below 2^-14 of the largest to 2^-25 of it),
  * below the output's own rounding; with fp32 queries, queries and weights keep
- * 22 bits or more.  Values of V past 1e33 in magnitude may give infinities; scales of
- * V count to 2^-85 absolutely, so that groups of V that span less lose them.  A NaN
- * or infinite query, or a NaN key, makes its own heads' output NaN.
+ * 22 bits or more.  V may have any finite size; its scales count to 2^-85 absolutely,
+ * so that groups of V that span less lose them, and so do those that span 2^-25 of
+ * the largest scale among the values that are attended to.  A NaN or infinite query,
+ * or a NaN key, makes its own heads' output NaN.
  * workspace: paged_decode_q4_workspace_size(batch, q_dtype, geom) bytes, 256-byte
  * aligned, contents irrelevant on entry, as for paged_decode; it must not be used
  * by another call that runs concurrently.  A length below 0 or past the table

@@ -33,11 +33,13 @@
 //    that nothing large is carried through a long sum.  With fp32 queries 8 is taken
 //    off the operand instead (exactly), and queries and weights enter as two fp16
 //    parts (22 bits), two products each.
-//  * Weights are rounded to fp16 after the V scale is multiplied in, relative to a
-//    reference that includes log2 of the largest V scale (2^-11 at most, below the
-//    2^-8 of the bf16 output); the offsets' part sum p z and all sums stay fp32.
-//  * Reference maximum: lags.  State and output are rescaled only when a score or a
-//    V scale exceeds the reference by more than grow_by() or scale_grow() (one vote
+//  * Weights are rounded to fp16 after the V scale is multiplied in, relative to the
+//    largest V scale (2^-11 at most, below the 2^-8 of the bf16 output).  That scale is
+//    a reference of the codes' sums alone: the weights themselves, their sum and the
+//    offsets' sum p z are fp32 and relative to the maximum score only, so that neither
+//    scales of 0 nor scales far apart reach them.
+//  * Both references lag.  State and output are rescaled only when a score or a
+//    V scale exceeds its reference by more than grow_by() or scale_grow() (one vote
 //    per tile).
 //  * Work split: the tiles of all sequences in one list, cut into equal contiguous
 //    shares, one per CTA; each (CTA, sequence) piece leaves a partial state that a
@@ -73,10 +75,13 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kHold = 16;         // 16-key products between additions of the offsets' sums
-// The reference moves when a score passes it by 2^grow_by() or a V scale its bound by
-// 2^scale_grow(): weights stay below 2^12 (bf16 queries; fp16 holds 11 bits of those
-// down to 2^-14), or, moved up by 2^bias(), below 2^15 (fp32 queries, whose second
-// part then has its bits for weights down to 2^-14 of the largest).
+// A weight is 2^(score - maximum - kDown): sums of 2^31 keys' weights times any finite
+// offset stay finite, and offsets down to 2^-78 keep their bits.  The references move
+// when a score passes the maximum by 2^grow_by() or a V scale its bound by
+// 2^scale_grow(): fp16 weights stay below 2^12 (bf16 queries; fp16 holds 11 bits of
+// those down to 2^-14), or, moved up by 2^bias(), below 2^15 (fp32 queries, whose
+// second part then has its bits for weights down to 2^-14 of the largest).
+constexpr float kDown = 40.f;
 template <bool F32>
 __host__ __device__ constexpr float grow_by() { return F32 ? 2.f : 8.f; }
 template <bool F32>
@@ -509,8 +514,11 @@ q4_split_kernel(const Q4DecodeArgs a) {
     constexpr int OT = PAIR ? NG : 2 * NG;  // output tiles of 16 rows
     float o[OT][4], ct[NT][4], zacc[NT], l[NP];
     // reference of the queries' weights, the same with -inf as 0, and the score
-    // that makes it move; log2 of the V scale it counts with, and their limit
-    float m[NP], mr[NP], lim[NP], sref = 0.f, slim = 0.f;
+    // that makes it move; the V scale that makes the scales' reference move, and what
+    // weights are multiplied by before their V scale (a power of two, like the former)
+    float m[NP], mr[NP], lim[NP], slim = 0.f, wmul = 0.f;
+    auto inverse = [](float x) { return __uint_as_float((254u << 23) - __float_as_uint(x)); };
+    auto weight_scale = [&]() { return inverse(slim) * exp2f(kDown + bias<F32>() + scale_grow<F32>()); };
     auto settle = [&]() {
 #pragma unroll
         for (int i = 0; i < OT; ++i)
@@ -532,8 +540,8 @@ q4_split_kernel(const Q4DecodeArgs a) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) ct[j][e] = 0.f;
         }
-        sref = -60.f;
-        slim = 0.f;
+        slim = exp2f(scale_grow<F32>() - 60.f);
+        wmul = weight_scale();
 #pragma unroll
         for (int i = 0; i < NP; ++i) {
             m[i] = lim[i] = -INFINITY;
@@ -841,11 +849,13 @@ q4_split_kernel(const Q4DecodeArgs a) {
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1)
                 smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, off));
-            // the least power of two above the scales so far, 2^-60 .. 2^100
-            const int se = min(max((int)(__float_as_uint(smax) >> 23) - 126, -60), 100);
-            const float sold = sref;
-            sref = fmaxf(sref, (float)se);
-            slim = exp2f(sref + scale_grow<F32>());
+            // the least power of two above the scales so far, 2^-60 at least
+            constexpr int kGrow = (int)scale_grow<F32>();
+            const int se = min(max((int)(__float_as_uint(smax) >> 23) - 126, -60), 126 - kGrow);
+            const float was = slim;
+            slim = fmaxf(slim, __uint_as_float((uint32_t)(se + kGrow + 127) << 23));
+            wmul = weight_scale();
+            const float fs = was * inverse(slim);
             float f[NP];
 #pragma unroll
             for (int i = 0; i < NP; ++i) {
@@ -857,11 +867,11 @@ q4_split_kernel(const Q4DecodeArgs a) {
 #pragma unroll
                 for (int off = QN == 8 ? 4 : 2; off < 32; off <<= 1)
                     mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                const float mn = fmaxf(m[i] - sold + bias<F32>(), mx) + sref - bias<F32>();
+                const float mn = fmaxf(m[i], mx + kDown);
                 f[i] = m[i] == -INFINITY ? 0.f : ex2(m[i] - mn);
                 m[i] = mn;
                 mr[i] = mn == -INFINITY ? 0.f : mn;
-                lim[i] = mn - sref + bias<F32>() + grow_by<F32>();
+                lim[i] = mn - kDown + grow_by<F32>();
                 l[i] *= f[i];
             }
             // factors of this lane's columns 2c, 2c + 1 and of column r
@@ -878,8 +888,11 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 fr = (my_q & 1) ? x1 : x0;
             }
 #pragma unroll
+            for (int j = 0; j < NT; ++j) zacc[j] *= fr;
+            f0 *= fs;
+            f1 *= fs;
+#pragma unroll
             for (int j = 0; j < NT; ++j) {
-                zacc[j] *= fr;
                 ct[j][0] *= f0;
                 ct[j][1] *= f1;
                 ct[j][2] *= f0;
@@ -916,6 +929,9 @@ q4_split_kernel(const Q4DecodeArgs a) {
                     w[i] = (my_q & 1) ? x1 : x0;
                 }
             }
+            float wm[4];  // for the codes
+#pragma unroll
+            for (int i = 0; i < 4; ++i) wm[i] = w[i] * wmul;
             // columns: a word per key (its weight in this column's half), or per two
             // keys
             constexpr int PW = PAIR ? 4 : 2;
@@ -925,7 +941,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 float ws[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    ws[i] = w[i] * bf16lo(vsz[y][j][i]);
+                    ws[i] = wm[i] * bf16lo(vsz[y][j][i]);
                     zacc[j] = fmaf(w[i], bf16hi(vsz[y][j][i]), zacc[j]);
                 }
                 if constexpr (PAIR) {
@@ -1027,7 +1043,7 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 if (g >= NG || gi != 2 * c / QN) continue;
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float u = 1.f / code_unit<F32>() / (e & 1 ? 16.f : 1.f);
+                    const float u = inverse(wmul) / code_unit<F32>() / (e & 1 ? 16.f : 1.f);
                     const float* x = o[(PAIR ? g >> 1 : g) * 2 + (e >> 1)] + 2 * (e & 1);
                     const bool mixed = !F32 && (e & 1);  // holds its even neighbour too
                     val[j][0][e] = fmaf(x[0] - (mixed ? x[-2] : 0.f), u, z0);
