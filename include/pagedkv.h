@@ -550,9 +550,10 @@ int paged_kv_read_q4(const void* k_cache, const void* v_cache, const int32_t* sl
  * Supported: any Hq / Hkv up to 64; head_dim 128 with any block_size, 64 with an
  * even one; batch <= 4096; max_blocks_per_seq * block_size up to 2^31 - 4097, and
  * below 2^34 for the whole batch.
- * Rounding: with bf16 queries each weight is multiplied by its V scale and
- * rounded to fp16 (11 bits; those below 2^-14 of the largest to 2^-25 of it),
- * below the output's own rounding; with fp32 queries, queries and weights keep
+ * Rounding: bf16 queries enter the scores exactly (products of those below 2^-7 of
+ * the largest are cut at 2^-14 of it, per unit of code); each weight is multiplied by its
+ * V scale and rounded to fp16 (11 bits; those below 2^-14 of the largest to 2^-25 of
+ * it), below the output's own rounding.  With fp32 queries, queries and weights keep
  * 22 bits or more.  V may have any finite size; its scales count to 2^-85 absolutely,
  * so that groups of V that span less lose them, and so do those that span 2^-25 of
  * the largest scale among the values that are attended to.  A NaN or infinite query,

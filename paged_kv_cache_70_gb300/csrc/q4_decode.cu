@@ -182,16 +182,18 @@ __device__ __forceinline__ void mma_from(float* d, const uint32_t* a, uint32_t b
 
 // Codes 2i and 2i + 1 of both halves of x as operands, in units of code_unit().
 //  * bf16 queries: a code in the low bits of an fp16's mantissa is a subnormal, so
-//    fields of the word are operands as they are.  `low` is code 2i, u0, and
-//    `both` the byte of the two, u0 + 16 u1: two logic operations per pair of codes,
-//    no shift (the upper bytes come by a permutation).  The other operand or the
-//    result takes u1 out again: q0 u0 + q1 u1 = (q0 - q1 / 16) u0 + (q1 / 16) both.
+//    fields of the word are operands as they are, without a shift (the upper bytes
+//    come by a permutation): u0 and 16 u1 for the scores (score_pair), whose other
+//    operands, q0 and q1 / 16, are exact; u0 and the byte of the two, u0 + 16 u1, for
+//    the output (code_pair), one logic operation less for half of the pairs: there
+//    both meet the same weights and the result takes u0 out again.
 //    The products are aligned by the operands' exponent fields, which overstate a
 //    subnormal by up to 2^10, and cut 25 bits below the largest: about 2^-15 of the
-//    largest weight, under the 2^-11 that the weights' own rounding leaves.
+//    largest weight, under the 2^-11 that the weights' own rounding leaves, and 2^-15
+//    of the largest query for queries whose last bit is below that.
 //  * EXACT (fp32 queries): 1024 + u, then minus 1024 + 8, gives the normal number
-//    u0 - 8, and 1024 + 16 u, minus 1024 + 128, 16 (u1 - 8) for `both`; the second
-//    parts of queries and weights keep their bits.
+//    u0 - 8, and 1024 + 16 u, minus 1024 + 128, 16 (u1 - 8); the second parts of
+//    queries and weights keep their bits.
 template <bool EXACT>
 __device__ __forceinline__ void code_pair(uint32_t x, int i, uint32_t& low, uint32_t& both) {
     if constexpr (EXACT) {
@@ -203,6 +205,16 @@ __device__ __forceinline__ void code_pair(uint32_t x, int i, uint32_t& low, uint
     } else {
         both = i ? __byte_perm(x, 0u, 0x4341) : x & 0x00FF00FFu;
         low = both & 0x000F000Fu;
+    }
+}
+template <bool EXACT>
+__device__ __forceinline__ void score_pair(uint32_t x, int i, uint32_t& low, uint32_t& high) {
+    if constexpr (EXACT) {
+        code_pair<true>(x, i, low, high);
+    } else {
+        const uint32_t y = i ? __byte_perm(x, 0u, 0x4341) : x;
+        low = y & 0x000F000Fu;
+        high = y & 0x00F000F0u;
     }
 }
 template <bool EXACT>
@@ -574,9 +586,9 @@ q4_split_kernel(const Q4DecodeArgs a) {
                 }
             }
         }
-        // the query scaled by a power of two to below 2^12: fp16 then holds
-        // bf16 queries exactly down to 2^-25 of the largest, and two parts
-        // hold 23 bits of fp32 ones
+        // the query scaled by a power of two to below 2^12: fp16 then holds bf16
+        // queries (and 1/16 of them) exactly down to 2^-24 of the largest, and two
+        // parts hold 23 bits of fp32 ones
         float mx = 0.f;
 #pragma unroll
         for (int j = 0; j < NT; ++j)
@@ -617,12 +629,8 @@ q4_split_kernel(const Q4DecodeArgs a) {
             qs[j][1] = __shfl_sync(0xffffffffu, sum, 8 * c + 4);
             start[j][0] = F32 ? 0.f : -8.f * qs[j][0];
             start[j][1] = F32 ? 0.f : -8.f * qs[j][1];
-            // (codes of odd dims count 16 times, and bring their even neighbours')
 #pragma unroll
-            for (int e = 0; e < 8; e += 2) {
-                x[e + 1] *= 0.0625f;
-                if constexpr (!F32) x[e] -= x[e + 1];
-            }
+            for (int e = 1; e < 8; e += 2) x[e] *= 0.0625f;  // (codes of odd dims count 16 times)
             if constexpr (PAIR) {
                 // word (unit u of 2, pair of groups gp): dims 4u .. 4u + 3 of the
                 // chunk, k-step e / 2, word e % 2
@@ -706,8 +714,8 @@ q4_split_kernel(const Q4DecodeArgs a) {
 #pragma unroll
                 for (int st = 0; st < 2; ++st) {
                     uint32_t af[4];
-                    code_pair<F32>(x[0], st, af[0], af[2]);
-                    code_pair<F32>(x[1], st, af[1], af[3]);
+                    score_pair<F32>(x[0], st, af[0], af[2]);
+                    score_pair<F32>(x[1], st, af[1], af[3]);
 #pragma unroll
                     for (int part = 0; part < PARTS; ++part) {
                         const uint32_t b0 = qf[part][w][2 * st], b1 = qf[part][w][2 * st + 1];
