@@ -504,7 +504,8 @@ int paged_copy_blocks(void* k_cache, void* v_cache, const int32_t* src, const in
  *          groups of 32 dims a scale s and an offset z, both bf16 (s first).
  *          The 16-bit unit r * NG + g of the codes (r < 8, little-endian) holds
  *          the 4-bit codes u of dims 32 g + 4 r .. 32 g + 4 r + 3, lowest bits
- *          first.  The value of code u in group g is s_g * (u - 8) + z_g.
+ *          first.  The value of code u in group g is s_g * (u - 8) + z_g; s_g may have
+ *          either sign (paged_kv_write_q4 stores none below 0).
  * A page is copied by paged_copy_blocks with a geom whose pages have the same
  * number of bytes (e.g. one head, block_size 1, head_dim Hkv * B * R / 2, bf16).
  */

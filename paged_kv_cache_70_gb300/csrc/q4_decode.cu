@@ -846,7 +846,8 @@ q4_split_kernel(const Q4DecodeArgs a) {
             for (int j = 0; j < NT; ++j)
 #pragma unroll
                 for (int i = 0; i < 4; i += 2)
-                    smax = fmax3(smax, bf16lo(vsz[y][j][i]), bf16lo(vsz[y][j][i + 1]));
+                    smax = fmax3(smax, fabsf(bf16lo(vsz[y][j][i])),  // (of either sign)
+                                 fabsf(bf16lo(vsz[y][j][i + 1])));
 #pragma unroll
             for (int h = 0; h < NV; ++h)
 #pragma unroll

@@ -4,6 +4,7 @@ import pytest
 
 import paged_kv_cache_70_gb300 as pkv
 import q4_bounds as B
+import q4_oracle as Q
 from gpu_helpers import to_dev, widen
 from test_q4_bounds import competing
 
@@ -28,3 +29,24 @@ def check(q, kc, vc, table, lens, scale):
 def test_few_keys_with_large_scores(hq, hkv, d, outliers):
     case = competing(hq, hkv, d, 48, 3, 5, outliers)
     check(*case, scale=3.0)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 128), (8, 2, 128), (16, 2, 64), (4, 2, 64)])
+@pytest.mark.parametrize("share", [1.0, 0.5])
+def test_scales_of_either_sign(dtype, hq, hkv, d, share):
+    """Rows of another writer: the scales of some groups of K and V below 0."""
+    rng = np.random.default_rng(d + hq)
+    n, block = 300, 16
+    lens = [n, 77]
+    q = rng.standard_normal((2, hq, d)).astype(np.float32)
+    q = Q.bf16_bits(q) if dtype == "bf16" else q
+    table = np.arange(2 * 19, dtype=np.int32).reshape(2, 19)
+    pools = []
+    for _ in range(2):
+        rows = Q.quantise(rng.standard_normal((38, hkv, block, d)).astype(np.float32))
+        sz = rows[..., d // 2:].copy().view(np.uint16)
+        sz[..., 0::2] |= np.where(rng.random(sz[..., 0::2].shape) < share, 0x8000, 0).astype(np.uint16)
+        rows[..., d // 2:] = sz.view(np.uint8)
+        pools.append(rows)
+    check(q, *pools, table, lens, d ** -0.5)
