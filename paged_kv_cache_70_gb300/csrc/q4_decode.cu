@@ -364,13 +364,9 @@ q4_split_kernel(const Q4DecodeArgs a) {
         __syncthreads();
     }
     const int32_t total = tstart[a.batch];
-    // (the combine, let start here, reads the tile starts before it waits)
-    if (first_cta) {
-        for (int b = tid; b <= a.batch; b += blockDim.x) a.tstart[b] = tstart[b];
-        __threadfence();
-        __syncthreads();
-    }
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (first_cta)  // for the combine, which reads them behind its wait
+        for (int b = tid; b <= a.batch; b += blockDim.x) a.tstart[b] = tstart[b];
     const int32_t len = share_len(total, a.batch, gridDim.x);
     const int32_t t0 = share_first(tstart, a.batch, (int64_t)blockIdx.x * len);
     const int32_t t1 = share_first(tstart, a.batch, (int64_t)(blockIdx.x + 1) * len);
@@ -1167,13 +1163,12 @@ __global__ void __launch_bounds__(kCombineMost * 32) q4_combine_kernel(const Q4C
     const int64_t id = (int64_t)blockIdx.x * per_cta + warp / a.w;
     const bool live = id < (int64_t)a.batch * a.hq;
     const int b = live ? (int)(id / a.hq) : 0, h = live ? (int)(id % a.hq) : 0;
-    // The tile starts: stored and fenced by the split's first block before it lets
-    // this kernel start, which therefore needs not wait for them.
+    // everything that the split stores is visible behind this wait only, its tile starts too
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int32_t ta = __ldcg(a.tstart + b), tb = __ldcg(a.tstart + b + 1);
     const int32_t len = share_len(__ldcg(a.tstart + a.batch), a.batch, a.ctas);
     const int c0 = (ta + b + 1) / len, c1 = tb > ta && live ? (tb + b) / len : c0 - 1;
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     float M = -INFINITY, L = 0.f, acc[E];
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;

@@ -1,6 +1,7 @@
 """The 4-bit decode against bounds from the roundings it makes (q4_bounds)."""
 import numpy as np
 import pytest
+import torch
 
 import paged_kv_cache_70_gb300 as pkv
 import q4_bounds as B
@@ -50,3 +51,24 @@ def test_scales_of_either_sign(dtype, hq, hkv, d, share):
         rows[..., d // 2:] = sz.view(np.uint8)
         pools.append(rows)
     check(q, *pools, table, lens, d ** -0.5)
+
+
+def test_one_workspace_in_calls_with_other_tile_starts():
+    """Calls back to back whose plans differ, in one workspace: each has its own bits."""
+    rng = np.random.default_rng(3)
+    hq, hkv, d, block = 16, 8, 128, 16
+    pool = Q.quantise(rng.standard_normal((400, hkv, block, d)).astype(np.float32))
+    kd = to_dev(pool)
+    calls, ws = [], None
+    for lens in ([3000, 20, 1], [7, 7, 7], [0, 2500, 900], [64, 0, 0]):
+        table = rng.integers(0, 400, (3, 190)).astype(np.int32)
+        q = torch.randn(3, hq, d, device="cuda", dtype=torch.bfloat16)
+        args = q, kd, kd, to_dev(table), to_dev(np.asarray(lens, np.int32))
+        if ws is None:
+            ws = torch.empty(pkv.paged_decode_q4_workspace_size(3, hq, torch.bfloat16, kd),
+                             dtype=torch.uint8, device="cuda")
+        calls.append((args, pkv.paged_decode_q4(*args)))
+    torch.cuda.synchronize()
+    outs = [(want, pkv.paged_decode_q4(*args, workspace=ws))
+            for _ in range(100) for args, want in calls]
+    assert all(torch.equal(a, b) for a, b in outs)
