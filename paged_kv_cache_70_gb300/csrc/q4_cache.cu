@@ -287,21 +287,31 @@ q4_read_kernel(const unsigned char* __restrict__ kc, const unsigned char* __rest
         for (int u = 0; u < U; ++u) {
             const int vec = v0 + 32 * u + lane;
             const uint32_t w = words_to_units<NG>(words[u], lane, (vec / 4) % NG);
-            const float s = bf16lo(sz[u]), z = bf16hi(sz[u]);
-            float x[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i)  // u - 8 times s is exact: one rounding
-                x[i] = fmaf((float)((w >> (4 * i)) & 15u) - 8.f, s, z);
             if (vec >= vecs) continue;
             const int64_t e = e0 + (int64_t)vec * 8;
+            // one fused multiply and add of the output's own type: one rounding
             if constexpr (F32) {
+                const float s = bf16lo(sz[u]), z = bf16hi(sz[u]);
+                float x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+                    x[i] = fmaf((float)((w >> (4 * i)) & 15u) - 8.f, s, z);
                 float4* o = reinterpret_cast<float4*>(static_cast<float*>(dst) + e);
                 o[0] = make_float4(x[0], x[1], x[2], x[3]);
                 o[1] = make_float4(x[4], x[5], x[6], x[7]);
             } else {
+                const uint32_t ss = __byte_perm(sz[u], 0u, 0x1010), zz = __byte_perm(sz[u], 0u, 0x3232);
+                uint32_t x[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    // bf16 128 + u of the byte's two codes, minus 136
+                    const uint32_t y = w >> (8 * i);
+                    x[i] = (y & 0xFu) | ((y << 12) & 0xF0000u) | 0x43004300u;
+                    asm("sub.rn.bf16x2 %0, %0, %1;" : "+r"(x[i]) : "r"(0x43084308u));
+                    asm("fma.rn.bf16x2 %0, %0, %1, %2;" : "+r"(x[i]) : "r"(ss), "r"(zz));
+                }
                 *reinterpret_cast<uint4*>(static_cast<uint16_t*>(dst) + e) =
-                    make_uint4(pack_bf16x2(x[0], x[1]), pack_bf16x2(x[2], x[3]),
-                               pack_bf16x2(x[4], x[5]), pack_bf16x2(x[6], x[7]));
+                    make_uint4(x[0], x[1], x[2], x[3]);
             }
         }
     }

@@ -72,3 +72,26 @@ def test_one_workspace_in_calls_with_other_tile_starts():
     outs = [(want, pkv.paged_decode_q4(*args, workspace=ws))
             for _ in range(100) for args, want in calls]
     assert all(torch.equal(a, b) for a, b in outs)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+def test_read_rounds_once(d):
+    """Rows whose value lies beside the middle of two bf16 neighbours, nearer to it than
+    fp32 can tell: scale 129/128 or 131/128, codes 3 or 5 off 8, offsets of 2^-30."""
+    s, u, sign = np.meshgrid([0x3F81, 0x3F83], [11, 5, 13, 3], [1, -1], indexing="ij")
+    s, u, sign = (x.reshape(-1) for x in (s, u, sign))
+    rows = np.zeros((len(s), 1, 5 * d // 8), np.uint8)
+    rows[..., :d // 2] = (u * 17)[:, None, None]
+    sz = np.stack((s, Q.bf16_bits(sign * np.float32(2.0 ** -30))), -1).astype(np.uint16)
+    rows[..., d // 2:] = np.tile(sz, (1, d // 32)).view(np.uint8)[:, None]
+    pool = rows.reshape(1, 1, len(s), -1)
+    k, v = pkv.paged_kv_read_q4(to_dev(pool), to_dev(pool),
+                                to_dev(np.arange(len(s), dtype=np.int32)), torch.bfloat16)
+    x = Q.values(rows)
+    # the neighbours of 8 significant bits, and the nearer of the two
+    step = np.exp2(np.floor(np.log2(np.abs(x))) - 7)
+    lo = np.floor(x / step) * step
+    want = np.where(x - lo < lo + step - x, lo, lo + step)
+    middle = (Q.values(rows).astype(np.float32) - lo) / step == 0.5
+    assert middle.sum() >= 4 * d  # (fp32 sees these in the middle)
+    assert np.array_equal(widen(k), want) and np.array_equal(widen(v), want)
