@@ -7,7 +7,8 @@ import paged_kv_cache_70_gb300 as pkv
 import q4_bounds as B
 import q4_oracle as Q
 from gpu_helpers import to_dev, widen
-from test_q4_bounds import competing
+from test_q4_bounds import competing, long_case
+from test_q4_gpu import DECODE, decode_case
 
 pytestmark = pytest.mark.gpu
 
@@ -22,6 +23,27 @@ def check(q, kc, vc, table, lens, scale):
     mean = lambda x: np.sqrt(np.mean(x ** 2))
     assert mean(err) <= mean(rms), f"{mean(err) / mean(rms):.3g} of the mean bound"
     assert pkv.paged_error_flags() == 0
+
+
+@pytest.mark.parametrize("i", range(len(DECODE)))
+def test_lengths_and_heads(i):
+    lens, hq, hkv, d, block, dtype = DECODE[i]
+    q, kc, vc, table = decode_case(lens, hq, hkv, d, block, dtype, 100 + i)
+    check(q, kc, vc, table, lens, d ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [300, 9000, 12345, 20000])
+@pytest.mark.parametrize("d", [64, 128])
+def test_long_contexts(dtype, n, d):
+    check(*long_case(dtype, n, d, n), scale=d ** -0.5)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [0.0, 0.5, -0.3, 3.0])
+def test_flat_and_peaked_weights(dtype, scale):
+    q, kc, vc, table = decode_case([700, 45], 8, 4, 128, 16, dtype, 7)
+    check(q, kc, vc, table, [700, 45], scale)
 
 
 @pytest.mark.parametrize("hq,hkv,d", [(4, 2, 128), (8, 2, 128), (16, 2, 128), (4, 2, 64), (8, 2, 64),

@@ -53,3 +53,70 @@ def test_differences_of_queries_in_fp16_are_rejected(hq, hkv, d, outliers):
     want, tol, _ = B.decode(*case, 3.0)
     assert not B.rejects(scores_of_differences(*case, 3.0, True), want, tol)
     assert B.rejects(scores_of_differences(*case, 3.0, False), want, tol)
+
+
+def long_case(dtype, n, d, seed):
+    """One sequence of n keys as the decode tests make them."""
+    rng = np.random.default_rng(seed)
+    block = 256
+    blocks = -(-n // block)
+    k, v = (rng.standard_normal((blocks, 1, block, d)).astype(np.float32) for _ in range(2))
+    for x in (k, v):
+        x[..., 3::29] *= 4
+    q = rng.standard_normal((1, 2, d)).astype(np.float32)
+    table = np.arange(blocks, dtype=np.int32)[None]
+    return Q.bf16_bits(q) if dtype == "bf16" else q, Q.quantise(k), Q.quantise(v), table, [n]
+
+
+def without(case, dropped, scale):
+    """The output with some positions left out."""
+    return Q.decode(*case, scale, [dropped])[0]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [12345, 20000])
+def test_lost_keys_are_rejected_at_long_contexts(dtype, n):
+    case = long_case(dtype, n, 128, n)
+    scale = 128 ** -0.5
+    want, tol, _ = B.decode(*case, scale)
+    assert np.allclose(want, Q.decode(*case, scale)[0], rtol=1e-12, atol=1e-15)
+    for got in (np.zeros_like(want),                                  # nothing
+                without(case, range(n * 7 // 10, n), scale),          # the last pieces
+                without(case, range(n // 2 // 32 * 32, n // 2 // 32 * 32 + 32), scale)):  # a tile
+        assert np.mean(np.abs(got - want) > tol) > 0.5
+    assert B.rejects(without(case, [n - 1], scale), want, tol)        # the last key
+
+
+@pytest.mark.parametrize("n", [300, 9000])
+def test_coarser_queries_and_weights_are_rejected(n):
+    """fp32 queries held in fp16 or bf16, their weights in fp16, and bf16 queries'
+    weights in bf16."""
+    case = long_case("f32", n, 128, n)
+    scale = 128 ** -0.5
+    want, tol, _ = B.decode(*case, scale)
+    q = case[0]
+    for coarse in (q.astype(np.float16).astype(np.float32), Q.bf16_value(Q.bf16_bits(q))):
+        assert B.rejects(Q.decode(coarse, *case[1:], scale)[0], want, tol)
+    assert B.rejects(coarse_weights(case, scale, lambda w: w.astype(np.float16)), want, tol)
+    case = long_case("bf16", n, 128, n)
+    want, tol, _ = B.decode(*case, scale)
+    half = coarse_weights(case, scale, lambda w: w.astype(np.float16))
+    assert not B.rejects(half, want, tol)
+    assert B.rejects(coarse_weights(case, scale, lambda w: Q.bf16_value(Q.bf16_bits(w))), want, tol)
+
+
+def coarse_weights(case, scale, cast):
+    """The output with the weights times V scales (relative to the largest) cast."""
+    q, kc, vc, table, lens = case
+    x = Q.bf16_value(q) if q.dtype == np.uint16 else q
+    at = np.arange(lens[0])
+    block = kc.shape[2]
+    k = Q.values(kc[table[0, at // block], 0, at % block])
+    u, s, z = Q.parts(vc[table[0, at // block], 0, at % block])
+    out = np.zeros(q.shape)
+    for h in range(q.shape[1]):
+        e = scale * (k @ x[0, h].astype(np.float64))
+        p = np.exp(e - e.max())
+        w = np.asarray(cast((p[:, None] * s / s.max()).astype(np.float32)), np.float64) * s.max()
+        out[0, h] = ((w * u).sum(0) + p @ z) / p.sum()
+    return out
