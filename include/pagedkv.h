@@ -523,7 +523,8 @@ int paged_copy_blocks(void* k_cache, void* v_cache, const int32_t* src, const in
  * at the ends of the range (2^-8 of |lo| + |hi|).  A group that holds a NaN or
  * an infinity, or spans more than fp32 holds, reads back as NaN.  Duplicate
  * slots, negative slots and slots past the pool as in paged_kv_write.  k, v and
- * the pools 16-byte aligned.
+ * the pools 16-byte aligned; num_kv_heads * head_dim up to 2^30, here and in
+ * paged_kv_read_q4 (PKV_ERR_UNSUPPORTED).
  */
 int paged_kv_write_q4(const void* k, const void* v, int32_t kv_dtype, const int32_t* slot_mapping,
                       int64_t num_tokens, void* k_cache, void* v_cache, const pkv_geom* geom,

@@ -28,6 +28,9 @@ int check_q4_geom(const pkv_geom* g) {
     return g->head_dim == 64 || g->head_dim == 128 ? PKV_OK : PKV_ERR_UNSUPPORTED;
 }
 
+// the write and the read count a token's row in 32 bits, 8 values at a time
+bool row_too_long(const pkv_geom* g) { return (int64_t)g->num_kv_heads * g->head_dim > (1 << 30); }
+
 // rows' worth of grid: one warp per token, 4 tokens per CTA
 constexpr int64_t kMaxTokens = (int64_t)4 * 0x7fffffff;
 
@@ -41,6 +44,7 @@ int paged_kv_write_q4(const void* k, const void* v, int32_t kv_dtype, const int3
     const int st = check_q4_geom(geom);
     if (st != PKV_OK) return st;
     if (!elt_size(kv_dtype) || num_tokens < 0 || num_tokens > kMaxTokens) return PKV_ERR_INVALID;
+    if (row_too_long(geom)) return PKV_ERR_UNSUPPORTED;
     if (num_tokens == 0) return PKV_OK;
     if (!k || !v || !slot_mapping || !k_cache || !v_cache) return PKV_ERR_INVALID;
     if (!aligned(k, 16) || !aligned(v, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16))
@@ -59,6 +63,7 @@ int paged_kv_read_q4(const void* k_cache, const void* v_cache, const int32_t* sl
     const int st = check_q4_geom(geom);
     if (st != PKV_OK) return st;
     if (!elt_size(kv_dtype) || num_tokens < 0 || num_tokens > kMaxTokens) return PKV_ERR_INVALID;
+    if (row_too_long(geom)) return PKV_ERR_UNSUPPORTED;
     if (num_tokens == 0) return PKV_OK;
     if (!k_out || !v_out || !slot_mapping || !k_cache || !v_cache) return PKV_ERR_INVALID;
     if (!aligned(k_out, 16) || !aligned(v_out, 16) || !aligned(k_cache, 16) ||
