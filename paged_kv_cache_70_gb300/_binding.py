@@ -705,6 +705,7 @@ except ImportError:  # pragma: no cover - a torch build without it
 
 _geoms: dict = {}
 _sizes: dict = {}
+_INT32 = 2**31 - 1
 
 
 def _geom(*key):
@@ -755,6 +756,8 @@ def _q4_shape(k_cache: torch.Tensor):
     if k_cache.dtype != torch.uint8 or k_cache.dim() != 4 or k_cache.shape[3] not in (40, 80):
         raise ValueError("a 4-bit pool is uint8 [num_blocks, Hkv, block_size, 5 * head_dim / 8]")
     nb, hkv, bs, r = k_cache.shape
+    if hkv > _INT32 or bs > _INT32:  # (ctypes would cut them off)
+        raise ValueError("num_kv_heads and block_size are 32-bit")
     return nb, hkv, bs, r * 8 // 5
 
 
@@ -840,6 +843,8 @@ def paged_decode_q4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
     rows, width = block_table.shape
     if d != dk or v_cache.shape != k_cache.shape or rows < batch or cache_seqlens.numel() < batch:
         raise ValueError("shape mismatch")
+    if max(batch, width) > _INT32:
+        raise ValueError("q and a table's row hold 2^31 - 1 entries at most")
     if out is None:
         out = torch.empty_like(q)
     elif out.shape != q.shape:
@@ -873,11 +878,15 @@ def paged_kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: 
             (start is not None and start.numel() < batch) or \
             (seqlens_out is not None and seqlens_out.numel() < batch):
         raise ValueError("shape mismatch")
+    if max(keep.numel(), batch, width) > _INT32:
+        raise ValueError("keep, cu_keep and a table's row hold 2^31 - 1 entries at most")
     if k_cache.dtype == torch.uint8:
         nb, hkv, bs, d = _q4_shape(k_cache)
         code = PKV_Q4
     else:
         nb, bs, hkv, d = k_cache.shape
+        if max(bs, hkv, d) > _INT32:
+            raise ValueError("block_size, num_kv_heads and head_dim are 32-bit")
         code = _dtype_code(k_cache)
     i32 = torch.int32
     load_library()
