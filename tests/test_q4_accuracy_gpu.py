@@ -117,3 +117,20 @@ def test_read_rounds_once(d):
     middle = (Q.values(rows).astype(np.float32) - lo) / step == 0.5
     assert middle.sum() >= 4 * d  # (fp32 sees these in the middle)
     assert np.array_equal(widen(k), want) and np.array_equal(widen(v), want)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 128), (8, 1, 64)])
+@pytest.mark.parametrize("size", [1e-30, 1e-15, 1e15, 1e30])
+def test_sizes_of_queries_and_keys(dtype, hq, hkv, d, size):
+    """Queries of any size over keys of the inverse: scores of the usual size."""
+    rng = np.random.default_rng(hq)
+    lens, block = [90, 33], 16
+    q = (rng.standard_normal((2, hq, d)) * size).astype(np.float32)
+    k, v = (rng.standard_normal((12, hkv, block, d)).astype(np.float32) for _ in range(2))
+    table = np.arange(12, dtype=np.int32).reshape(2, 6)
+    check(Q.bf16_bits(q) if dtype == "bf16" else q, Q.quantise((k / size).astype(np.float32)),
+          Q.quantise(v), table, lens, d ** -0.5)
+    # every product at its largest, of one sign
+    q[:], k[:] = size, 1 / size
+    check(Q.bf16_bits(q) if dtype == "bf16" else q, Q.quantise(k), Q.quantise(v), table, lens, d ** -1)
