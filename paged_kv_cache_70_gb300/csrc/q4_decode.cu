@@ -851,6 +851,17 @@ q4_split_kernel(const Q4DecodeArgs a) {
         }
         grow |= smax > slim;
         if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {  // move the reference to the running maximum
+            // (an infinite scale makes its own group NaN, and is no reference for the others)
+            smax = 0.f;
+#pragma unroll
+            for (int y = 0; y < KS; ++y)
+#pragma unroll
+                for (int j = 0; j < NT; ++j)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const float x = fabsf(bf16lo(vsz[y][j][i]));
+                        smax = fmaxf(smax, x < INFINITY ? x : 0.f);
+                    }
 #pragma unroll
             for (int off = 1; off < 32; off <<= 1)
                 smax = fmaxf(smax, __shfl_xor_sync(0xffffffffu, smax, off));

@@ -134,3 +134,26 @@ def test_sizes_of_queries_and_keys(dtype, hq, hkv, d, size):
     # every product at its largest, of one sign
     q[:], k[:] = size, 1 / size
     check(Q.bf16_bits(q) if dtype == "bf16" else q, Q.quantise(k), Q.quantise(v), table, lens, d ** -1)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 128), (8, 2, 128), (16, 2, 128), (4, 2, 64)])
+@pytest.mark.parametrize("bad", [np.inf, -np.inf, np.nan])
+def test_an_infinity_in_v_stays_in_its_group(dtype, hq, hkv, d, bad):
+    """One value of V that is no number: its 32 dims are NaN, the others as without it."""
+    rng = np.random.default_rng(d)
+    n, block = 500, 16
+    q = rng.standard_normal((1, hq, d)).astype(np.float32)
+    q = Q.bf16_bits(q) if dtype == "bf16" else q
+    k, v = (rng.standard_normal((32, hkv, block, d)).astype(np.float32) for _ in range(2))
+    table = np.arange(32, dtype=np.int32)[None]
+    kc, vc = Q.quantise(k), Q.quantise(v)
+    v[7, 1, 5, 33] = bad
+    broken = Q.quantise(v)
+    out = widen(pkv.paged_decode_q4(to_dev(q), to_dev(kc), to_dev(broken), to_dev(table),
+                                    to_dev(np.asarray([n], np.int32))))
+    want, tol, _ = B.decode(q, kc, vc, table, [n], d ** -0.5)
+    nan = np.zeros(out.shape, bool)
+    nan[:, hq // hkv:, 32:64] = True
+    assert np.array_equal(np.isnan(out), nan)
+    assert np.all(np.abs(out - want)[~nan] <= tol[~nan])
