@@ -68,6 +68,8 @@ def build(force: bool = False, verbose: bool = False, extra: tuple[str, ...] = (
         for cmd, r in zip(jobs, results):
             if verbose or r.returncode != 0:
                 sys.stderr.write(r.stdout + r.stderr)
+            else:  # what -warn-spills says of a kernel
+                sys.stderr.writelines(x + "\n" for x in r.stderr.splitlines() if "spill" in x.lower())
             if r.returncode != 0:
                 raise RuntimeError(f"nvcc failed: {' '.join(cmd)}")
     if force or jobs or _stale(LIB, objs):
