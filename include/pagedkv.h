@@ -557,11 +557,11 @@ int paged_kv_read_q4(const void* k_cache, const void* v_cache, const int32_t* sl
  * V scale and rounded to fp16 (11 bits; those below 2^-14 of the largest to 2^-25 of
  * it), below the output's own rounding.  With fp32 queries, queries and weights keep
  * 22 bits or more.  Queries and K up to 1e30 in magnitude (a query is scaled to fp16's
- * range, and what that leaves for K and the scale is fp32's); V may have any finite size; its scales count to 2^-85 absolutely,
- * so that groups of V that span less lose them, and so do those that span 2^-25 of
- * the largest scale among the values that are attended to.  A NaN or infinite query,
- * or a NaN key, makes its own heads' output NaN; a group of V that holds no numbers, its
- * own 32 dims.
+ * range, and what that leaves for K and the scale is fp32's).  V may have any finite
+ * size; its scales count to 2^-85 absolutely and to 2^-25 of the largest scale that a
+ * head's keys hold, so that groups of V that span less lose them.  A NaN or infinite
+ * query, or a NaN key, makes its own heads' output NaN; a group of V that holds no
+ * numbers, its own 32 dims.
  * workspace: paged_decode_q4_workspace_size(batch, q_dtype, geom) bytes, 256-byte
  * aligned, contents irrelevant on entry, as for paged_decode; it must not be used
  * by another call that runs concurrently.  A length below 0 or past the table

@@ -292,6 +292,16 @@ cudaError_t launch_shaped(int device, int64_t mean, int32_t batch, CompactArgs& 
 // tokens of 1, 2, 4, 5, 6 and 8 contexts of 8 K - 40 K (bf16, 8 heads, d = 128), us:
 //   OneList 48, 65, - | TwoLists 69, 58, 96 | FewLists 73, 73, 88, 129, 144, 173
 //   LongLists 118, 96, 125, 155, 166, 181 (64 contexts up to 4 K: 98, FewLists 113)
+// Narrower vectors have fewer slices' worth of bytes, and the rule is near the best of
+// the four except where many slices of a 4-bit row are just too many at once.  Rule and
+// best, us, 1, 2, 4, 6, 8 long contexts and 64 shorter ones: 4-bit rows, d = 64 (8-byte
+// vectors) 47, 47, 59, 75, 136, 30 and 47, 47, 47, 74, 86, 30; 4-bit rows, d = 128
+// (16-byte) 55, 56, 72, 97, 136, 48 and 54, 56, 62, 95, 110, 47; rows of 84 bytes
+// (4-byte) 35, 36, 30, 35, 56, 18 and 35, 35, 30, 35, 50, 18; of 42 bytes (2-byte) 53,
+// 54, 45, 53, 66, 23 and the same.
+// The lists' lengths are on the device, so the rule has their mean only.  Half of one
+// context of 41 K among 63 empty lists takes 115 - 129 (best 85), among 639 520 (best 421),
+// and one list of 2048 among 639 empty ones 113 (the others 171 and more).
 template <typename Vec>
 cudaError_t launch_typed(const DeviceInfo& dev, int64_t mean, int32_t batch, CompactArgs& a,
                          cudaStream_t stream) {

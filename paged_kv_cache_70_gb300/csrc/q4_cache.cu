@@ -19,11 +19,12 @@
 // that the codes leave (and arrive) as whole 32-bit words, consecutive over the
 // lanes.
 //
-// Measured (17,928 rows of 8 x 128, bf16, 96.4 MB of rows and codes): write 20.9 us,
-// 4614 GB/s, bound by issue slots (79 % busy, 17 instructions per value for
-// minimum, maximum, scaling, rounding and packing); read 16.1 us, 5983 GB/s (0.88 of
-// the measured copy rate).  Its first form, with conversions, clamps and a division per
-// value, took 27.
+// Measured (17,928 rows of 8 x 128, bf16, 96.4 MB of rows and codes): write 20.8 us,
+// 4634 GB/s, bound by issue slots (79 % busy, 17 instructions per value for
+// minimum, maximum, scaling, rounding and packing); its first form, with conversions,
+// clamps and a division per value, took 27.  Read 16.7 us, 5780 GB/s (0.85 of the
+// measured copy rate; 34,567 rows 30.7 us, 0.89), with a multiply and add per value in
+// fp32 and a second rounding 17.0.
 #include <algorithm>
 
 #include "common.cuh"

@@ -52,14 +52,17 @@
 //    page holds there.  Every wait is time-limited.
 //
 // Measured (bf16 queries, device time of split and combine; of the measured copy rate):
-//   8 sequences of 16 K - 41 K keys, 16 / 8 heads, d = 128, 303 MB   52.9 us  0.85
-//   the same with 32 / 8 heads 63.4 us (issue slots), 64 / 8 heads 90.7
-//   64 sequences of 128 - 4096 keys, 16 / 8 heads, B = 16, 173 MB    37.1 us  0.69
-//   8 x 16 K - 41 K keys, 16 / 8 heads, d = 64, 152 MB               39.9 us
-//   one of 7777 keys, 32 / 4 heads, d = 64                            8.8 us
-//   fp32 queries, 8 x 8 K - 20 K keys, 16 / 8 heads, d = 128         45.0 us
-// 7 us of each are two launches, the plan, the first tile and the combine; the long
-// contexts' split alone issues in half of its cycles (profile: 52 %).
+//   8 sequences of 16 K - 41 K keys, 16 / 8 heads, d = 128, 303 MB   54.5 us  0.82
+//   the same with 32 / 8 heads 67.0 us, 64 / 8 heads 93.7
+//   64 sequences of 128 - 4096 keys, 16 / 8 heads, B = 16, 173 MB    38.6 us  0.66
+//   8 x 16 K - 41 K keys, 16 / 8 heads, d = 64, 152 MB               42.0 us
+//   one of 7777 keys, 32 / 4 heads, d = 64                            9.8 us
+//   fp32 queries, 8 x 8 K - 20 K keys, 16 / 8 heads, d = 128         45.7 us
+// 8 us of each are two launches, the plan, the first tile and the combine.  No pipe is
+// full in any of the long ones (issue 55 - 60 %, ALU 49 - 55, tensor 18 - 33): three or
+// four warps per scheduler wait for their own chains, so the time goes with the
+// instructions executed, 31 million at 16 / 8 heads, 41 at 32 / 8 (2 % of them for
+// spilled registers), 57 at 64 / 8, 26 at d = 64 and 27 with fp32 queries.
 #include <cuda_fp16.h>
 
 #include <algorithm>
@@ -95,7 +98,9 @@ constexpr size_t kStaticSmem = 1024;  // left for static shared memory
 
 // Consumer warps: 12 with the 128 registers that 16 warps leave a thread, or 8 with
 // 168 where 8 queries keep four column tiles (8 long contexts, 2 queries per KV head
-// 53.8 us with 12 and 57.2 with 8; 8 queries 128 and 96, for spilled registers).
+// 53.8 us with 12 and 57.2 with 8; 8 queries 128 and 96, for spilled registers).  With
+// 3 or 4 queries at d = 128 the 12 spill too, 76 bytes a thread (fp32 queries 104): 67.1
+// us, and 67.6 with 8; fp32 queries over half the keys 55.6 and 52.3.
 __host__ __device__ constexpr int consumers(int qn) { return qn == 8 ? 8 : 12; }
 __host__ __device__ constexpr int threads(int qn) { return (consumers(qn) + kProducers) * 32; }
 
@@ -186,7 +191,9 @@ __device__ __forceinline__ void mma_from(float* d, const uint32_t* a, uint32_t b
 //    come by a permutation): u0 and 16 u1 for the scores (score_pair), whose other
 //    operands, q0 and q1 / 16, are exact; u0 and the byte of the two, u0 + 16 u1, for
 //    the output (code_pair), one logic operation less for half of the pairs: there
-//    both meet the same weights and the result takes u0 out again.
+//    both meet the same weights and the result takes u0 out again.  (The byte in the
+//    scores as well, beside q0 - q1 / 16, took 0.4 us less at 8 long contexts and 2 less
+//    with 4 queries per KV head, and fp16 does not hold that difference.)
 //    The products are aligned by the operands' exponent fields, which overstate a
 //    subnormal by up to 2^10, and cut 25 bits below the largest: about 2^-15 of the
 //    largest weight, under the 2^-11 that the weights' own rounding leaves, and 2^-15
