@@ -157,3 +157,18 @@ def test_an_infinity_in_v_stays_in_its_group(dtype, hq, hkv, d, bad):
     nan[:, hq // hkv:, 32:64] = True
     assert np.array_equal(np.isnan(out), nan)
     assert np.all(np.abs(out - want)[~nan] <= tol[~nan])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 2, 128), (8, 2, 128), (16, 2, 128), (4, 2, 64)])
+@pytest.mark.parametrize("size", [1e-18, 1.6e38])
+def test_the_least_and_largest_values(dtype, hq, hkv, d, size):
+    """V whose groups span nearly all that fp32 holds, and V far below 1."""
+    rng = np.random.default_rng(hq + d)
+    lens, block = [700, 33], 16
+    q = rng.standard_normal((2, hq, d)).astype(np.float32)
+    k = rng.standard_normal((88, hkv, block, d)).astype(np.float32)
+    v = (rng.uniform(-1, 1, (88, hkv, block, d)) * size).astype(np.float32)
+    table = np.arange(88, dtype=np.int32).reshape(2, 44)
+    check(Q.bf16_bits(q) if dtype == "bf16" else q, Q.quantise(k), Q.quantise(v), table, lens,
+          d ** -0.5)
