@@ -60,8 +60,9 @@ extern "C" {
 #endif
 
 /* element types */
-/* PKV_Q4: 4-bit rows, for the calls that name it ("4-bit pools" below) */
-typedef enum pkv_dtype { PKV_F32 = 0, PKV_BF16 = 1, PKV_Q4 = 2 } pkv_dtype;
+/* PKV_Q4, PKV_Q8: 4-bit and 8-bit pools, for the calls that name them ("4-bit pools",
+ * "8-bit pools" below) */
+typedef enum pkv_dtype { PKV_F32 = 0, PKV_BF16 = 1, PKV_Q4 = 2, PKV_Q8 = 3 } pkv_dtype;
 
 /* status codes */
 #define PKV_OK 0
@@ -600,6 +601,135 @@ int paged_kv_compact(void* k_cache, void* v_cache, const int32_t* block_table,
                      int32_t max_blocks_per_seq, const int32_t* start, const int32_t* keep,
                      int32_t total_keep, const int32_t* cu_keep, int32_t batch,
                      int32_t* seqlens_out, const pkv_geom* geom, cudaStream_t stream);
+
+/*
+ * Position rotation of new tokens -- what the writes below apply to keys on their way
+ * into the cache and to the queries of the same tokens.  The dims (i, i + R / 2) of a
+ * head (interleaved != 0: (2 i, 2 i + 1)), i < R / 2 with R = rotary_dim, of a token
+ * at position p become
+ *   x_a c - x_b s,  x_b c + x_a s   with c = cos_sin[p][i], s = cos_sin[p][R / 2 + i];
+ * dims from R on stay as they are.  Every product and sum is rounded to fp32, the result
+ * once more to the type that it is stored in.
+ *   cos_sin    DEVICE fp32 [num_positions, R], 16-byte aligned: R / 2 cosines, then R / 2
+ *              sines of each position (of whatever frequencies and scaling the model has)
+ *   rotary_dim a multiple of 16, 16 .. head_dim
+ *   positions  DEVICE int32 [num_tokens], the position each token is rotated by, or NULL:
+ *              token_pos.  They differ where tokens were evicted from the cache
+ *              (paged_kv_compact) and the rotation goes on counting them.
+ *   q          the tokens' queries [num_tokens, Hq, d] of kv_dtype, or NULL; q_out, which
+ *              may be q itself with q's stride, receives them rotated.  The row of a
+ *              padding token, or of one whose position is outside the table, is passed on
+ *              as it is.
+ *   q_stride, q_out_stride   elements from token to token
+ */
+typedef struct pkv_rope {
+    const float* cos_sin;
+    int32_t num_positions;
+    int32_t rotary_dim;
+    int32_t interleaved;
+    const int32_t* positions;
+    const void* q;
+    int64_t q_stride;
+    void* q_out;
+    int64_t q_out_stride;
+} pkv_rope;
+
+/*
+ * paged_kv_write_rope -- paged_kv_write_positions with the position rotation on the way
+ * ("11. Paged attention 与 online softmax" §11.1; "自己来实现一个"): K rows are rotated
+ * and written, V rows written as they are, and the queries rotated, in one launch.
+ * Tokens, block_table, slot_mapping_out and flags as in paged_kv_write_positions, but
+ * for a table entry outside the pool, which sets PKV_FLAG_BAD_BLOCK; a token whose
+ * rotation's position is outside cos_sin is not written (PKV_FLAG_BAD_LENGTH).
+ * k, v [num_tokens, Hkv, d] with k_stride and v_stride elements from token to token (the
+ * columns of one projection's output, for instance).  The strides in bytes and every
+ * address are multiples of 16.  Supported: fp32 and bf16 rows into fp32 and bf16 pools
+ * (geom->dtype), head_dim 64 or 128, Hq * d and num_tokens up to 2^30.
+ */
+int paged_kv_write_rope(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                        int32_t kv_dtype, const pkv_rope* rope, const int32_t* block_table,
+                        int32_t max_blocks_per_seq, int32_t num_seqs, const int32_t* token_seq,
+                        const int32_t* token_pos, int64_t num_tokens, int32_t* slot_mapping_out,
+                        void* k_cache, void* v_cache, const pkv_geom* geom, cudaStream_t stream);
+
+/*
+ * 8-bit pools -- K and V as e4m3 codes with a scale for each block and KV head ("Sayfalı
+ * dikkat": the cache is what bounds the batch; half of bf16's bytes).  geom->dtype is
+ * PKV_Q8 in every call below, head_dim 64 or 128.
+ * Layout:
+ *   pools  e4m3 [num_blocks, num_kv_heads, block_size, head_dim]
+ *   scales fp32 [num_blocks, num_kv_heads], one array for K and one for V; a value is
+ *          its code times its block's and head's scale.  The write makes scales powers
+ *          of two; the read and the decode take any finite ones.
+ * A page is copied by paged_copy_blocks with a geom whose pages have the same number of
+ * bytes (e.g. one head, block_size 1, head_dim Hkv * B * d / 2, bf16), its scales by a
+ * second call (one head, block_size 1, head_dim Hkv, fp32).  Tokens cannot be moved
+ * from page to page (paged_kv_compact): their codes belong to their page's scale.
+ */
+
+/*
+ * paged_kv_write_q8 -- the tokens' K and V rows into 8-bit pools at their positions, K
+ * rotated first where rope is not NULL (then also the queries, as above).  Arguments and
+ * flags as in paged_kv_write_rope.
+ * The tokens of a call that lie in one page of one sequence follow one another, in
+ * ascending positions.  With a the largest finite magnitude among their values of a head
+ * they need the least power of two n >= 2^-100 with a <= 448 n.  If they begin the page
+ * (the first of them is at a multiple of block_size) its scale becomes s = n, whatever
+ * it was.  Else s = max(n, the least power of two >= the old scale), and where that
+ * differs from the old scale the codes of the rows in front of them become
+ * e4m3(code * (old / s)).  The new codes are e4m3(x / s), rounded to nearest even.
+ * Every value is then within 2^-4 of itself or 2^-10 s of what was written (the larger),
+ * and 2^-10 s more for each time that the scale grew afterwards.  Rows behind the tokens
+ * keep their codes.  A NaN or an infinity is stored as a NaN of its own.  An old scale
+ * below 0, above 2^126 or NaN makes the page's scale NaN.  The pages written must
+ * belong to one sequence only (copy shared ones first, paged_copy_blocks).
+ */
+int paged_kv_write_q8(const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+                      int32_t kv_dtype, const pkv_rope* rope, const int32_t* block_table,
+                      int32_t max_blocks_per_seq, int32_t num_seqs, const int32_t* token_seq,
+                      const int32_t* token_pos, int64_t num_tokens, void* k_cache, void* v_cache,
+                      float* k_scale, float* v_scale, const pkv_geom* geom, cudaStream_t stream);
+
+/*
+ * paged_kv_read_q8 -- rows of 8-bit pools as values: row n of k_out and v_out
+ * ([num_tokens, Hkv, d] of kv_dtype, rounded once) holds what slot_mapping[n] stores; a
+ * negative slot gives a row of zeros, and so does a slot past the pool
+ * (PKV_FLAG_BAD_SLOT).  The same slot may appear more than once.  With the slots of all
+ * keys of a step's requests (paged_build_slot_mapping) this yields the packed K/V that
+ * paged_varlen_prefill takes with block_table == NULL: prompts over an 8-bit cache.
+ * k_out, v_out and the pools 16-byte aligned; Hkv * d and num_tokens up to 2^30.
+ */
+int paged_kv_read_q8(const void* k_cache, const void* v_cache, const float* k_scale,
+                     const float* v_scale, const int32_t* slot_mapping, int64_t num_tokens,
+                     void* k_out, void* v_out, int32_t kv_dtype, const pkv_geom* geom,
+                     cudaStream_t stream);
+
+/*
+ * paged_decode_q8 -- paged_decode over 8-bit pools: one query per sequence (q, out
+ * [batch, Hq, d] of q_dtype, PKV_F32 or PKV_BF16), cache_seqlens[b] keys each, read
+ * through block_table row b; 0 when cache_seqlens[b] == 0.  Codes and scales are used
+ * as stored; scores, softmax statistics and sums are fp32.
+ * Supported: any Hq / Hkv up to 64; head_dim 128 with any block_size (multiples of 8
+ * are fastest), 64 with an even one; batch <= 4096; num_blocks * Hkv below 2^31;
+ * max_blocks_per_seq * block_size up to 2^31 - 4097, and below 2^34 for the whole batch.
+ * Rounding: bf16 queries enter the scores exactly (down to 2^-31 of the largest value of
+ * the query); each weight is multiplied by its V scale and rounded to fp16 (11 bits; those
+ * below 2^-20 of the largest of a head's to 2^-31 of it), below the output's own
+ * rounding.  With fp32 queries, queries and weights keep 22 bits.  A NaN or infinite
+ * query, or a NaN key, makes its own heads' output NaN, and so does a V scale that is no
+ * number; a NaN code of V makes its own dim NaN.
+ * workspace: paged_decode_q8_workspace_size(batch, q_dtype, geom) bytes, 256-byte
+ * aligned, contents irrelevant on entry, as for paged_decode; it must not be used by
+ * another call that runs concurrently.  A length below 0 or past the table counts as
+ * the nearest valid one (PKV_FLAG_BAD_LENGTH); keys of a bad page are skipped
+ * (PKV_FLAG_BAD_BLOCK).
+ */
+size_t paged_decode_q8_workspace_size(int32_t batch, int32_t q_dtype, const pkv_geom* geom);
+int paged_decode_q8(const void* q, int32_t q_dtype, const void* k_cache, const void* v_cache,
+                    const float* k_scale, const float* v_scale, const int32_t* block_table,
+                    int32_t max_blocks_per_seq, const int32_t* cache_seqlens, int32_t batch,
+                    float scale, void* out, void* workspace, size_t workspace_bytes,
+                    const pkv_geom* geom, cudaStream_t stream);
 
 /* paged_status_string -- static text for a PKV_* status code. */
 const char* paged_status_string(int status);

@@ -18,7 +18,7 @@ import torch
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libpagedkv.so")
 
-PKV_F32, PKV_BF16, PKV_Q4 = 0, 1, 2
+PKV_F32, PKV_BF16, PKV_Q4, PKV_Q8 = 0, 1, 2, 3
 PKV_FLAG_BAD_BLOCK = 1 << 0
 PKV_FLAG_BAD_SLOT = 1 << 1
 PKV_FLAG_BAD_LENGTH = 1 << 2
@@ -60,6 +60,11 @@ EXPORTED = (
     "paged_decode_q4",
     "paged_kv_compact",
     "paged_bm_compact",
+    "paged_kv_write_rope",
+    "paged_kv_write_q8",
+    "paged_kv_read_q8",
+    "paged_decode_q8_workspace_size",
+    "paged_decode_q8",
 )
 PKV_ERR_NO_SPACE = -5
 
@@ -98,6 +103,16 @@ class MixedStep(ctypes.Structure):
         ("group_prefix_len", ctypes.c_void_p), ("n_groups", ctypes.c_int32),
         ("max_group_size", ctypes.c_int32), ("decode_out", ctypes.c_void_p),
         ("scale", ctypes.c_float),
+    ]
+
+
+class Rope(ctypes.Structure):
+    """pkv_rope of include/pagedkv.h"""
+    _fields_ = [
+        ("cos_sin", ctypes.c_void_p), ("num_positions", ctypes.c_int32),
+        ("rotary_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32),
+        ("positions", ctypes.c_void_p), ("q", ctypes.c_void_p), ("q_stride", ctypes.c_int64),
+        ("q_out", ctypes.c_void_p), ("q_out_stride", ctypes.c_int64),
     ]
 
 
@@ -186,6 +201,20 @@ def load_library(path: str | None = None):
         lib.paged_decode_q4.restype = ctypes.c_int
         lib.paged_kv_compact.argtypes = [vp, vp, vp, i32, vp, vp, i32, vp, i32, vp, gp, vp]
         lib.paged_kv_compact.restype = ctypes.c_int
+        rp = ctypes.POINTER(Rope)
+        lib.paged_kv_write_rope.argtypes = [vp, i64, vp, i64, i32, rp, vp, i32, i32, vp, vp, i64,
+                                            vp, vp, vp, gp, vp]
+        lib.paged_kv_write_rope.restype = ctypes.c_int
+        lib.paged_kv_write_q8.argtypes = [vp, i64, vp, i64, i32, rp, vp, i32, i32, vp, vp, i64,
+                                          vp, vp, vp, vp, gp, vp]
+        lib.paged_kv_write_q8.restype = ctypes.c_int
+        lib.paged_kv_read_q8.argtypes = [vp, vp, vp, vp, vp, i64, vp, vp, i32, gp, vp]
+        lib.paged_kv_read_q8.restype = ctypes.c_int
+        lib.paged_decode_q8_workspace_size.argtypes = [i32, i32, gp]
+        lib.paged_decode_q8_workspace_size.restype = sz
+        lib.paged_decode_q8.argtypes = [vp, i32, vp, vp, vp, vp, vp, i32, vp, i32, ctypes.c_float,
+                                        vp, vp, sz, gp, vp]
+        lib.paged_decode_q8.restype = ctypes.c_int
         lib.paged_status_string.argtypes = [ctypes.c_int]
         lib.paged_status_string.restype = ctypes.c_char_p
         if path is None:
@@ -597,27 +626,42 @@ class BlockManager:
 
 
 def paged_copy_blocks(k_cache: torch.Tensor, v_cache: torch.Tensor, src: torch.Tensor,
-                      dst: torch.Tensor) -> None:
+                      dst: torch.Tensor, k_scale: torch.Tensor | None = None,
+                      v_scale: torch.Tensor | None = None) -> None:
     """Block dst[i] of both pools becomes a copy of block src[i] (int32 CUDA
-    tensors): the copies a copy-on-write needs.  4-bit pools as well."""
+    tensors): the copies a copy-on-write needs.  4-bit pools as well, and 8-bit
+    ones with their scales."""
     _cuda_contig("k_cache", k_cache)
     _cuda_contig("v_cache", v_cache, k_cache.dtype)
     _cuda_contig("src", src, torch.int32)
     _cuda_contig("dst", dst, torch.int32)
     if src.numel() != dst.numel() or v_cache.shape != k_cache.shape:
         raise ValueError("shape mismatch")
-    if k_cache.dtype == torch.uint8:  # a 4-bit page, moved as one row of 16-bit words
-        q4_geom_of(k_cache, k_cache.shape[1])
+    calls = [(k_cache, v_cache)]
+    if k_cache.dtype in (torch.uint8, torch.float8_e4m3fn):
+        # a page of codes, moved as one row of 16-bit words
+        if k_cache.dtype == torch.uint8:
+            q4_geom_of(k_cache, k_cache.shape[1])
+        else:
+            nb, hkv, _, _ = _q8_shape(k_cache)
+            for n, t in (("k_scale", k_scale), ("v_scale", v_scale)):
+                if t is None or tuple(t.shape) != (nb, hkv):
+                    raise ValueError(f"{n} must be [num_blocks, Hkv]")
+                _cuda_contig(n, t, torch.float32)
+            calls.append((k_scale, v_scale))
         words = k_cache[0].numel() // 2 if len(k_cache) else 1
         if words > 2**31 - 1:
             raise ValueError("a page holds 2^31 16-bit words at most")
-        g = Geom(1, 1, words, 1, len(k_cache), PKV_BF16)
+        geoms = [Geom(1, 1, words, 1, len(k_cache), PKV_BF16)]
+        if len(calls) > 1:
+            geoms.append(Geom(1, 1, max(1, hkv), 1, nb, PKV_F32))
     else:
-        g = geom_of(k_cache, k_cache.shape[2])
+        geoms = [geom_of(k_cache, k_cache.shape[2])]
     with torch.cuda.device(k_cache.device):
-        st = load_library().paged_copy_blocks(_ptr(k_cache), _ptr(v_cache), _ptr(src), _ptr(dst),
-                                              src.numel(), ctypes.byref(g), _stream(k_cache))
-    _check("paged_copy_blocks", st)
+        for (k, v), g in zip(calls, geoms):
+            st = load_library().paged_copy_blocks(_ptr(k), _ptr(v), _ptr(src), _ptr(dst),
+                                                  src.numel(), ctypes.byref(g), _stream(k_cache))
+            _check("paged_copy_blocks", st)
 
 
 def paged_mixed_step(k_cache: torch.Tensor, v_cache: torch.Tensor, scale: float,
@@ -897,3 +941,228 @@ def paged_kv_compact(k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: 
             _arg("keep", keep, index, i32), keep.numel(), _arg("cu_keep", cu_keep, index, i32),
             batch, None if seqlens_out is None else _arg("seqlens_out", seqlens_out, index, i32),
             _geom(hkv, hkv, d, bs, nb, code))
+
+
+# ---- the position rotation and 8-bit pools ---------------------------------------
+def q8_cache_shape(num_blocks: int, block_size: int, num_kv_heads: int,
+                   head_dim: int) -> tuple[int, int, int, int]:
+    """Shape of an 8-bit K or V pool (float8_e4m3fn): [num_blocks, num_kv_heads,
+    block_size, head_dim]; its scales are float32 [num_blocks, num_kv_heads]."""
+    if head_dim not in (64, 128):
+        raise ValueError("8-bit pools hold head_dim 64 or 128")
+    return num_blocks, num_kv_heads, block_size, head_dim
+
+
+def _q8_shape(k_cache: torch.Tensor):
+    """(num_blocks, num_kv_heads, block_size, head_dim) of an 8-bit pool."""
+    if k_cache.dtype != torch.float8_e4m3fn or k_cache.dim() != 4 or \
+            k_cache.shape[3] not in (64, 128):
+        raise ValueError("an 8-bit pool is float8_e4m3fn [num_blocks, Hkv, block_size, head_dim]")
+    nb, hkv, bs, d = k_cache.shape
+    if hkv > _INT32 or bs > _INT32:  # (ctypes would cut them off)
+        raise ValueError("num_kv_heads and block_size are 32-bit")
+    return nb, hkv, bs, d
+
+
+def q8_geom_of(k_cache: torch.Tensor, num_heads: int) -> Geom:
+    """pkv_geom of an 8-bit pool [num_blocks, num_kv_heads, block_size, head_dim]."""
+    nb, hkv, bs, d = _q8_shape(k_cache)
+    return Geom(num_heads, hkv, d, bs, nb, PKV_Q8)
+
+
+def _scales(index: int, k_cache, v_cache, k_scale, v_scale) -> tuple[int, int]:
+    """The scales' addresses, checked with the pools they belong to."""
+    if v_cache.shape != k_cache.shape or k_scale.shape != k_cache.shape[:2] or \
+            v_scale.shape != k_cache.shape[:2]:
+        raise ValueError("the pools have one shape and the scales are [num_blocks, Hkv]")
+    return (_arg("k_scale", k_scale, index, torch.float32),
+            _arg("v_scale", v_scale, index, torch.float32))
+
+
+def _rows(name: str, t: torch.Tensor, index: int, dtype=None) -> tuple[int, int]:
+    """Address and token stride (elements) of rows [N, H, d] whose heads are contiguous."""
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor" if not t.is_cuda else
+                         f"{name} must be on the device of the other tensors")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    n, h, d = t.shape
+    sn, sh, sd = t.stride()
+    if n * h * d and ((d > 1 and sd != 1) or (h > 1 and sh != d)):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    return t.data_ptr(), (sn if n > 1 else h * d)
+
+
+def _write_new(func: str, k, v, cos_sin, block_table, token_seq, token_pos, q, q_out, rope_pos,
+               interleaved, hkv, d, tail, geom):
+    """The arguments that paged_kv_write_rope and paged_kv_write_q8 share; returns q_out."""
+    index = k.get_device()
+    n = k.shape[0]
+    if k.shape != v.shape or k.shape[1:] != (hkv, d):
+        raise ValueError("shape mismatch between k/v rows and the pools")
+    if token_seq.numel() != n or token_pos.numel() != n or \
+            (rope_pos is not None and rope_pos.numel() != n):
+        raise ValueError("token_seq, token_pos and rope_pos must have one entry per token row")
+    rows, width = block_table.shape
+    if max(rows, width, n) > _INT32:
+        raise ValueError("tokens and the table's rows and columns are 32-bit")
+    i32 = torch.int32
+    code = _dtype_code(k)
+    kp, ks = _rows("k", k, index)
+    vp, vs = _rows("v", v, index, k.dtype)
+    rope, hq = None, hkv
+    if cos_sin is None:
+        if q is not None or q_out is not None or rope_pos is not None:
+            raise ValueError("q, q_out and rope_pos go with cos_sin")
+    else:
+        if cos_sin.dim() != 2 or max(cos_sin.shape) > _INT32:
+            raise ValueError("cos_sin must be [positions, rotary_dim]")
+        rope = Rope(cos_sin=_arg("cos_sin", cos_sin, index, torch.float32),
+                    num_positions=cos_sin.shape[0], rotary_dim=cos_sin.shape[1],
+                    interleaved=1 if interleaved else 0,
+                    positions=None if rope_pos is None else _arg("rope_pos", rope_pos, index, i32))
+        if q is not None:
+            if q.dim() != 3 or q.shape[0] != n or q.shape[2] != d or q.shape[1] > _INT32:
+                raise ValueError("q must be [N, Hq, d]")
+            hq = q.shape[1]
+            rope.q, rope.q_stride = _rows("q", q, index, k.dtype)
+            if q_out is None:
+                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+            elif q_out.shape != q.shape:
+                raise ValueError("q_out must have q's shape")
+            rope.q_out, rope.q_out_stride = _rows("q_out", q_out, index, k.dtype)
+        elif q_out is not None:
+            raise ValueError("q_out goes with q")
+    load_library()
+    _launch(func, index, kp, ks, vp, vs, code, None if rope is None else ctypes.byref(rope),
+            _arg("block_table", block_table, index, i32), width, rows,
+            _arg("token_seq", token_seq, index, i32), _arg("token_pos", token_pos, index, i32), n,
+            *tail, geom(hq))
+    return q_out
+
+
+def paged_kv_write_rope(k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor,
+                        block_table: torch.Tensor, token_seq: torch.Tensor,
+                        token_pos: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                        q: torch.Tensor | None = None, q_out: torch.Tensor | None = None,
+                        rope_pos: torch.Tensor | None = None, interleaved: bool = False,
+                        slot_mapping_out: torch.Tensor | None = None) -> torch.Tensor | None:
+    """paged_kv_write_positions with k (and q [N, Hq, d], returned in q_out) rotated
+    on the way by rope_pos (token_pos where None); cos_sin [positions, rotary_dim]
+    holds each position's cosines, then its sines.  The heads of a token are
+    contiguous in k, v, q and q_out, the tokens may be strided."""
+    index = k.get_device()
+    nb, bs, hkv, d = k_cache.shape
+    if v_cache.shape != k_cache.shape or max(bs, hkv, d) > _INT32:
+        raise ValueError("shape mismatch between the pools")
+    if slot_mapping_out is not None and slot_mapping_out.numel() != k.shape[0]:
+        raise ValueError("slot_mapping_out must have one entry per token row")
+    if cos_sin is None:
+        raise ValueError("cos_sin is needed (paged_kv_write_positions writes without it)")
+    code = _dtype_code(k_cache)
+    tail = (None if slot_mapping_out is None else
+            _arg("slot_mapping_out", slot_mapping_out, index, torch.int32),
+            _arg("k_cache", k_cache, index), _arg("v_cache", v_cache, index, k_cache.dtype))
+    return _write_new("paged_kv_write_rope", k, v, cos_sin, block_table, token_seq, token_pos, q,
+                      q_out, rope_pos, interleaved, hkv, d, tail,
+                      lambda hq: _geom(hq, hkv, d, bs, nb, code))
+
+
+def paged_kv_write_q8(k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
+                      token_seq: torch.Tensor, token_pos: torch.Tensor, k_cache: torch.Tensor,
+                      v_cache: torch.Tensor, k_scale: torch.Tensor, v_scale: torch.Tensor,
+                      cos_sin: torch.Tensor | None = None, q: torch.Tensor | None = None,
+                      q_out: torch.Tensor | None = None, rope_pos: torch.Tensor | None = None,
+                      interleaved: bool = False) -> torch.Tensor | None:
+    """In-place write of k/v [N, Hkv, d] rows (fp32 or bf16) into 8-bit pools
+    (q8_cache_shape) at their positions, with the pages' scales; the tokens of one
+    page follow one another.  With cos_sin, k and q are rotated first, as in
+    paged_kv_write_rope."""
+    index = k.get_device()
+    nb, hkv, bs, d = _q8_shape(k_cache)
+    tail = (_arg("k_cache", k_cache, index), _arg("v_cache", v_cache, index, k_cache.dtype),
+            *_scales(index, k_cache, v_cache, k_scale, v_scale))
+    return _write_new("paged_kv_write_q8", k, v, cos_sin, block_table, token_seq, token_pos, q,
+                      q_out, rope_pos, interleaved, hkv, d, tail,
+                      lambda hq: _geom(hq, hkv, d, bs, nb, PKV_Q8))
+
+
+def paged_kv_read_q8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
+                     v_scale: torch.Tensor, slot_mapping: torch.Tensor,
+                     dtype: torch.dtype = torch.bfloat16, k_out: torch.Tensor | None = None,
+                     v_out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
+    """The values [N, Hkv, d] that 8-bit pools hold at slot_mapping [N], in
+    ``dtype`` (fp32 or bf16); rows of zeros at negative slots."""
+    index = k_cache.get_device()
+    nb, hkv, bs, d = _q8_shape(k_cache)
+    n = slot_mapping.numel()
+    shape = (n, hkv, d)
+    if k_out is None:
+        k_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
+    if v_out is None:
+        v_out = torch.empty(shape, dtype=k_out.dtype, device=k_cache.device)
+    if k_out.shape != shape or v_out.shape != shape:
+        raise ValueError("k_out / v_out must be [N, Hkv, d]")
+    load_library()
+    _launch("paged_kv_read_q8", index, _arg("k_cache", k_cache, index),
+            _arg("v_cache", v_cache, index, k_cache.dtype),
+            *_scales(index, k_cache, v_cache, k_scale, v_scale),
+            _arg("slot_mapping", slot_mapping, index, torch.int32), n,
+            _arg("k_out", k_out, index), _arg("v_out", v_out, index, k_out.dtype),
+            _dtype_code(k_out), _geom(hkv, hkv, d, bs, nb, PKV_Q8))
+    return k_out, v_out
+
+
+def _decode_q8_size(index: int, batch: int, code: int, *geom) -> int:
+    """paged_decode_q8_workspace_size on device `index`, looked up after the first."""
+    key = (index, batch, code) + geom
+    need = _sizes.get(key)
+    if need is None:
+        if len(_sizes) > 1000:
+            _sizes.clear()
+        with torch.cuda.device(index):
+            need = _sizes[key] = int(load_library().paged_decode_q8_workspace_size(
+                batch, code, _geom(*geom)))
+    return need
+
+
+def paged_decode_q8_workspace_size(batch: int, q_heads: int, q_dtype: torch.dtype,
+                                   k_cache: torch.Tensor) -> int:
+    nb, hkv, bs, d = _q8_shape(k_cache)
+    code = _dtype_code(torch.empty(0, dtype=q_dtype))
+    return _decode_q8_size(k_cache.get_device(), batch, code, q_heads, hkv, d, bs, nb, PKV_Q8)
+
+
+def paged_decode_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                    k_scale: torch.Tensor, v_scale: torch.Tensor, block_table: torch.Tensor,
+                    cache_seqlens: torch.Tensor, scale: float | None = None,
+                    out: torch.Tensor | None = None,
+                    workspace: torch.Tensor | None = None) -> torch.Tensor:
+    """One query token per sequence (q [batch, Hq, d], fp32 or bf16) over its
+    cache_seqlens[b] keys in 8-bit pools."""
+    index = q.get_device()
+    batch, hq, d = q.shape
+    nb, hkv, bs, dk = _q8_shape(k_cache)
+    rows, width = block_table.shape
+    if d != dk or rows < batch or cache_seqlens.numel() < batch:
+        raise ValueError("shape mismatch")
+    if max(batch, width, hq) > _INT32:
+        raise ValueError("q and a table's row hold 2^31 - 1 entries at most")
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    code = _dtype_code(q)
+    args = (_arg("q", q, index), code, _arg("k_cache", k_cache, index),
+            _arg("v_cache", v_cache, index, k_cache.dtype),
+            *_scales(index, k_cache, v_cache, k_scale, v_scale),
+            _arg("block_table", block_table, index, torch.int32), width,
+            _arg("cache_seqlens", cache_seqlens, index, torch.int32), batch,
+            1.0 / math.sqrt(d) if scale is None else scale, _arg("out", out, index, q.dtype))
+    if workspace is None:
+        need = _decode_q8_size(index, batch, code, hq, hkv, d, bs, nb, PKV_Q8)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    load_library()
+    _launch("paged_decode_q8", index, *args, _arg("workspace", workspace, index),
+            workspace.numel() * workspace.element_size(), _geom(hq, hkv, d, bs, nb, PKV_Q8))
+    return out

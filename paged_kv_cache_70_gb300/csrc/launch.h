@@ -260,6 +260,66 @@ cudaError_t launch_q4_decode(const DeviceInfo& dev, const Q4DecodePlan& plan, co
                              int64_t num_blocks, int q_dtype, unsigned int* err,
                              cudaStream_t stream);
 
+// ---- writes with the position rotation (rope_write.cu, q8_cache.cu) ------------------
+struct RopeWriteLaunch {
+    const void* k;
+    const void* v;
+    int src_dtype;               // of k, v, q and q_out
+    int64_t k_stride, v_stride;  // elements from token to token
+    const int32_t* token_seq;
+    const int32_t* token_pos;
+    const int32_t* rope_pos;     // null: token_pos
+    int64_t num_tokens;
+    const int32_t* table;
+    int32_t num_seqs, max_blocks;
+    const float* cos_sin;        // [positions, rot]; rot 0: no rotation
+    int32_t positions, rot, interleaved;
+    const void* q;               // null: no queries
+    void* q_out;
+    int64_t q_stride, q_out_stride;
+    int32_t* slots_out;          // may be null
+    void* k_cache;
+    void* v_cache;
+    int cache_dtype;
+    int32_t hq, hkv, d, block_size;
+    int64_t num_blocks;
+    unsigned int* err;
+};
+cudaError_t launch_rope_write(const RopeWriteLaunch& r, cudaStream_t stream);
+
+// ---- 8-bit pools (q8_cache.cu, q8_decode.cu) -----------------------------------------
+cudaError_t launch_q8_write(const DeviceInfo& dev, const RopeWriteLaunch& r, float* k_scale,
+                            float* v_scale, cudaStream_t stream);
+cudaError_t launch_q8_read(const void* k_cache, const void* v_cache, const float* k_scale,
+                           const float* v_scale, const int32_t* slots, int64_t num_tokens,
+                           void* k, void* v, int dst_dtype, int hkv, int d, int block_size,
+                           int64_t num_slots, unsigned int* err, cudaStream_t stream);
+
+struct Q8DecodePlan {
+    int no;           // warps' worth of 8 query heads per KV head
+    int hc;           // KV heads per CTA
+    int wh;           // warps that share a head and its queries
+    int head_groups;  // grid.y = Hkv / hc
+    int ctas;         // grid.x (CTAs along the keys)
+    int tile;         // keys per stage
+    int piece;        // keys per copy (divides the tile and the page)
+    int stages;
+    size_t smem_bytes;
+    size_t ws_bytes;  // workspace bytes needed (the same for every max_blocks)
+};
+
+// Returns false when the geometry is not supported.
+bool plan_q8_decode(const DeviceInfo& dev, int32_t batch, int32_t max_blocks, int hq, int hkv,
+                    int d, int block_size, int64_t num_blocks, int q_dtype, Q8DecodePlan* plan);
+
+cudaError_t launch_q8_decode(const DeviceInfo& dev, const Q8DecodePlan& plan, const void* q,
+                             const void* k_cache, const void* v_cache, const float* k_scale,
+                             const float* v_scale, const int32_t* table, int32_t max_blocks,
+                             const int32_t* seqlens, int32_t batch, float scale, void* out,
+                             void* workspace, int hq, int hkv, int d, int block_size,
+                             int64_t num_blocks, int q_dtype, unsigned int* err,
+                             cudaStream_t stream);
+
 // ---- compaction (compact.cu) ---------------------------------------------------
 // A token's row is `pieces` runs of piece_bytes, head_bytes apart; tokens are
 // token_bytes apart within a page, pages page_bytes apart.
