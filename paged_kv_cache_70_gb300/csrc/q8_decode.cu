@@ -177,6 +177,10 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
         mbar_init(&merge_bar[1], units);
         fence_barrier_init();
     }
+    if (tid >= WC * 32 && tid < WC * 32 + 64 && lane == 0)  // the producers' first K and V maps
+        asm volatile("prefetch.tensormap [%0];" ::"l"(
+                         reinterpret_cast<uint64_t>(tid == WC * 32 ? &kmap : &vmap))
+                     : "memory");
     asm volatile("griddepcontrol.wait;" ::: "memory");
 
     // ---- plan: tile starts of the sequences (an exclusive scan of their tiles)
@@ -275,6 +279,18 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                                                               id < a.num_blocks));
             }
             const bool bad = good < np;
+            // the scale of this lane's (piece, head), the first 32 of them before the wait
+            auto scale_of = [&](int32_t id32, int c0, int i0, int* at) {
+                const int n = min(32, np - c0) * a.hc;
+                const int i = min(i0 + lane, n - 1);
+                const int p = (int)((i * inv_hc) >> 16), h = i - p * a.hc;
+                const int32_t id = __shfl_sync(0xffffffffu, id32, p);
+                const bool here = i0 + lane < n && id >= 0 && id < a.num_blocks;
+                *at = here ? ((c0 + p) * a.hc + h) * 2 : -1;
+                return here ? __ldg(from + (int64_t)id * a.hkv + head0 + h) : 0.f;
+            };
+            int first_at;
+            const float first = scale_of(page, 0, 0, &first_at);
             bool ok = true;
             if (lane == 0) {
                 ok = mbar_wait(&empty[s], (fills & 1) ^ 1, a.err);
@@ -286,23 +302,8 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
             __syncwarp();
             if (!__all_sync(0xffffffffu, ok)) break;
             last_k = k;
-            float* to = scales + (size_t)s * pieces * a.hc * 2 + is_v;
-            for (int c0 = 0; c0 < np; c0 += 32) {
-                const int32_t id32 = c0 == 0 ? page : fetch(seq, q0, q1, c0);
-                const int n = min(32, np - c0) * a.hc;
-                for (int i0 = 0; i0 < n; i0 += 32) {
-                    const int i = min(i0 + lane, n - 1);
-                    const int p = (int)((i * inv_hc) >> 16), h = i - p * a.hc;
-                    const int32_t id = __shfl_sync(0xffffffffu, id32, p);
-                    if (i0 + lane < n && id >= 0 && id < a.num_blocks)
-                        to[((c0 + p) * a.hc + h) * 2] =
-                            __ldg(from + (int64_t)id * a.hkv + head0 + h);
-                }
-            }
-            __syncwarp();
-            if (lane == 0)
-                mbar_arrive_expect_tx(&full[s], (uint32_t)good * a.hc * P * D);
-            __syncwarp();
+            // the copies first: the scales may still be on their way, and the barrier counts
+            // bytes that arrive before they are expected
             unsigned char* dst = ring + (size_t)(2 * s + is_v) * half_bytes;
             for (int c0 = 0; c0 < np; c0 += 32) {
                 const int32_t id = c0 == 0 ? page : fetch(seq, q0, q1, c0);
@@ -313,6 +314,20 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                               p - pg * a.block_size, id * a.hkv + head0, &full[s], pol);
                 }
             }
+            float* to = scales + (size_t)s * pieces * a.hc * 2 + is_v;
+            if (first_at >= 0) to[first_at] = first;
+            if (np * a.hc > 32)
+                for (int c0 = 0; c0 < np; c0 += 32) {
+                    const int32_t id32 = c0 == 0 ? page : fetch(seq, q0, q1, c0);
+                    for (int i0 = c0 == 0 ? 32 : 0; i0 < min(32, np - c0) * a.hc; i0 += 32) {
+                        int at;
+                        const float x = scale_of(id32, c0, i0, &at);
+                        if (at >= 0) to[at] = x;
+                    }
+                }
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive_expect_tx(&full[s], (uint32_t)good * a.hc * P * D);
             __syncwarp();
             s += prods;
             if (s >= S) {
