@@ -10,15 +10,18 @@
 // another in the list (a run); a run is found by its first token, which differs from
 // the token before it in sequence or page.
 //
-// What bounds it: bytes for long runs, the chain token -> page -> old scale -> rows for
-// single tokens.  A (run, head) is held by wr warps in registers from the load over the
-// maximum to the store, so that rows are read once: 4 rows (d = 64: 8) per warp and
-// step, 8 steps (fp32: 4); only runs of more rows than that are read twice.  The
-// CTAs take `window` tokens each, as few as fill the GPU: one CTA per token would be
-// mostly CTAs in which no run begins.
+// What bounds it: bytes for long runs, the chain token -> page -> rows -> angles for
+// single tokens.  A CTA looks at 256 tokens at once, one per thread, for one head of K or
+// V, and takes every `parts`-th of the runs that begin among them: a warp each, or, runs
+// of more rows than a warp holds, all its warps together.  Rows stay in shared memory
+// from the load over the maximum to the store, so that they are read once (runs of more
+// rows than a CTA holds: twice).  A thread copies there (cp.async) what it reads itself:
+// no barrier but those of the maximum, and no registers for rows in flight.  Keys are put
+// back rotated, bf16 ones in 16 bits that round to the same code.
 // Read: row n of the outputs is code * scale at slot_mapping[n], rounded once to the
 // output's type; zeros for a negative slot.
 #include <algorithm>
+#include <atomic>
 
 #include "launch.h"
 #include "q8.cuh"
@@ -29,8 +32,12 @@ namespace pkv {
 namespace {
 
 constexpr int kWarps = 8;  // per CTA of the write
+// row steps that a CTA holds in shared memory, 8 KiB each (fp32: 16): 64 KiB, so that
+// three CTAs share an SM
 template <bool F32>
-__host__ __device__ constexpr int row_steps() { return F32 ? 4 : 8; }  // that a warp holds
+__host__ __device__ constexpr int most_steps() { return F32 ? 4 : 8; }
+template <bool F32>
+__host__ __device__ constexpr int step_bytes() { return kWarps * 32 * (F32 ? 64 : 32); }
 
 struct Q8WriteArgs {
     const void* k;
@@ -43,10 +50,10 @@ struct Q8WriteArgs {
     float* vs;
     RopeTable table;
     RopeQuery q;
-    int64_t kv_ctas;    // the CTAs behind them take the queries
-    int32_t wr;         // warps per (run, head)
-    int32_t groups;     // of kWarps / wr heads
-    int32_t window;     // tokens whose runs a CTA takes
+    uint64_t kv_step;   // CTAs of K and V per CTA while there are any, in 2^-32
+    uint32_t kv_ctas;   // the others take the queries
+    int32_t steps;      // row steps held
+    int32_t parts;      // CTAs that share the runs of kWarps * 32 tokens
     unsigned int* err;
 };
 
@@ -62,200 +69,414 @@ __device__ __forceinline__ float scale_up(float s) {
     return __uint_as_float((__float_as_uint(s) + 0x7fffffu) & 0x7f800000u);
 }
 
-template <int D, bool F32, bool MIX>
-__device__ __forceinline__ void write_runs(const Q8WriteArgs& a) {
-    constexpr int U = D / 16, RS = 32 / U;  // lanes per row, rows per step
-    constexpr int S = row_steps<F32>();
-    __shared__ uint32_t red[2][kWarps];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const bool is_v = blockIdx.x & 1;
-    const int64_t id = blockIdx.x >> 1;
-    const int64_t n0 = id / a.groups * a.window;
-    const int64_t n1 = min(n0 + a.window, a.tok.num);
-    const int group = (int)(id % a.groups);
-    const int team = warp / a.wr, rank = warp % a.wr;
-    const int h = group * (kWarps / a.wr) + team;
-    const bool has = h < a.tok.hkv;
-    const bool reports = group == 0 && !is_v && warp == 0;  // flags what is wrong with tokens
-    const int32_t B = (int32_t)a.tok.block.d;
-    unsigned char* const pool = is_v ? a.vc : a.kc;
-    float* const scales = is_v ? a.vs : a.ks;
-    const int rot = is_v ? 0 : a.table.rot;
-    const int u = lane % U;
-    int da, db;
-    unit_dims<MIX>(u, rot, &da, &db);
-    const bool spins = u < (rot >> 4);
-    const unsigned char* const rows =
-        static_cast<const unsigned char*>(is_v ? a.v : a.k) + (int64_t)h * D * (F32 ? 4 : 2);
-    const int64_t stride = (is_v ? a.v_stride : a.k_stride) * (F32 ? 4 : 2);
-    int turn = 0;  // of `red`
+// x and y cut to bf16, with the last bit set where something was cut off
+__device__ __forceinline__ uint32_t odd_bf16x2(float x, float y) {
+    const uint32_t lo = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x5410);
+    const uint32_t hi = __byte_perm(__float_as_uint(x), __float_as_uint(y), 0x7632);
+    uint32_t some;
+    asm("min.u16x2 %0, %1, %2;" : "=r"(some) : "r"(lo), "r"(0x00010001u));
+    return hi | some;
+}
 
-    // the largest of the team's
-    auto team_max = [&](uint32_t m) {
+// the largest magnitude of 16 bf16, NaNs aside
+__device__ __forceinline__ float largest_bf16(const uint4& a, const uint4& b) {
+    const uint32_t w[8] = {a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+    uint32_t m = 0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        asm("{\n\t.reg .b32 t;\n\tabs.bf16x2 t, %1;\n\tmax.bf16x2 %0, %0, t;\n\t}" : "+r"(m) : "r"(w[i]));
+    return fmaxf(bf16lo(m), bf16hi(m));
+}
+
+// A thread's unit in shared memory: pieces of 16 bytes, kPiece apart, at `slot`
+constexpr int kPiece = kWarps * 32 * 16;
+template <bool F32>
+__device__ __forceinline__ void stage_unit(uint32_t slot, const unsigned char* a,
+                                           const unsigned char* b) {
+    constexpr int C = F32 ? 4 : 2;
+#pragma unroll
+    for (int j = 0; j < C; ++j)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(slot + j * kPiece),
+                     "l"((j < C / 2 ? a : b) + (j % (C / 2)) * 16)
+                     : "memory");
+}
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 w;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(w.x), "=r"(w.y), "=r"(w.z), "=r"(w.w) : "r"(at) : "memory");
+    return w;
+}
+__device__ __forceinline__ void sts16(uint32_t at, uint4 w) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(w.x), "r"(w.y),
+                 "r"(w.z), "r"(w.w)
+                 : "memory");
+}
+template <bool F32>
+__device__ __forceinline__ RawUnit<F32> staged_unit(uint32_t slot) {
+    constexpr int C = F32 ? 4 : 2;
+    RawUnit<F32> x;
+#pragma unroll
+    for (int j = 0; j < C; ++j) (j < C / 2 ? x.a[j % (C / 2)] : x.b[j % (C / 2)]) = lds16(slot + j * kPiece);
+    return x;
+}
+template <bool F32>
+__device__ __forceinline__ void restage_unit(uint32_t slot, const float* x) {
+    constexpr int C = F32 ? 4 : 2, E = 16 / C;
+#pragma unroll
+    for (int j = 0; j < C; ++j) {
+        const float* y = x + E * j;
+        if constexpr (F32)
+            sts16(slot + j * kPiece, make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]),
+                                                __float_as_uint(y[2]), __float_as_uint(y[3])));
+        else
+            sts16(slot + j * kPiece, make_uint4(odd_bf16x2(y[0], y[1]), odd_bf16x2(y[2], y[3]),
+                                                odd_bf16x2(y[4], y[5]), odd_bf16x2(y[6], y[7])));
+    }
+}
+
+// which tokens of a CTA's window begin a run (the tokens of one sequence on one page),
+// and which continue the run of the token before them
+struct Window {
+    uint32_t starts[kWarps], goes_on[kWarps];
+};
+
+__device__ __forceinline__ void look_at_window(const NewTokens& t, const RopeTable& table,
+                                               int64_t n0, unsigned int* err, Window* w) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t n = n0 + threadIdx.x;
+    int32_t s = -1, p = -1, rp = 0;
+    if (n < t.num) {
+        s = __ldg(t.seq + n);
+        p = __ldg(t.pos + n);
+        rp = __ldg(t.rope_pos + n);
+    }
+    int32_t s1 = __shfl_up_sync(0xffffffffu, s, 1), p1 = __shfl_up_sync(0xffffffffu, p, 1);
+    if (lane == 0) {
+        s1 = n > 0 && n <= t.num ? __ldg(t.seq + n - 1) : -1;
+        p1 = n > 0 && n <= t.num ? __ldg(t.pos + n - 1) : -1;
+    }
+    if (n < t.num) token_ok(t, table, s, p, rp, err);
+    const bool placed = s >= 0 && s < t.num_seqs && p >= 0 &&
+                        (int32_t)t.block.quot((uint32_t)p) < t.max_blocks;
+    const bool on = placed && s1 == s && p1 >= 0 &&
+                    t.block.quot((uint32_t)p1) == t.block.quot((uint32_t)p);
+    const uint32_t starts = __ballot_sync(0xffffffffu, placed && !on);
+    const uint32_t goes_on = __ballot_sync(0xffffffffu, on);
+    if (lane == 0) {
+        w->starts[warp] = starts;
+        w->goes_on[warp] = goes_on;
+    }
+}
+
+// the length of the run that begins at token n0 + at of a window
+__device__ __forceinline__ int32_t run_length(const NewTokens& t, int64_t n0, const Window& w,
+                                              int at) {
+    const int lane = threadIdx.x & 31;
+    int end = at + 1;  // the first token behind it
+    while (end < kWarps * 32) {
+        const uint32_t rest = ~w.goes_on[end >> 5] >> (end & 31);
+        if (rest) return end + __ffs(rest) - 1 - at;
+        end = (end | 31) + 1;
+    }
+    // it may go on behind the window
+    const int32_t s = __ldg(t.seq + n0 + at);
+    const uint32_t pg = t.block.quot((uint32_t)__ldg(t.pos + n0 + at));
+    int32_t len = end - at;
+    for (bool more = true; more;) {
+        bool same[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int64_t n = n0 + at + len + 32 * j + lane;
+            same[j] = false;
+            if (n < t.num) {
+                const int32_t ts = __ldg(t.seq + n), tp = __ldg(t.pos + n);
+                same[j] = ts == s && tp >= 0 && t.block.quot((uint32_t)tp) == pg;
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            if (!more) continue;
+            const uint32_t m = __ballot_sync(0xffffffffu, same[j]);
+            more = m == 0xffffffffu;
+            len += more ? 32 : __ffs(~m) - 1;
+        }
+    }
+    return len;
+}
+
+// the k-th token (from 0) of a window that begins a run, below 0: there are fewer
+__device__ __forceinline__ int nth_start(const Window& w, int k) {
+    for (int i = 0; i < kWarps; ++i) {
+        uint32_t m = w.starts[i];
+        const int n = __popc(m);
+        if (k >= n) {
+            k -= n;
+            continue;
+        }
+        for (; k > 0; --k) m &= m - 1;
+        return 32 * i + __ffs(m) - 1;
+    }
+    return -1;
+}
+
+// `count` times 16 codes times `ratio`, every step-th from `first` on (rare: kept out of
+// the registers of what runs every time)
+__device__ __noinline__ void rescale(unsigned char* codes, int64_t count, float ratio, int first,
+                                     int step) {
+    uint4* const w = reinterpret_cast<uint4*>(codes);
+    for (int64_t i0 = first; i0 < count; i0 += step * 4) {
+        uint4 c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            if (i0 + step * i < count) c[i] = w[i0 + step * i];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (i0 + step * i >= count) continue;
+            uint32_t* y = reinterpret_cast<uint32_t*>(&c[i]);
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                uint32_t lo, hi;
+                e4m3_f16(y[e], lo, hi);
+                const float2 f = __half22float2(*reinterpret_cast<__half2*>(&lo));
+                const float2 g = __half22float2(*reinterpret_cast<__half2*>(&hi));
+                y[e] = e4m3x2(f.x * ratio, f.y * ratio) | e4m3x2(g.x * ratio, g.y * ratio) << 16;
+            }
+            w[i0 + step * i] = c[i];
+        }
+    }
+}
+
+// What a CTA writes: K or V of one head
+struct Head {
+    const unsigned char* rows;  // of the new tokens
+    unsigned char* pool;        // at the head in page 0
+    float* scales;
+    int64_t stride;             // bytes from token to token
+    int64_t page_bytes;
+    uint32_t slot;              // this thread's place in the staging buffer
+    int32_t rot;
+    int u, da, db;              // this lane's unit and its chunks
+};
+
+// The run of `len` tokens from n on, in `page`, written by W warps of which this is
+// the rank-th; W is 1 or all of the CTA's.
+template <int D, bool F32, bool MIX, int W>
+__device__ __forceinline__ void write_run(const Q8WriteArgs& a, const Head& hd, int64_t n,
+                                          int32_t len, int32_t page, int rank, uint32_t* red) {
+    constexpr int U = D / 16, RS = 32 / U;  // lanes per row, rows per step
+    constexpr int step = W * RS;
+    constexpr uint32_t kNext = (F32 ? 4 : 2) * kPiece;  // a thread's next slot
+    const int lane = threadIdx.x & 31;
+    const int cap = step * a.steps;                     // rows held
+    const int32_t r0 = rank * RS + lane / U;            // this lane's first row
+    const int32_t* const pos = a.tok.pos + n;
+    const int32_t* const rope_pos = a.tok.rope_pos + n;
+    const int32_t B = (int32_t)a.tok.block.d;
+    const int32_t p = __ldg(pos);
+    const int32_t p0 = (int32_t)a.tok.block.quot((uint32_t)p) * B;  // the page's first position
+    const int32_t front = p - p0;                                   // rows in front of the run
+    float* const sp = hd.scales + (int64_t)page * a.tok.hkv;
+    const float old = front > 0 ? *sp : 0.f;
+    const bool spins = hd.u < (hd.rot >> 4);
+
+    // the largest of the warps'
+    auto run_max = [&](uint32_t m) {
         m = __reduce_max_sync(0xffffffffu, m);
-        if (a.wr == 1) return m;
-        if (lane == 0) red[turn][warp] = m;
-        asm volatile("bar.sync %0, %1;" ::"r"(1 + team), "r"(a.wr * 32) : "memory");
-        for (int i = 0; i < a.wr; ++i) m = max(m, red[turn][team * a.wr + i]);
-        turn ^= 1;
+        if constexpr (W > 1) {
+            __syncthreads();
+            if (lane == 0) red[rank] = m;
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < W; ++i) m = max(m, red[i]);
+        }
         return m;
     };
-
-    // the run of `len` tokens from n on, on one page of B positions from `p0` on, the
-    // first of them at p
-    auto write_run = [&](int64_t n, int32_t len, int32_t page, int32_t p0, int32_t p) {
-        const int32_t front = p - p0;  // rows of the page in front of the run
-        float* const sp = scales + (int64_t)page * a.tok.hkv + h;
-        const float old = has && front > 0 ? *sp : 0.f;
-        const int cap = a.wr * RS * S;
-        RawUnit<F32> raw[S];
-        auto row = [&](int32_t base, int i) { return base + (i * a.wr + rank) * RS + lane / U; };
-        auto load = [&](int32_t base) {
-#pragma unroll
-            for (int i = 0; i < S; ++i)
-                if (row(base, i) < len && has)
-                    load_unit<F32>(rows + (n + row(base, i)) * stride, da, db, raw[i]);
-        };
-        // this lane's part of row r, rotated, and its place in the page; below 0: none
-        auto value = [&](int32_t r, const RawUnit<F32>& w, float* x) {
-            if (r >= len || !has) return -1;
-            UnitAngles ang;
-            if (a.table.rot) {
-                const int32_t rp = __ldg(a.tok.rope_pos + n + r);
-                if (rp < 0 || rp >= a.table.positions) return -1;
-                if (spins) load_angles(a.table, rp, u, ang);
-            }
-            widen_unit<F32>(w, x);
-            if (spins) rotate_unit<MIX>(x, ang);
-            return __ldg(a.tok.pos + n + r) - p0;
-        };
-        uint32_t top = 0;  // the largest magnitude's bits + 1
-        for (int32_t base = 0; base < len; base += cap) {
-            load(base);
-#pragma unroll
-            for (int i = 0; i < S; ++i) {
-                float x[16];
-                if (value(row(base, i), raw[i], x) < 0) continue;
-                float m = 0.f;
-                // (x + 0 x is NaN for an infinity, and fmaxf takes no notice of NaN)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) m = fmaxf(m, fabsf(fmaf(x[e], 0.f, x[e])));
-                top = max(top, __float_as_uint(m) + 1);
-            }
+    // this lane's parts of the rows from base on
+    auto fetch = [&](int32_t base) {
+        const unsigned char* from = hd.rows + (n + base + r0) * hd.stride;
+        uint32_t slot = hd.slot;
+        for (int32_t r = base + r0; r < min(len, base + cap); r += step) {
+            stage_unit<F32>(slot, from + hd.da * (F32 ? 4 : 2), from + hd.db * (F32 ? 4 : 2));
+            from += step * hd.stride;
+            slot += kNext;
         }
-        top = team_max(top);
-        if (top == 0) return;  // no row to write
-        float s = scale_for(__uint_as_float(top - 1));
-        unsigned char* const head = pool + ((int64_t)page * a.tok.hkv + h) * B * D;
-        if (front > 0) {
-            const float was = scale_up(old);
-            s = was <= s ? s : was;  // (NaN stays)
-            if (s != old) {
-                const float ratio = old * __frcp_rn(s);
-                uint4* const w = reinterpret_cast<uint4*>(head);
-                for (int64_t i = rank * 32 + lane; i < (int64_t)front * (D / 16);
-                     i += a.wr * 32) {
-                    uint4 c = w[i];
-                    uint32_t* y = reinterpret_cast<uint32_t*>(&c);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t lo, hi;
-                        e4m3_f16(y[e], lo, hi);
-                        const float2 f = __half22float2(*reinterpret_cast<__half2*>(&lo));
-                        const float2 g = __half22float2(*reinterpret_cast<__half2*>(&hi));
-                        y[e] = e4m3x2(f.x * ratio, f.y * ratio) |
-                               e4m3x2(g.x * ratio, g.y * ratio) << 16;
-                    }
-                    w[i] = c;
-                }
-            }
-        }
-        // (the team has read the old scale: it met in team_max)
-        if (rank == 0 && lane == 0) *sp = s;
-        const float inv = __frcp_rn(s);
-        for (int32_t base = 0; base < len; base += cap) {
-            if (len > cap) load(base);
-#pragma unroll
-            for (int i = 0; i < S; ++i) {
-                float x[16];
-                const int32_t at = value(row(base, i), raw[i], x);
-                if (at < 0) continue;
-#pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = fmaf(x[e], 0.f, x[e] * inv);  // inf: NaN
-                uint32_t w[4];
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    w[e] = e4m3x2(x[4 * e], x[4 * e + 1]) |
-                           e4m3x2(x[4 * e + 2], x[4 * e + 3]) << 16;
-                unsigned char* const to = head + (int64_t)at * D;
-                *reinterpret_cast<uint2*>(to + da) = make_uint2(w[0], w[1]);
-                *reinterpret_cast<uint2*>(to + db) = make_uint2(w[2], w[3]);
-            }
-        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     };
-
-    for (int64_t base = n0; base < n1; base += 32) {
-        // runs that begin at one of these tokens
-        const int64_t n = base + lane;
-        int32_t s = -1, p = 0;
-        bool starts = false;
-        if (n < n1) {
-            s = __ldg(a.tok.seq + n);
-            p = __ldg(a.tok.pos + n);
-            const int32_t rp = __ldg(a.tok.rope_pos + n);
-            const int32_t s1 = n > 0 ? __ldg(a.tok.seq + n - 1) : -1;
-            const int32_t p1 = n > 0 ? __ldg(a.tok.pos + n - 1) : -1;
-            token_ok(a.tok, a.table, s, p, rp, reports ? a.err : nullptr);
-            starts = s >= 0 && s < a.tok.num_seqs && p >= 0 &&
-                     (int32_t)a.tok.block.quot((uint32_t)p) < a.tok.max_blocks &&
-                     (s1 != s || p1 < 0 ||
-                      a.tok.block.quot((uint32_t)p1) != a.tok.block.quot((uint32_t)p));
-        }
-        uint32_t found = __ballot_sync(0xffffffffu, starts);
-        while (found) {
-            const int bit = __ffs(found) - 1;
-            found &= found - 1;
-            const int32_t rs = __shfl_sync(0xffffffffu, s, bit);
-            const int32_t rp = __shfl_sync(0xffffffffu, p, bit);
-            const int32_t page = token_page(a.tok, rs, rp, reports && lane == 0 ? a.err : nullptr);
-            if (page < 0) continue;
-            const int32_t pg = (int32_t)a.tok.block.quot((uint32_t)rp);
-            // the tokens behind it on the same page: 128 at a time where a page can
-            // hold more than 32
-            int32_t len = 1;
-            for (bool more = true; more;) {
-                bool same[4];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int64_t t = base + bit + len + 32 * i + lane;
-                    same[i] = false;
-                    if ((i == 0 || B > 32) && t < a.tok.num) {
-                        const int32_t ts = __ldg(a.tok.seq + t), tp = __ldg(a.tok.pos + t);
-                        same[i] = ts == rs && tp >= 0 &&
-                                  (int32_t)a.tok.block.quot((uint32_t)tp) == pg;
-                    }
+    // the position that row r is rotated by (0 without a rotation), below 0: none, the
+    // row is not written
+    auto turn_of = [&](int32_t r) {
+        if (!a.table.rot) return 0;
+        const int32_t rp = __ldg(rope_pos + r);
+        return rp < a.table.positions ? rp : -1;
+    };
+    // rotates the rows from base on in place (to odd where bf16 holds them: a further
+    // rounding to 4 bits then gives what one rounding gives); the largest magnitude's
+    // bits + 1
+    auto rotate_rows = [&](int32_t base) {
+        uint32_t top = 0, slot = hd.slot;
+#pragma unroll 1
+        for (int32_t r = base + r0; r < min(len, base + cap); r += step, slot += kNext) {
+            const int32_t rp = turn_of(r);
+            if (rp < 0) continue;
+            UnitAngles ang;
+            if (spins) load_angles(a.table, rp, hd.u, ang);
+            const RawUnit<F32> raw = staged_unit<F32>(slot);
+            float x[16], m = 0.f;  // (the maximum takes no notice of a NaN)
+            if (!F32 && !hd.rot) {
+                m = largest_bf16(raw.a[0], raw.b[0]);
+            } else {
+                widen_unit<F32>(raw, x);
+                if (spins) {
+                    rotate_unit<MIX>(x, ang);
+                    restage_unit<F32>(slot, x);
                 }
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    if (!more || (i > 0 && B <= 32)) continue;
-                    const uint32_t m = __ballot_sync(0xffffffffu, same[i]);
-                    more = m == 0xffffffffu;
-                    len += more ? 32 : __ffs(~m) - 1;
-                }
+                for (int e = 0; e < 16; e += 2) m = fmax3(m, fabsf(x[e]), fabsf(x[e + 1]));
             }
-            write_run(base + bit, len, page, pg * B, rp);
+            top = max(top, __float_as_uint(m) + 1);
+        }
+        return top;
+    };
+    uint32_t top = 0;
+    for (int32_t base = 0; base < len; base += cap) {
+        fetch(base);
+        top = max(top, rotate_rows(base));
+    }
+    top = run_max(top);
+    if (top == 0) return;  // no row to write
+    const bool inf = top - 1 == 0x7f800000u;
+    if (inf) {  // once more over the finite ones
+        top = 1;
+        for (int32_t base = 0; base < len; base += cap) {
+            if (len > cap) {
+                fetch(base);
+                rotate_rows(base);
+            }
+            uint32_t slot = hd.slot;
+#pragma unroll 1
+            for (int32_t r = base + r0; r < min(len, base + cap); r += step, slot += kNext) {
+                float x[16];
+                if (turn_of(r) < 0) continue;
+                widen_unit<F32>(staged_unit<F32>(slot), x);
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    if (fabsf(x[e]) < INFINITY) top = max(top, __float_as_uint(fabsf(x[e])) + 1);
+            }
+        }
+        top = run_max(top);
+    }
+    float s = scale_for(__uint_as_float(top - 1));
+    unsigned char* const head = hd.pool + page * hd.page_bytes;
+    if (front > 0) {
+        const float was = scale_up(old);
+        s = was <= s ? s : was;  // (NaN stays)
+        if (s != old) {
+            const float ratio = old * __frcp_rn(s);
+            rescale(head, (int64_t)front * (D / 16), ratio, rank * 32 + lane, W * 32);
+        }
+    }
+    // (all warps of the run have read the old scale: they met in run_max)
+    if (rank == 0 && lane == 0) *sp = s;
+    const float inv = __frcp_rn(s);
+    for (int32_t base = 0; base < len; base += cap) {
+        if (len > cap) {
+            fetch(base);
+            rotate_rows(base);
+        }
+        uint32_t slot = hd.slot;
+#pragma unroll 1
+        for (int32_t r = base + r0; r < min(len, base + cap); r += step, slot += kNext) {
+            if (turn_of(r) < 0) continue;
+            const int32_t at = __ldg(pos + r) - p0;
+            float x[16];
+            widen_unit<F32>(staged_unit<F32>(slot), x);
+            if (inf) {
+#pragma unroll
+                for (int e = 0; e < 16; ++e) x[e] = fmaf(x[e], 0.f, x[e]);  // to NaN
+            }
+            uint32_t w[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float2 y = fmul2(make_float2(x[4 * e], x[4 * e + 1]), make_float2(inv, inv));
+                const float2 z = fmul2(make_float2(x[4 * e + 2], x[4 * e + 3]),
+                                       make_float2(inv, inv));
+                w[e] = e4m3x2(y.x, y.y) | e4m3x2(z.x, z.y) << 16;
+            }
+            unsigned char* const to = head + (int64_t)at * D;
+            if (hd.db == hd.da + 8) {
+                *reinterpret_cast<uint4*>(to + hd.da) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+                *reinterpret_cast<uint2*>(to + hd.da) = make_uint2(w[0], w[1]);
+                *reinterpret_cast<uint2*>(to + hd.db) = make_uint2(w[2], w[3]);
+            }
         }
     }
 }
 
 template <int D, bool F32, bool MIX>
-__global__ void __launch_bounds__(kWarps * 32, 2) q8_write_kernel(const Q8WriteArgs a) {
+__device__ __forceinline__ void write_runs(const Q8WriteArgs& a, uint32_t cta) {
+    constexpr int U = D / 16, RS = 32 / U;
+    extern __shared__ __align__(16) unsigned char stage[];
+    __shared__ uint32_t red[kWarps];
+    __shared__ Window window;
+    __shared__ int32_t longs[kWarps * 32][3];  // runs that take the whole CTA
+    __shared__ int n_longs;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const bool is_v = cta & 1;
+    const int h = (int)((cta >> 1) % (uint32_t)a.tok.hkv);
+    const uint32_t rest = (cta >> 1) / (uint32_t)a.tok.hkv;
+    const int part = (int)(rest % (uint32_t)a.parts);
+    const int64_t n0 = (int64_t)(rest / (uint32_t)a.parts) * (kWarps * 32);
+    unsigned int* const err = h == 0 && !is_v ? a.err : nullptr;
+    if (threadIdx.x == 0) n_longs = 0;
+    look_at_window(a.tok, a.table, n0, part == 0 ? err : nullptr, &window);
+    __syncthreads();
+    Head hd;
+    hd.rows = static_cast<const unsigned char*>(is_v ? a.v : a.k) + (int64_t)h * D * (F32 ? 4 : 2);
+    hd.stride = (is_v ? a.v_stride : a.k_stride) * (F32 ? 4 : 2);
+    hd.page_bytes = (int64_t)a.tok.hkv * a.tok.block.d * D;
+    hd.pool = (is_v ? a.vc : a.kc) + (int64_t)h * a.tok.block.d * D;
+    hd.scales = (is_v ? a.vs : a.ks) + h;
+    hd.slot = smem_u32(stage) + threadIdx.x * 16;
+    hd.rot = is_v ? 0 : a.table.rot;
+    hd.u = lane % U;
+    unit_dims<MIX>(hd.u, hd.rot, &hd.da, &hd.db);
+    // every parts-th run, one per warp; what a warp does not hold is left for all
+    for (int k = part + warp * a.parts;; k += kWarps * a.parts) {
+        const int first = nth_start(window, k);
+        if (first < 0) break;
+        const int64_t n = n0 + first;
+        const int32_t page = token_page(a.tok, __ldg(a.tok.seq + n), __ldg(a.tok.pos + n),
+                                        lane == 0 ? err : nullptr);
+        if (page < 0) continue;
+        const int32_t len = run_length(a.tok, n0, window, first);
+        if (len > RS * a.steps) {
+            if (lane == 0) {
+                const int at = atomicAdd(&n_longs, 1);
+                longs[at][0] = first;
+                longs[at][1] = len;
+                longs[at][2] = page;
+            }
+        } else {
+            write_run<D, F32, MIX, 1>(a, hd, n, len, page, 0, nullptr);
+        }
+    }
+    __syncthreads();
+    const int total = n_longs;
+    for (int i = 0; i < total; ++i)
+        write_run<D, F32, MIX, kWarps>(a, hd, n0 + longs[i][0], longs[i][1], longs[i][2], warp, red);
+}
+
+template <int D, bool F32, bool MIX>
+__global__ void __launch_bounds__(kWarps * 32, 3) q8_write_kernel(const Q8WriteArgs a) {
     PKV_DEPENDENT_PROLOGUE();
-    if (blockIdx.x < a.kv_ctas) {
-        write_runs<D, F32, MIX>(a);
+    // CTAs of K and V lie among those of the queries, which fill the GPU behind them
+    const uint32_t kv = (uint32_t)min((blockIdx.x * a.kv_step) >> 32, (uint64_t)a.kv_ctas);
+    if (kv < a.kv_ctas && ((blockIdx.x + 1ull) * a.kv_step) >> 32 > kv) {
+        write_runs<D, F32, MIX>(a, kv);
         return;
     }
-    const int64_t id = (int64_t)(blockIdx.x - a.kv_ctas) * kWarps + (threadIdx.x >> 5);
+    const int64_t id = (int64_t)(blockIdx.x - kv) * kWarps + (threadIdx.x >> 5);
     const int64_t n = id / a.q.warps;
     if (n < a.tok.num)
         query_warp<D, F32, MIX>(a.q, a.table, a.tok.seq, a.tok.rope_pos, n,
@@ -335,6 +556,23 @@ __global__ void __launch_bounds__(kReadWarps * 32) q8_read_kernel(const Q8ReadAr
     }
 }
 
+template <int D, bool F32, bool MIX>
+cudaError_t launch_write(const DeviceInfo& dev, const Q8WriteArgs& a, int64_t ctas, size_t smem,
+                         cudaStream_t stream) {
+    auto kern = q8_write_kernel<D, F32, MIX>;
+    // the most shared memory a CTA may have, set once per device
+    static std::atomic<uint64_t> set{0};
+    const uint64_t bit = 1ull << dev.device;
+    if (!(set.load(std::memory_order_relaxed) & bit)) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 most_steps<F32>() * step_bytes<F32>());
+        if (e != cudaSuccess) return e;
+        set.fetch_or(bit, std::memory_order_relaxed);
+    }
+    return launch_dependent(kern, dim3((unsigned)ctas), dim3(kWarps * 32), smem, stream, a);
+}
+
 }  // namespace
 
 cudaError_t launch_q8_write(const DeviceInfo& dev, const RopeWriteLaunch& r, float* k_scale,
@@ -354,29 +592,31 @@ cudaError_t launch_q8_write(const DeviceInfo& dev, const RopeWriteLaunch& r, flo
     a.ks = k_scale;
     a.vs = v_scale;
     a.table = RopeTable{r.cos_sin, r.positions, r.rot};
-    // warps that hold a page's rows of a head, up to a CTA's
-    const int per = 32 / (r.d / 16) * (f32 ? row_steps<true>() : row_steps<false>());
-    a.wr = 1;
-    while (a.wr < kWarps && a.wr * per < r.block_size) a.wr *= 2;
-    const int heads = kWarps / a.wr;
-    a.groups = (r.hkv + heads - 1) / heads;
-    const double all = (double)r.num_tokens * a.groups * 2;
-    a.window = (int32_t)std::min(64.0, std::max(1.0, all / (32.0 * dev.num_sms)));
-    a.kv_ctas = (r.num_tokens + a.window - 1) / a.window * a.groups * 2;
-    int64_t ctas = a.kv_ctas;
+    // steps that a page's rows take of one warp
+    const int rows = 32 / (r.d / 16), most = f32 ? most_steps<true>() : most_steps<false>();
+    a.steps = (int32_t)std::min<int64_t>(most, ((int64_t)r.block_size + rows - 1) / rows);
+    const size_t smem = (size_t)a.steps * (f32 ? step_bytes<true>() : step_bytes<false>());
+    // CTAs that share a window: as many as fill the GPU, but no fewer tokens than warps
+    constexpr int kWindow = kWarps * 32;
+    const int64_t windows = (r.num_tokens + kWindow - 1) / kWindow;
+    const int64_t fill = 3 * dev.num_sms / (windows * r.hkv * 2);
+    a.parts = (int32_t)std::max<int64_t>(
+        1, std::min<int64_t>(fill, (std::min<int64_t>(r.num_tokens, kWindow) + kWarps - 1) / kWarps));
+    const int64_t kv_ctas = windows * a.parts * r.hkv * 2;
+    int64_t ctas = kv_ctas;
     if (r.q) {
         const int32_t w = (int32_t)(f32 ? unit_warps<true>(r.hq, r.d) : unit_warps<false>(r.hq, r.d));
         a.q = RopeQuery{r.q, r.q_out, r.q_stride, r.q_out_stride, r.hq, w};
         ctas += (r.num_tokens * w + kWarps - 1) / kWarps;
     }
     if (ctas > 0x7fffffff) return cudaErrorNotSupported;
+    a.kv_ctas = (uint32_t)kv_ctas;
+    const uint64_t even = (((uint64_t)kv_ctas << 32) + ctas - 1) / ctas;
+    a.kv_step = std::min(2 * even, (uint64_t)1 << 32);
     a.err = r.err;
     cudaError_t e = cudaErrorInvalidValue;
-    auto go = [&](auto kern) {
-        e = launch_dependent(kern, dim3((unsigned)ctas), dim3(kWarps * 32), 0, stream, a);
-    };
 #define PKV_Q8_CASE(DD, FF, MM) \
-    if (r.d == DD && f32 == FF && mix == MM) go(q8_write_kernel<DD, FF, MM>);
+    if (r.d == DD && f32 == FF && mix == MM) e = launch_write<DD, FF, MM>(dev, a, ctas, smem, stream);
     PKV_Q8_CASE(64, false, false) PKV_Q8_CASE(64, false, true)
     PKV_Q8_CASE(64, true, false) PKV_Q8_CASE(64, true, true)
     PKV_Q8_CASE(128, false, false) PKV_Q8_CASE(128, false, true)

@@ -136,6 +136,8 @@ __device__ __forceinline__ void load_angles(const RopeTable& t, int32_t pos, int
     y.s[4] = s1.x; y.s[5] = s1.y; y.s[6] = s1.z; y.s[7] = s1.w;
 }
 
+// (Packed f32x2 products and sums would halve the instructions, but sums of packed products
+// are compiled to fused ones, whatever rounding they ask for.)
 template <bool MIX>
 __device__ __forceinline__ void rotate_unit(float* x, const UnitAngles& t) {
 #pragma unroll
