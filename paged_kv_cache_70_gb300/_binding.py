@@ -1,4 +1,5 @@
-"""ctypes binding of libpagedkv.so (include/pagedkv.h).
+"""Binding of libpagedkv.so (include/pagedkv.h): ctypes, and for the calls on 8-bit pools
+and with the position rotation a compiled module (csrc/binding.cpp).
 
 Argument marshalling only: shapes and dtypes are read from torch tensors,
 device pointers and the current CUDA stream are passed to the C ABI, and a
@@ -9,11 +10,15 @@ for device memory and streams.
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import math
 import os
 import threading
 
 import torch
+
+from . import build
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "_build", "libpagedkv.so")
@@ -970,75 +975,30 @@ def q8_geom_of(k_cache: torch.Tensor, num_heads: int) -> Geom:
     return Geom(num_heads, hkv, d, bs, nb, PKV_Q8)
 
 
-def _scales(index: int, k_cache, v_cache, k_scale, v_scale) -> tuple[int, int]:
-    """The scales' addresses, checked with the pools they belong to."""
-    if v_cache.shape != k_cache.shape or k_scale.shape != k_cache.shape[:2] or \
-            v_scale.shape != k_cache.shape[:2]:
-        raise ValueError("the pools have one shape and the scales are [num_blocks, Hkv]")
-    return (_arg("k_scale", k_scale, index, torch.float32),
-            _arg("v_scale", v_scale, index, torch.float32))
+_native_module = None
 
 
-def _rows(name: str, t: torch.Tensor, index: int, dtype=None) -> tuple[int, int]:
-    """Address and token stride (elements) of rows [N, H, d] whose heads are contiguous."""
-    if t.get_device() != index or index < 0:
-        raise ValueError(f"{name} must be a CUDA tensor" if not t.is_cuda else
-                         f"{name} must be on the device of the other tensors")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-    n, h, d = t.shape
-    sn, sh, sd = t.stride()
-    if n * h * d and ((d > 1 and sd != 1) or (h > 1 and sh != d)):
-        raise ValueError(f"{name}: the heads of a token must be contiguous")
-    return t.data_ptr(), (sn if n > 1 else h * d)
-
-
-def _write_new(func: str, k, v, cos_sin, block_table, token_seq, token_pos, q, q_out, rope_pos,
-               interleaved, hkv, d, tail, geom):
-    """The arguments that paged_kv_write_rope and paged_kv_write_q8 share; returns q_out."""
-    index = k.get_device()
-    n = k.shape[0]
-    if k.shape != v.shape or k.shape[1:] != (hkv, d):
-        raise ValueError("shape mismatch between k/v rows and the pools")
-    if token_seq.numel() != n or token_pos.numel() != n or \
-            (rope_pos is not None and rope_pos.numel() != n):
-        raise ValueError("token_seq, token_pos and rope_pos must have one entry per token row")
-    rows, width = block_table.shape
-    if max(rows, width, n) > _INT32:
-        raise ValueError("tokens and the table's rows and columns are 32-bit")
-    i32 = torch.int32
-    code = _dtype_code(k)
-    kp, ks = _rows("k", k, index)
-    vp, vs = _rows("v", v, index, k.dtype)
-    rope, hq = None, hkv
-    if cos_sin is None:
-        if q is not None or q_out is not None or rope_pos is not None:
-            raise ValueError("q, q_out and rope_pos go with cos_sin")
-    else:
-        if cos_sin.dim() != 2 or max(cos_sin.shape) > _INT32:
-            raise ValueError("cos_sin must be [positions, rotary_dim]")
-        rope = Rope(cos_sin=_arg("cos_sin", cos_sin, index, torch.float32),
-                    num_positions=cos_sin.shape[0], rotary_dim=cos_sin.shape[1],
-                    interleaved=1 if interleaved else 0,
-                    positions=None if rope_pos is None else _arg("rope_pos", rope_pos, index, i32))
-        if q is not None:
-            if q.dim() != 3 or q.shape[0] != n or q.shape[2] != d or q.shape[1] > _INT32:
-                raise ValueError("q must be [N, Hq, d]")
-            hq = q.shape[1]
-            rope.q, rope.q_stride = _rows("q", q, index, k.dtype)
-            if q_out is None:
-                q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
-            elif q_out.shape != q.shape:
-                raise ValueError("q_out must have q's shape")
-            rope.q_out, rope.q_out_stride = _rows("q_out", q_out, index, k.dtype)
-        elif q_out is not None:
-            raise ValueError("q_out goes with q")
-    load_library()
-    _launch(func, index, kp, ks, vp, vs, code, None if rope is None else ctypes.byref(rope),
-            _arg("block_table", block_table, index, i32), width, rows,
-            _arg("token_seq", token_seq, index, i32), _arg("token_pos", token_pos, index, i32), n,
-            *tail, geom(hq))
-    return q_out
+def _native():
+    """The compiled half of the calls below (csrc/binding.cpp), with the library's entry
+    points."""
+    global _native_module
+    if _native_module is None:
+        lib = load_library()
+        with _lock:
+            if _native_module is None:
+                path = build.binding_path()
+                if not os.path.exists(path):
+                    raise RuntimeError(f"{os.path.basename(path)} not found beside {LIB_PATH}; "
+                                       "build it with `python -m paged_kv_cache_70_gb300.build`")
+                loader = importlib.machinery.ExtensionFileLoader("_pagedkv", path)
+                spec = importlib.util.spec_from_loader("_pagedkv", loader)
+                m = importlib.util.module_from_spec(spec)
+                loader.exec_module(m)
+                m.bind(_check, *(ctypes.cast(getattr(lib, n), ctypes.c_void_p).value for n in (
+                    "paged_kv_write_rope", "paged_kv_write_q8", "paged_kv_read_q8",
+                    "paged_decode_q8", "paged_decode_q8_workspace_size")))
+                _native_module = m
+    return _native_module
 
 
 def paged_kv_write_rope(k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor,
@@ -1051,21 +1011,9 @@ def paged_kv_write_rope(k: torch.Tensor, v: torch.Tensor, cos_sin: torch.Tensor,
     on the way by rope_pos (token_pos where None); cos_sin [positions, rotary_dim]
     holds each position's cosines, then its sines.  The heads of a token are
     contiguous in k, v, q and q_out, the tokens may be strided."""
-    index = k.get_device()
-    nb, bs, hkv, d = k_cache.shape
-    if v_cache.shape != k_cache.shape or max(bs, hkv, d) > _INT32:
-        raise ValueError("shape mismatch between the pools")
-    if slot_mapping_out is not None and slot_mapping_out.numel() != k.shape[0]:
-        raise ValueError("slot_mapping_out must have one entry per token row")
-    if cos_sin is None:
-        raise ValueError("cos_sin is needed (paged_kv_write_positions writes without it)")
-    code = _dtype_code(k_cache)
-    tail = (None if slot_mapping_out is None else
-            _arg("slot_mapping_out", slot_mapping_out, index, torch.int32),
-            _arg("k_cache", k_cache, index), _arg("v_cache", v_cache, index, k_cache.dtype))
-    return _write_new("paged_kv_write_rope", k, v, cos_sin, block_table, token_seq, token_pos, q,
-                      q_out, rope_pos, interleaved, hkv, d, tail,
-                      lambda hq: _geom(hq, hkv, d, bs, nb, code))
+    return (_native_module or _native()).write(
+        k, v, cos_sin, block_table, token_seq, token_pos, k_cache, v_cache, None, None, q, q_out,
+        rope_pos, interleaved, slot_mapping_out)
 
 
 def paged_kv_write_q8(k: torch.Tensor, v: torch.Tensor, block_table: torch.Tensor,
@@ -1078,13 +1026,9 @@ def paged_kv_write_q8(k: torch.Tensor, v: torch.Tensor, block_table: torch.Tenso
     (q8_cache_shape) at their positions, with the pages' scales; the tokens of one
     page follow one another.  With cos_sin, k and q are rotated first, as in
     paged_kv_write_rope."""
-    index = k.get_device()
-    nb, hkv, bs, d = _q8_shape(k_cache)
-    tail = (_arg("k_cache", k_cache, index), _arg("v_cache", v_cache, index, k_cache.dtype),
-            *_scales(index, k_cache, v_cache, k_scale, v_scale))
-    return _write_new("paged_kv_write_q8", k, v, cos_sin, block_table, token_seq, token_pos, q,
-                      q_out, rope_pos, interleaved, hkv, d, tail,
-                      lambda hq: _geom(hq, hkv, d, bs, nb, PKV_Q8))
+    return (_native_module or _native()).write(
+        k, v, cos_sin, block_table, token_seq, token_pos, k_cache, v_cache, k_scale, v_scale, q,
+        q_out, rope_pos, interleaved, None)
 
 
 def paged_kv_read_q8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torch.Tensor,
@@ -1093,44 +1037,16 @@ def paged_kv_read_q8(k_cache: torch.Tensor, v_cache: torch.Tensor, k_scale: torc
                      v_out: torch.Tensor | None = None) -> tuple[torch.Tensor, torch.Tensor]:
     """The values [N, Hkv, d] that 8-bit pools hold at slot_mapping [N], in
     ``dtype`` (fp32 or bf16); rows of zeros at negative slots."""
-    index = k_cache.get_device()
-    nb, hkv, bs, d = _q8_shape(k_cache)
-    n = slot_mapping.numel()
-    shape = (n, hkv, d)
-    if k_out is None:
-        k_out = torch.empty(shape, dtype=dtype, device=k_cache.device)
-    if v_out is None:
-        v_out = torch.empty(shape, dtype=k_out.dtype, device=k_cache.device)
-    if k_out.shape != shape or v_out.shape != shape:
-        raise ValueError("k_out / v_out must be [N, Hkv, d]")
-    load_library()
-    _launch("paged_kv_read_q8", index, _arg("k_cache", k_cache, index),
-            _arg("v_cache", v_cache, index, k_cache.dtype),
-            *_scales(index, k_cache, v_cache, k_scale, v_scale),
-            _arg("slot_mapping", slot_mapping, index, torch.int32), n,
-            _arg("k_out", k_out, index), _arg("v_out", v_out, index, k_out.dtype),
-            _dtype_code(k_out), _geom(hkv, hkv, d, bs, nb, PKV_Q8))
-    return k_out, v_out
-
-
-def _decode_q8_size(index: int, batch: int, code: int, *geom) -> int:
-    """paged_decode_q8_workspace_size on device `index`, looked up after the first."""
-    key = (index, batch, code) + geom
-    need = _sizes.get(key)
-    if need is None:
-        if len(_sizes) > 1000:
-            _sizes.clear()
-        with torch.cuda.device(index):
-            need = _sizes[key] = int(load_library().paged_decode_q8_workspace_size(
-                batch, code, _geom(*geom)))
-    return need
+    return (_native_module or _native()).read_q8(k_cache, v_cache, k_scale, v_scale, slot_mapping,
+                                                 dtype, k_out, v_out)
 
 
 def paged_decode_q8_workspace_size(batch: int, q_heads: int, q_dtype: torch.dtype,
                                    k_cache: torch.Tensor) -> int:
-    nb, hkv, bs, d = _q8_shape(k_cache)
+    g = q8_geom_of(k_cache, q_heads)
     code = _dtype_code(torch.empty(0, dtype=q_dtype))
-    return _decode_q8_size(k_cache.get_device(), batch, code, q_heads, hkv, d, bs, nb, PKV_Q8)
+    with torch.cuda.device(k_cache.device):
+        return int(load_library().paged_decode_q8_workspace_size(batch, code, ctypes.byref(g)))
 
 
 def paged_decode_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
@@ -1140,29 +1056,6 @@ def paged_decode_q8(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tenso
                     workspace: torch.Tensor | None = None) -> torch.Tensor:
     """One query token per sequence (q [batch, Hq, d], fp32 or bf16) over its
     cache_seqlens[b] keys in 8-bit pools."""
-    index = q.get_device()
-    batch, hq, d = q.shape
-    nb, hkv, bs, dk = _q8_shape(k_cache)
-    rows, width = block_table.shape
-    if d != dk or rows < batch or cache_seqlens.numel() < batch:
-        raise ValueError("shape mismatch")
-    if max(batch, width, hq) > _INT32:
-        raise ValueError("q and a table's row hold 2^31 - 1 entries at most")
-    if out is None:
-        out = torch.empty_like(q)
-    elif out.shape != q.shape:
-        raise ValueError("out must have q's shape")
-    code = _dtype_code(q)
-    args = (_arg("q", q, index), code, _arg("k_cache", k_cache, index),
-            _arg("v_cache", v_cache, index, k_cache.dtype),
-            *_scales(index, k_cache, v_cache, k_scale, v_scale),
-            _arg("block_table", block_table, index, torch.int32), width,
-            _arg("cache_seqlens", cache_seqlens, index, torch.int32), batch,
-            1.0 / math.sqrt(d) if scale is None else scale, _arg("out", out, index, q.dtype))
-    if workspace is None:
-        need = _decode_q8_size(index, batch, code, hq, hkv, d, bs, nb, PKV_Q8)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    load_library()
-    _launch("paged_decode_q8", index, *args, _arg("workspace", workspace, index),
-            workspace.numel() * workspace.element_size(), _geom(hq, hkv, d, bs, nb, PKV_Q8))
-    return out
+    return (_native_module or _native()).decode_q8(q, k_cache, v_cache, k_scale, v_scale,
+                                                   block_table, cache_seqlens, scale, out,
+                                                   workspace)

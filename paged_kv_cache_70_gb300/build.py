@@ -6,6 +6,8 @@
 ``prefill.cu`` are not units of their own: ``step.cu`` includes them, so that
 its one-launch step kernel can run their CTA functions.  The CUDA runtime is
 linked statically, so the library needs only the NVIDIA driver at run time.
+``binding.cpp`` becomes a Python extension module beside the library (g++, with the
+headers of the installed torch).
 """
 from __future__ import annotations
 
@@ -14,6 +16,7 @@ import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
@@ -48,12 +51,49 @@ def _stale(target: str, deps: list[str]) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def binding_path() -> str:
+    """The compiled half of the Python binding, for this Python and torch."""
+    import torch
+    tag = f"cp{sys.version_info[0]}{sys.version_info[1]}-torch{torch.__version__}"
+    return os.path.join(BUILD, f"_pagedkv.{tag}.so")
+
+
+def build_binding(force: bool = False) -> str:
+    """csrc/binding.cpp against the installed torch (g++; no CUDA code in it)."""
+    import torch
+    src = os.path.join(CSRC, "binding.cpp")
+    out = binding_path()
+    if not force and not _stale(out, [src, os.path.join(INCLUDE, "pagedkv.h")]):
+        return out
+    os.makedirs(BUILD, exist_ok=True)
+    root = os.path.dirname(torch.__file__)
+    nvcc = os.path.realpath(shutil.which("nvcc") or "/usr/local/cuda/bin/nvcc")
+    cuda = os.path.join(os.path.dirname(os.path.dirname(nvcc)), "include")
+    cxx = shutil.which("g++")
+    if not cxx:
+        raise RuntimeError("g++ not found: it is required to build the Python binding")
+    tmp = out + f".tmp{os.getpid()}"
+    cmd = [cxx, "-O2", "-std=c++20", "-fPIC", "-shared", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           "-isystem", os.path.join(root, "include"),
+           "-isystem", os.path.join(root, "include", "torch", "csrc", "api", "include"),
+           "-isystem", sysconfig.get_paths()["include"], "-isystem", cuda, src, "-o", tmp,
+           "-L" + os.path.join(root, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout + r.stderr)
+        raise RuntimeError(f"g++ failed: {' '.join(cmd)}")
+    os.replace(tmp, out)
+    return out
+
+
 def build(force: bool = False, verbose: bool = False, extra: tuple[str, ...] = ()) -> str:
     os.makedirs(BUILD, exist_ok=True)
     nvcc = _nvcc()
     headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC)
                if f.endswith((".cuh", ".h")) or f in INCLUDED]
     headers.append(os.path.join(INCLUDE, "pagedkv.h"))
+    binding = cf.ThreadPoolExecutor(max_workers=1).submit(build_binding, force)
     objs, jobs = [], []
     for src in sources():
         obj = os.path.join(BUILD, os.path.basename(src)[:-3] + ".o")
@@ -80,6 +120,7 @@ def build(force: bool = False, verbose: bool = False, extra: tuple[str, ...] = (
             sys.stderr.write(r.stdout + r.stderr)
             raise RuntimeError("link of libpagedkv.so failed")
         os.replace(tmp, LIB)
+    binding.result()
     return LIB
 
 

@@ -191,3 +191,28 @@ def test_oracle_write_keeps_what_the_header_promises():
         err = np.abs(got[page, :, n % 16] - x[n])
         assert np.all(err <= np.maximum(2.0 ** -4 * np.abs(x[n]), 2.0 ** -10 * s)
                       + 2.0 ** -10 * s * grew[page][:, None])
+
+
+def test_compiled_binding_fails_loudly_without_its_module(lib, monkeypatch, tmp_path):
+    from paged_kv_cache_70_gb300 import _binding
+    monkeypatch.setattr(_binding, "_native_module", None)
+    monkeypatch.setattr(build, "binding_path", lambda: str(tmp_path / "missing.so"))
+    with pytest.raises(RuntimeError, match="not found"):
+        pkv.paged_decode_q8(*[torch.zeros(1)] * 7)
+
+
+def test_compiled_binding_checks_its_arguments(lib):
+    from paged_kv_cache_70_gb300 import _binding
+    m = _binding._native()
+    for f in (m.write, m.read_q8, m.decode_q8, m.bind):
+        with pytest.raises(TypeError):
+            f()
+    t = torch.zeros(1)
+    with pytest.raises(TypeError):  # no tensor
+        m.decode_q8(None, *[t] * 9)
+    with pytest.raises(ValueError):  # not on a GPU
+        m.decode_q8(*[t] * 7, None, None, None)
+    with pytest.raises(ValueError):
+        m.read_q8(*[t] * 5, torch.float32, None, None)
+    with pytest.raises(ValueError):
+        m.bind(print, 0, 0, 0, 0, 0)
