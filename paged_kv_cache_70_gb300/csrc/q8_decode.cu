@@ -88,7 +88,7 @@ struct Q8DecodeArgs {
     int32_t wh;      // warps that share a head and its queries (16 of a tile's keys each)
     int32_t piece;   // keys per copy
     int32_t stages;
-    FastDiv block;   // by the page size
+    FastDiv block, tile;  // by the page size, and by a tile's keys
 };
 
 // One stage's description, written by the producer of its K
@@ -168,15 +168,14 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     const uint32_t half_bytes = (uint32_t)(a.hc * T * D);  // K (or V) of a stage
     const int active = units * a.wh;  // consumer warps at work
-    if (tid == 0) {
-        for (int s = 0; s < S; ++s) {
-            mbar_init(&full[s], 2);  // a K and a V producer
-            mbar_init(&empty[s], active);
-        }
+    if (tid < S) {
+        mbar_init(&full[tid], 2);  // a K and a V producer
+        mbar_init(&empty[tid], active);
+    } else if (tid == kMaxStages) {
         mbar_init(&merge_bar[0], units * (a.wh - 1) + 1);
         mbar_init(&merge_bar[1], units);
-        fence_barrier_init();
     }
+    fence_barrier_init();
     if (tid >= WC * 32 && tid < WC * 32 + 64 && lane == 0)  // the producers' first K and V maps
         asm volatile("prefetch.tensormap [%0];" ::"l"(
                          reinterpret_cast<uint64_t>(tid == WC * 32 ? &kmap : &vmap))
@@ -187,33 +186,53 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
     const int64_t cap = (int64_t)a.max_blocks * a.block_size;
     const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0;
     {
-        constexpr int N = threads<F32>();
-        const int per = (a.batch + N - 1) / N;
-        const int lo = tid * per, hi = min(lo + per, a.batch);
-        int32_t sum = 0;
-        for (int b = lo; b < hi; ++b) {
+        // (what comes next, the table, is on its way meanwhile: 64 KB of it at most)
+        const int64_t line = (int64_t)tid * 128;
+        if (line < (int64_t)a.batch * a.max_blocks * 4)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(
+                reinterpret_cast<const unsigned char*>(a.table) + line));
+        auto tiles = [&](int b) {
             const int32_t L = __ldg(a.seqlens + b);
             if (first_cta && (L < 0 || L > cap)) flag_error(a.err, PKV_FLAG_BAD_LENGTH);
             const int32_t n = (int32_t)min((int64_t)max(L, 0), cap);
-            tstart[b + 1] = (n + T - 1) / T;
-            sum += tstart[b + 1];
-        }
-        int32_t inc = sum;
+            return (int32_t)a.tile.quot((uint32_t)(n + T - 1));
+        };
+        auto scan = [&](int32_t x) {
 #pragma unroll
-        for (int off = 1; off < 32; off <<= 1) {
-            const int32_t y = __shfl_up_sync(0xffffffffu, inc, off);
-            if (lane >= off) inc += y;
+            for (int off = 1; off < 32; off <<= 1) {
+                const int32_t y = __shfl_up_sync(0xffffffffu, x, off);
+                if (lane >= off) x += y;
+            }
+            return x;
+        };
+        if (a.batch <= 32) {  // one warp's work
+            if (warp == 0) {
+                const int32_t x = scan(lane < a.batch ? tiles(lane) : 0);
+                if (lane < a.batch) tstart[lane + 1] = x;
+                if (lane == 0) tstart[0] = 0;
+            }
+            __syncthreads();
+        } else {
+            constexpr int N = threads<F32>();
+            const int per = (a.batch + N - 1) / N;
+            const int lo = tid * per, hi = min(lo + per, a.batch);
+            int32_t sum = 0;
+            for (int b = lo; b < hi; ++b) {
+                tstart[b + 1] = tiles(b);
+                sum += tstart[b + 1];
+            }
+            const int32_t inc = scan(sum);
+            if (lane == 31) warp_sum[warp] = inc;
+            __syncthreads();
+            int32_t run = inc - sum;
+            for (int w = 0; w < warp; ++w) run += warp_sum[w];
+            for (int b = lo; b < hi; ++b) {
+                run += tstart[b + 1];
+                tstart[b + 1] = run;
+            }
+            if (tid == 0) tstart[0] = 0;
+            __syncthreads();
         }
-        if (lane == 31) warp_sum[warp] = inc;
-        __syncthreads();
-        int32_t run = inc - sum;
-        for (int w = 0; w < warp; ++w) run += warp_sum[w];
-        for (int b = lo; b < hi; ++b) {
-            run += tstart[b + 1];
-            tstart[b + 1] = run;
-        }
-        if (tid == 0) tstart[0] = 0;
-        __syncthreads();
     }
     const int32_t total = tstart[a.batch];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
@@ -809,6 +828,7 @@ cudaError_t launch_q8_decode(const DeviceInfo& dev, const Q8DecodePlan& p, const
     a.piece = p.piece;
     a.stages = p.stages;
     a.block = FastDiv((uint32_t)block_size);
+    a.tile = FastDiv((uint32_t)p.tile);
     CUtensorMap kmap, vmap;
     if (!pool_map(&kmap, k_cache, num_blocks, hkv, block_size, d, p.piece, p.hc) ||
         !pool_map(&vmap, v_cache, num_blocks, hkv, block_size, d, p.piece, p.hc))
