@@ -303,6 +303,7 @@ struct Q8DecodePlan {
     int ctas;         // grid.x (CTAs along the keys)
     int tile;         // keys per stage
     int piece;        // keys per copy (divides the tile and the page)
+    bool whole;       // a CTA per sequence and head group, no partial states
     int stages;
     size_t smem_bytes;
     size_t ws_bytes;  // workspace bytes needed (the same for every max_blocks)

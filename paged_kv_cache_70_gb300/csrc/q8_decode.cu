@@ -30,6 +30,8 @@
 //    swizzle (d = 64: 64-byte) so that a fragment's loads touch all banks once; the
 //    other warps own a (head, 8 queries) and 16 of the tile's keys each and hold a
 //    stage for their loads only.
+//    Short sequences that need no splitting (plan_q8_decode) are a CTA's each, which
+//    writes the output itself.
 //  * Keys of a page outside the pool are skipped and flagged; rows past the length
 //    never enter: scores of -inf, V codes and scales of 0, whatever the page holds
 //    there.  Every wait is time-limited.
@@ -79,6 +81,7 @@ struct Q8DecodeArgs {
     float* part_o;     // [ctas + batch][hq][D]
     float* part_ml;    // [ctas + batch][hq][2]
     int32_t* tstart;   // [batch + 1]
+    void* out;         // WHOLE
     unsigned int* err;
     int64_t num_blocks;
     float qscale;  // scale * log2(e)
@@ -140,10 +143,14 @@ __device__ __forceinline__ uint32_t swizzle(uint32_t off) {
     return D == 128 ? (off >> 3) & 0x70u : (off >> 3) & 0x30u;
 }
 
-template <int D, bool F32>
+template <int D, bool F32, bool WHOLE>
 __global__ void __launch_bounds__(threads<F32>(), 1)
 q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap) {
+    // WHOLE: the CTA's only sequence is blockIdx.x
+    const int batch = WHOLE ? 1 : a.batch;
+    const int32_t* const seqlens = a.seqlens + (WHOLE ? blockIdx.x : 0);
+    const int32_t* const table = a.table + (WHOLE ? (int64_t)blockIdx.x * a.max_blocks : 0);
     constexpr int WC = consumers<F32>();
     constexpr int PARTS = F32 ? 2 : 1;
     constexpr int KW = D / 16;   // words of K codes per lane and row: 16-dim steps
@@ -155,7 +162,7 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
     uint64_t* merge_bar = empty + kMaxStages;  // [2]
     Tag* tags = reinterpret_cast<Tag*>(smem + 256);
     int32_t* tstart = reinterpret_cast<int32_t*>(smem + kHeader);
-    unsigned char* scratch = smem + kHeader + up((size_t)(a.batch + 1) * 4, 128);
+    unsigned char* scratch = smem + kHeader + up((size_t)(batch + 1) * 4, 128);
     const int units = a.hc * a.no;  // (head, 8 queries) of the CTA
     const int S = a.stages, T = 16 * a.wh, P = a.piece;
     const int pieces = T / P;
@@ -184,15 +191,15 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
 
     // ---- plan: tile starts of the sequences (an exclusive scan of their tiles)
     const int64_t cap = (int64_t)a.max_blocks * a.block_size;
-    const bool first_cta = blockIdx.x == 0 && blockIdx.y == 0;
+    const bool first_cta = (WHOLE || blockIdx.x == 0) && blockIdx.y == 0;
     {
         // (what comes next, the table, is on its way meanwhile: 64 KB of it at most)
         const int64_t line = (int64_t)tid * 128;
-        if (line < (int64_t)a.batch * a.max_blocks * 4)
+        if (line < (int64_t)batch * a.max_blocks * 4)
             asm volatile("prefetch.global.L2 [%0];" ::"l"(
-                reinterpret_cast<const unsigned char*>(a.table) + line));
+                reinterpret_cast<const unsigned char*>(table) + line));
         auto tiles = [&](int b) {
-            const int32_t L = __ldg(a.seqlens + b);
+            const int32_t L = __ldg(seqlens + b);
             if (first_cta && (L < 0 || L > cap)) flag_error(a.err, PKV_FLAG_BAD_LENGTH);
             const int32_t n = (int32_t)min((int64_t)max(L, 0), cap);
             return (int32_t)a.tile.quot((uint32_t)(n + T - 1));
@@ -205,17 +212,17 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
             }
             return x;
         };
-        if (a.batch <= 32) {  // one warp's work
+        if (WHOLE || batch <= 32) {  // one warp's work
             if (warp == 0) {
-                const int32_t x = scan(lane < a.batch ? tiles(lane) : 0);
-                if (lane < a.batch) tstart[lane + 1] = x;
+                const int32_t x = scan(lane < batch ? tiles(lane) : 0);
+                if (lane < batch) tstart[lane + 1] = x;
                 if (lane == 0) tstart[0] = 0;
             }
             __syncthreads();
         } else {
             constexpr int N = threads<F32>();
-            const int per = (a.batch + N - 1) / N;
-            const int lo = tid * per, hi = min(lo + per, a.batch);
+            const int per = (batch + N - 1) / N;
+            const int lo = tid * per, hi = min(lo + per, batch);
             int32_t sum = 0;
             for (int b = lo; b < hi; ++b) {
                 tstart[b + 1] = tiles(b);
@@ -234,15 +241,25 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
             __syncthreads();
         }
     }
-    const int32_t total = tstart[a.batch];
+    const int32_t total = tstart[batch];
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (first_cta)  // for the combine, which reads them behind its wait
-        for (int b = tid; b <= a.batch; b += blockDim.x) a.tstart[b] = tstart[b];
-    const int32_t len = share_len(total, a.batch, gridDim.x);
-    const int32_t t0 = share_first(tstart, a.batch, (int64_t)blockIdx.x * len);
-    const int32_t t1 = share_first(tstart, a.batch, (int64_t)(blockIdx.x + 1) * len);
-    if (t0 >= t1) return;
     const int head0 = blockIdx.y * a.hc;
+    int32_t t0 = 0, t1 = total;
+    if constexpr (WHOLE) {
+        if (total == 0) {  // no keys
+            const int64_t at = ((int64_t)blockIdx.x * a.hq + head0 * (a.hq / a.hkv)) * D;
+            uint32_t* const o = static_cast<uint32_t*>(a.out) + (F32 ? at : at / 2);
+            for (int i = tid; i < a.hc * (a.hq / a.hkv) * D / (F32 ? 1 : 2); i += blockDim.x) o[i] = 0u;
+            return;
+        }
+    } else {
+        if (first_cta)  // for the combine, which reads them behind its wait
+            for (int b = tid; b <= batch; b += blockDim.x) a.tstart[b] = tstart[b];
+        const int32_t len = share_len(total, batch, gridDim.x);
+        t0 = share_first(tstart, batch, (int64_t)blockIdx.x * len);
+        t1 = share_first(tstart, batch, (int64_t)(blockIdx.x + 1) * len);
+        if (t0 >= t1) return;
+    }
 
     if (warp >= WC) {
         // ------------------------------ producers -----------------------------
@@ -261,13 +278,13 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
         const uint32_t inv_hc = 65536u / a.hc + 1;  // i / hc for i < 512, hc <= 16
         const int32_t tf = t0 + (warp - WC) / 2;
         if (tf >= t1) return;
-        int b = share_seq(tstart, a.batch, tf);  // the sequence of tile t
-        int32_t L = (int32_t)min((int64_t)max(__ldg(a.seqlens + b), 0), cap);
+        int b = share_seq(tstart, batch, tf);  // the sequence of tile t
+        int32_t L = (int32_t)min((int64_t)max(__ldg(seqlens + b), 0), cap);
         // the page of this lane's piece of the 32 from piece c0 on
         auto fetch = [&](int bb, int32_t p0, int32_t p1, int c0) {
             const int32_t p = p0 + (c0 + lane) * P;
             return c0 + lane < pieces && p < p1
-                       ? __ldg(a.table + (int64_t)bb * a.max_blocks + a.block.quot((uint32_t)p))
+                       ? __ldg(table + (int64_t)bb * a.max_blocks + a.block.quot((uint32_t)p))
                        : -1;
         };
         int32_t p0 = (tf - tstart[b]) * T, p1 = min(L, p0 + T);
@@ -282,7 +299,7 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
             if (t + prods < t1) {  // the next tile's sequence and pages
                 if (t + prods >= tstart[b + 1]) {
                     do ++b; while (tstart[b + 1] <= t + prods);
-                    L = (int32_t)min((int64_t)max(__ldg(a.seqlens + b), 0), cap);
+                    L = (int32_t)min((int64_t)max(__ldg(seqlens + b), 0), cap);
                 }
                 p0 = (t + prods - tstart[b]) * T;
                 p1 = min(L, p0 + T);
@@ -419,7 +436,7 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
         if (r < nq) {
 #pragma unroll
             for (int w = 0; w < KW; w += F32 ? 1 : 2) {
-                const int64_t at = ((int64_t)seq * a.hq + qh0 + r) * D + 16 * c + (w & 3) * 4 +
+                const int64_t at = ((int64_t)(WHOLE ? blockIdx.x : seq) * a.hq + qh0 + r) * D + 16 * c + (w & 3) * 4 +
                                    (w >= 4 ? 64 : 0);
                 if constexpr (F32) {
                     const float4 u =
@@ -470,7 +487,7 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
 
     int s = 0;
     uint32_t phase = 0;    // of stage s
-    int seq = share_seq(tstart, a.batch, t0) - 1;  // sequence of tile k
+    int seq = share_seq(tstart, batch, t0) - 1;  // sequence of tile k
     int32_t next = 0;      // the tile that the next one begins with
     for (int32_t k = 0; k < n_tiles; ++k) {
         if (k == next) {  // (before the wait: the first queries come with the first tile)
@@ -532,7 +549,7 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                 const int at = rank * 16 + key;
                 if (at >= tag.rows) return false;
                 if (tag.bad < 0) return true;
-                const int32_t id = __ldg(a.table + (int64_t)seq * a.max_blocks +
+                const int32_t id = __ldg(table + (int64_t)seq * a.max_blocks +
                                          (tag.bad + at) / a.block_size);
                 return id >= 0 && id < a.num_blocks;
             };
@@ -699,6 +716,25 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
             ++merges;
         }
         if (rank != 0) continue;
+        if constexpr (WHOLE) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                if (2 * c + i >= nq) continue;
+                const float inv = l2[i] == 0.f ? 0.f : 1.f / l2[i];
+                const int64_t at = ((int64_t)blockIdx.x * a.hq + qh0 + 2 * c + i) * D + D / 8 * r;
+#pragma unroll
+                for (int x = 0; x < D / 8; x += 4) {
+                    const float4 y = make_float4(val[i][x] * inv, val[i][x + 1] * inv,
+                                                 val[i][x + 2] * inv, val[i][x + 3] * inv);
+                    if constexpr (F32)
+                        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + x) = y;
+                    else
+                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at + x) =
+                            make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+                }
+            }
+            continue;
+        }
         const int64_t slot = (int64_t)blockIdx.x + seq;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -713,10 +749,10 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
     }
 }
 
-template <int D, bool F32>
+template <int D, bool F32, bool WHOLE>
 cudaError_t launch_split(const DeviceInfo& dev, const Q8DecodePlan& p, const Q8DecodeArgs& a,
                          const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
-    auto kern = q8_split_kernel<D, F32>;
+    auto kern = q8_split_kernel<D, F32, WHOLE>;
     // the most shared memory a CTA may have, set once per device
     static std::atomic<uint64_t> set{0};
     const uint64_t bit = 1ull << dev.device;
@@ -727,8 +763,8 @@ cudaError_t launch_split(const DeviceInfo& dev, const Q8DecodePlan& p, const Q8D
         if (e != cudaSuccess) return e;
         set.fetch_or(bit, std::memory_order_relaxed);
     }
-    return launch_dependent(kern, dim3(p.ctas, p.head_groups), dim3(threads<F32>()), p.smem_bytes,
-                            stream, a, kmap, vmap);
+    return launch_dependent(kern, dim3(WHOLE ? a.batch : p.ctas, p.head_groups),
+                            dim3(threads<F32>()), p.smem_bytes, stream, a, kmap, vmap);
 }
 
 // the pool as (dim, token, page and head), boxes of `piece` tokens of `hc` heads
@@ -787,6 +823,13 @@ bool plan_q8_decode(const DeviceInfo& dev, int32_t batch, int32_t max_blocks, in
     const int64_t most = std::max(1, dev.num_sms / p->head_groups);
     if (tiles + batch > 0x7fffffffLL - most) return false;  // the line of tiles is 32 bits long
     p->ctas = (int)std::max<int64_t>(1, std::min(most, tiles));
+    // Sequences that the table keeps short, no more than there are SMs: a CTA takes all of
+    // one (and its heads), and no second kernel is needed.  At 16 / 8 heads, d = 128, 48 keys
+    // per tile, whole and split: one sequence of 40 keys 8.2 and 10.3 us, 180 keys 10.0 and
+    // 10.3, 380 keys 12.3 and 10.3; 64 sequences of 90 keys 8.6 and 14.7, 760 keys 22.6 and
+    // 25.6, 1500 keys 35.5 and 35.5.
+    const int64_t whole = (int64_t)batch * p->head_groups;
+    p->whole = tiles <= (4 + 12 * whole / dev.num_sms) * batch && whole <= dev.num_sms;
     const size_t slots = (size_t)most + batch;  // whatever the table's width is
     p->ws_bytes = up((size_t)(batch + 1) * 4, 256) + up(slots * hq * 2 * 4, 256) +
                   up(slots * hq * d * 4, 256);
@@ -833,13 +876,16 @@ cudaError_t launch_q8_decode(const DeviceInfo& dev, const Q8DecodePlan& p, const
     if (!pool_map(&kmap, k_cache, num_blocks, hkv, block_size, d, p.piece, p.hc) ||
         !pool_map(&vmap, v_cache, num_blocks, hkv, block_size, d, p.piece, p.hc))
         return cudaErrorInvalidValue;
+    a.out = out;
     const bool f32 = q_dtype == PKV_F32;
     cudaError_t e = cudaErrorInvalidValue;
-#define PKV_Q8_CASE(DD, FF) \
-    if (d == DD && f32 == FF) e = launch_split<DD, FF>(dev, p, a, kmap, vmap, stream);
+#define PKV_Q8_CASE(DD, FF)                                                         \
+    if (d == DD && f32 == FF)                                                       \
+        e = p.whole ? launch_split<DD, FF, true>(dev, p, a, kmap, vmap, stream)     \
+                    : launch_split<DD, FF, false>(dev, p, a, kmap, vmap, stream);
     PKV_Q8_CASE(128, false) PKV_Q8_CASE(128, true) PKV_Q8_CASE(64, false) PKV_Q8_CASE(64, true)
 #undef PKV_Q8_CASE
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || p.whole) return e;
     return launch_combine(d, f32, a.part_o, a.part_ml, a.tstart, out, batch, hq, p.ctas, stream);
 }
 

@@ -262,6 +262,16 @@ DECODE = [  # lens, Hq, Hkv, d, B, type
     ([700], 128, 2, 64, 16, "f32"),
     ([100, 3], 18, 6, 64, 64, "f32"),
     ([50] * 3, 32, 32, 128, 16, "bf16"),
+    # sequences that a CTA takes whole, at the border to those that are split, empty ones
+    ([192, 0, 1, 191], 16, 8, 128, 16, "bf16"),
+    ([193, 5], 16, 8, 128, 1, "bf16"),
+    ([0, 0, 0], 16, 8, 64, 8, "f32"),
+    ([512, 0, 300], 2, 1, 64, 32, "f32"),
+    ([0] + [47, 48, 49] * 21, 32, 8, 128, 16, "bf16"),
+    ([630, 0, 7] * 25 + [600], 16, 8, 128, 16, "bf16"),
+    ([9, 0, 160], 24, 1, 128, 20, "bf16"),
+    ([100] * 152, 8, 4, 128, 16, "bf16"),
+    ([100] * 153, 8, 4, 128, 16, "bf16"),
     # pages whose rows do not fill the swizzle's 8
     ([5, 100, 64], 8, 8, 128, 1, "bf16"),
     ([77, 200], 16, 8, 64, 2, "bf16"),
