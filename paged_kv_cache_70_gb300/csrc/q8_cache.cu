@@ -31,7 +31,8 @@ namespace pkv {
 
 namespace {
 
-constexpr int kWarps = 8;  // per CTA of the write
+constexpr int kWarps = 8;      // per CTA of the write
+constexpr int kFewRows = 32;  // of a page: its runs take a warp each
 // row steps that a CTA holds in shared memory, 8 KiB each (fp32: 16): 64 KiB, so that
 // three CTAs share an SM
 template <bool F32>
@@ -134,21 +135,30 @@ __device__ __forceinline__ void restage_unit(uint32_t slot, const float* x) {
     }
 }
 
-// which tokens of a CTA's window begin a run (the tokens of one sequence on one page),
-// and which continue the run of the token before them
-struct Window {
-    uint32_t starts[kWarps], goes_on[kWarps];
+// The runs (the tokens of one sequence on one page) that begin at tokens n0 .. n0 + 255,
+// a CTA's window
+constexpr int kWindow = kWarps * 32;
+struct Runs {
+    uint32_t starts[kWarps], goes_on[kWarps];  // tokens that begin a run, and that continue one
+    uint32_t behind[kWarps];                   // tokens behind the window that continue its last
+    int32_t seq, block;                        // that the last token lies in
+    int32_t first[kWindow], page[kWindow], len[kWindow];  // of each (page below 0: not in the pool)
 };
 
-__device__ __forceinline__ void look_at_window(const NewTokens& t, const RopeTable& table,
-                                               int64_t n0, unsigned int* err, Window* w) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t n = n0 + threadIdx.x;
-    int32_t s = -1, p = -1, rp = 0;
+// One thread looks at each token and at one behind the window; returns how many runs.
+__device__ __forceinline__ int find_runs(const NewTokens& t, const RopeTable& table, int64_t n0,
+                                         unsigned int* err, Runs* w) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t n = n0 + tid;
+    int32_t s = -1, p = -1, rp = 0, s2 = -1, p2 = -1;
     if (n < t.num) {
         s = __ldg(t.seq + n);
         p = __ldg(t.pos + n);
         rp = __ldg(t.rope_pos + n);
+    }
+    if (n + kWindow < t.num) {
+        s2 = __ldg(t.seq + n + kWindow);
+        p2 = __ldg(t.pos + n + kWindow);
     }
     int32_t s1 = __shfl_up_sync(0xffffffffu, s, 1), p1 = __shfl_up_sync(0xffffffffu, p, 1);
     if (lane == 0) {
@@ -156,67 +166,72 @@ __device__ __forceinline__ void look_at_window(const NewTokens& t, const RopeTab
         p1 = n > 0 && n <= t.num ? __ldg(t.pos + n - 1) : -1;
     }
     if (n < t.num) token_ok(t, table, s, p, rp, err);
-    const bool placed = s >= 0 && s < t.num_seqs && p >= 0 &&
-                        (int32_t)t.block.quot((uint32_t)p) < t.max_blocks;
-    const bool on = placed && s1 == s && p1 >= 0 &&
-                    t.block.quot((uint32_t)p1) == t.block.quot((uint32_t)p);
-    const uint32_t starts = __ballot_sync(0xffffffffu, placed && !on);
+    const int32_t block = (int32_t)t.block.quot((uint32_t)max(p, 0));
+    const bool placed = s >= 0 && s < t.num_seqs && p >= 0 && block < t.max_blocks;
+    const bool on = placed && s1 == s && p1 >= 0 && (int32_t)t.block.quot((uint32_t)p1) == block;
+    const bool begins = placed && !on;
+    const int32_t page = begins ? token_page(t, s, p, err) : -1;
+    const uint32_t starts = __ballot_sync(0xffffffffu, begins);
     const uint32_t goes_on = __ballot_sync(0xffffffffu, on);
     if (lane == 0) {
         w->starts[warp] = starts;
         w->goes_on[warp] = goes_on;
     }
-}
-
-// the length of the run that begins at token n0 + at of a window
-__device__ __forceinline__ int32_t run_length(const NewTokens& t, int64_t n0, const Window& w,
-                                              int at) {
-    const int lane = threadIdx.x & 31;
-    int end = at + 1;  // the first token behind it
-    while (end < kWarps * 32) {
-        const uint32_t rest = ~w.goes_on[end >> 5] >> (end & 31);
-        if (rest) return end + __ffs(rest) - 1 - at;
-        end = (end | 31) + 1;
+    if (tid == kWindow - 1) {
+        w->seq = placed ? s : -1;
+        w->block = block;
     }
-    // it may go on behind the window
-    const int32_t s = __ldg(t.seq + n0 + at);
-    const uint32_t pg = t.block.quot((uint32_t)__ldg(t.pos + n0 + at));
-    int32_t len = end - at;
-    for (bool more = true; more;) {
-        bool same[8];
+    __syncthreads();
+    const bool same = s2 >= 0 && s2 == w->seq && p2 >= 0 &&
+                      (int32_t)t.block.quot((uint32_t)p2) == w->block;
+    const uint32_t behind = __ballot_sync(0xffffffffu, same);
+    if (lane == 0) w->behind[warp] = behind;
+    int k = __popc(starts & ((1u << lane) - 1)), total = 0;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            const int64_t n = n0 + at + len + 32 * j + lane;
-            same[j] = false;
-            if (n < t.num) {
-                const int32_t ts = __ldg(t.seq + n), tp = __ldg(t.pos + n);
-                same[j] = ts == s && tp >= 0 && t.block.quot((uint32_t)tp) == pg;
-            }
-        }
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-            if (!more) continue;
-            const uint32_t m = __ballot_sync(0xffffffffu, same[j]);
-            more = m == 0xffffffffu;
-            len += more ? 32 : __ffs(~m) - 1;
-        }
-    }
-    return len;
-}
-
-// the k-th token (from 0) of a window that begins a run, below 0: there are fewer
-__device__ __forceinline__ int nth_start(const Window& w, int k) {
     for (int i = 0; i < kWarps; ++i) {
-        uint32_t m = w.starts[i];
-        const int n = __popc(m);
-        if (k >= n) {
-            k -= n;
-            continue;
-        }
-        for (; k > 0; --k) m &= m - 1;
-        return 32 * i + __ffs(m) - 1;
+        const int m = __popc(w->starts[i]);
+        total += m;
+        k += i < warp ? m : 0;
     }
-    return -1;
+    if (begins) {
+        int end = tid + 1;  // the first token behind it
+        while (end < kWindow) {
+            const uint32_t rest = ~w->goes_on[end >> 5] >> (end & 31);
+            if (rest) {
+                end += __ffs(rest) - 1;
+                break;
+            }
+            end = (end | 31) + 1;
+        }
+        w->first[k] = tid;
+        w->page[k] = page;
+        w->len[k] = end - tid;
+    }
+    __syncthreads();
+    return total;
+}
+
+// the length of run k, with what lies behind the window
+__device__ __forceinline__ int32_t run_length(const NewTokens& t, int64_t n0, const Runs& w,
+                                              int k) {
+    int32_t len = w.len[k];
+    if (w.first[k] + len < kWindow) return len;
+#pragma unroll 1
+    for (int i = 0; i < kWarps; ++i) {
+        const uint32_t rest = ~w.behind[i];
+        if (rest) return len + __ffs(rest) - 1;
+        len += 32;
+    }
+    for (int64_t n = n0 + w.first[k] + len;; n += 32, len += 32) {  // (pages of more than 256)
+        const int64_t at = n + (threadIdx.x & 31);
+        bool same = false;
+        if (at < t.num) {
+            const int32_t s = __ldg(t.seq + at), p = __ldg(t.pos + at);
+            same = s == w.seq && p >= 0 && (int32_t)t.block.quot((uint32_t)p) == w.block;
+        }
+        const uint32_t rest = ~__ballot_sync(0xffffffffu, same);
+        if (rest) return len + __ffs(rest) - 1;
+    }
 }
 
 // `count` times 16 codes times `ratio`, every step-th from `first` on (rare: kept out of
@@ -260,7 +275,7 @@ struct Head {
 
 // The run of `len` tokens from n on, in `page`, written by W warps of which this is
 // the rank-th; W is 1 or all of the CTA's.
-template <int D, bool F32, bool MIX, int W>
+template <int D, bool F32, bool MIX, bool ROT, int W>
 __device__ __forceinline__ void write_run(const Q8WriteArgs& a, const Head& hd, int64_t n,
                                           int32_t len, int32_t page, int rank, uint32_t* red) {
     constexpr int U = D / 16, RS = 32 / U;  // lanes per row, rows per step
@@ -277,7 +292,7 @@ __device__ __forceinline__ void write_run(const Q8WriteArgs& a, const Head& hd, 
     const int32_t front = p - p0;                                   // rows in front of the run
     float* const sp = hd.scales + (int64_t)page * a.tok.hkv;
     const float old = front > 0 ? *sp : 0.f;
-    const bool spins = hd.u < (hd.rot >> 4);
+    const bool spins = ROT && hd.u < (hd.rot >> 4);
 
     // the largest of the warps'
     auto run_max = [&](uint32_t m) {
@@ -300,21 +315,26 @@ __device__ __forceinline__ void write_run(const Q8WriteArgs& a, const Head& hd, 
             from += step * hd.stride;
             slot += kNext;
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
+        asm volatile("cp.async.commit_group;" ::: "memory");
     };
+    // The usual run is one of consecutive positions, all of them in the table: then
+    // nothing is looked up row by row.
+    const int32_t rp0 = a.table.rot ? __ldg(rope_pos) : 0;
+    bool plain = true;
     // the position that row r is rotated by (0 without a rotation), below 0: none, the
     // row is not written
     auto turn_of = [&](int32_t r) {
         if (!a.table.rot) return 0;
-        const int32_t rp = __ldg(rope_pos + r);
-        return rp < a.table.positions ? rp : -1;
+        const int32_t rp = plain ? rp0 + r : __ldg(rope_pos + r);
+        return plain || rp < a.table.positions ? rp : -1;
     };
     // rotates the rows from base on in place (to odd where bf16 holds them: a further
     // rounding to 4 bits then gives what one rounding gives); the largest magnitude's
     // bits + 1
     auto rotate_rows = [&](int32_t base) {
         uint32_t top = 0, slot = hd.slot;
-#pragma unroll 1
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        #pragma unroll 1
         for (int32_t r = base + r0; r < min(len, base + cap); r += step, slot += kNext) {
             const int32_t rp = turn_of(r);
             if (rp < 0) continue;
@@ -322,7 +342,7 @@ __device__ __forceinline__ void write_run(const Q8WriteArgs& a, const Head& hd, 
             if (spins) load_angles(a.table, rp, hd.u, ang);
             const RawUnit<F32> raw = staged_unit<F32>(slot);
             float x[16], m = 0.f;  // (the maximum takes no notice of a NaN)
-            if (!F32 && !hd.rot) {
+            if (!F32 && !ROT) {
                 m = largest_bf16(raw.a[0], raw.b[0]);
             } else {
                 widen_unit<F32>(raw, x);
@@ -340,6 +360,16 @@ __device__ __forceinline__ void write_run(const Q8WriteArgs& a, const Head& hd, 
     uint32_t top = 0;
     for (int32_t base = 0; base < len; base += cap) {
         fetch(base);
+        if (base == 0) {
+            for (int32_t r = r0; r < len; r += step) {
+                plain &= __ldg(pos + r) - p == r;
+                if (a.table.rot) {
+                    const int32_t rp = __ldg(rope_pos + r);
+                    plain &= rp - rp0 == r && rp < a.table.positions;
+                }
+            }
+            plain = __all_sync(0xffffffffu, plain && rp0 >= 0);
+        }
         top = max(top, rotate_rows(base));
     }
     top = run_max(top);
@@ -384,10 +414,10 @@ __device__ __forceinline__ void write_run(const Q8WriteArgs& a, const Head& hd, 
             rotate_rows(base);
         }
         uint32_t slot = hd.slot;
-#pragma unroll 1
+        #pragma unroll 1
         for (int32_t r = base + r0; r < min(len, base + cap); r += step, slot += kNext) {
             if (turn_of(r) < 0) continue;
-            const int32_t at = __ldg(pos + r) - p0;
+            const int32_t at = plain ? front + r : __ldg(pos + r) - p0;
             float x[16];
             widen_unit<F32>(staged_unit<F32>(slot), x);
             if (inf) {
@@ -413,24 +443,18 @@ __device__ __forceinline__ void write_run(const Q8WriteArgs& a, const Head& hd, 
     }
 }
 
-template <int D, bool F32, bool MIX>
+template <int D, bool F32, bool MIX, bool ROT>
 __device__ __forceinline__ void write_runs(const Q8WriteArgs& a, uint32_t cta) {
     constexpr int U = D / 16, RS = 32 / U;
     extern __shared__ __align__(16) unsigned char stage[];
     __shared__ uint32_t red[kWarps];
-    __shared__ Window window;
-    __shared__ int32_t longs[kWarps * 32][3];  // runs that take the whole CTA
-    __shared__ int n_longs;
+    __shared__ Runs runs;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool is_v = cta & 1;
     const int h = (int)((cta >> 1) % (uint32_t)a.tok.hkv);
     const uint32_t rest = (cta >> 1) / (uint32_t)a.tok.hkv;
     const int part = (int)(rest % (uint32_t)a.parts);
-    const int64_t n0 = (int64_t)(rest / (uint32_t)a.parts) * (kWarps * 32);
-    unsigned int* const err = h == 0 && !is_v ? a.err : nullptr;
-    if (threadIdx.x == 0) n_longs = 0;
-    look_at_window(a.tok, a.table, n0, part == 0 ? err : nullptr, &window);
-    __syncthreads();
+    const int64_t n0 = (int64_t)(rest / (uint32_t)a.parts) * kWindow;
     Head hd;
     hd.rows = static_cast<const unsigned char*>(is_v ? a.v : a.k) + (int64_t)h * D * (F32 ? 4 : 2);
     hd.stride = (is_v ? a.v_stride : a.k_stride) * (F32 ? 4 : 2);
@@ -438,42 +462,38 @@ __device__ __forceinline__ void write_runs(const Q8WriteArgs& a, uint32_t cta) {
     hd.pool = (is_v ? a.vc : a.kc) + (int64_t)h * a.tok.block.d * D;
     hd.scales = (is_v ? a.vs : a.ks) + h;
     hd.slot = smem_u32(stage) + threadIdx.x * 16;
-    hd.rot = is_v ? 0 : a.table.rot;
+    hd.rot = ROT ? a.table.rot : 0;
     hd.u = lane % U;
     unit_dims<MIX>(hd.u, hd.rot, &hd.da, &hd.db);
-    // every parts-th run, one per warp; what a warp does not hold is left for all
-    for (int k = part + warp * a.parts;; k += kWarps * a.parts) {
-        const int first = nth_start(window, k);
-        if (first < 0) break;
-        const int64_t n = n0 + first;
-        const int32_t page = token_page(a.tok, __ldg(a.tok.seq + n), __ldg(a.tok.pos + n),
-                                        lane == 0 ? err : nullptr);
-        if (page < 0) continue;
-        const int32_t len = run_length(a.tok, n0, window, first);
-        if (len > RS * a.steps) {
-            if (lane == 0) {
-                const int at = atomicAdd(&n_longs, 1);
-                longs[at][0] = first;
-                longs[at][1] = len;
-                longs[at][2] = page;
-            }
-        } else {
-            write_run<D, F32, MIX, 1>(a, hd, n, len, page, 0, nullptr);
-        }
+    // (one CTA of a window flags what is wrong with its tokens)
+    const int total = find_runs(a.tok, a.table, n0, h == 0 && part == 0 && !is_v ? a.err : nullptr,
+                                &runs);
+    // every parts-th run, one per warp, then those of more rows than a warp holds, by all
+    for (int k = part + warp * a.parts; k < total; k += kWarps * a.parts) {
+        if (runs.page[k] < 0) continue;
+        const int32_t len = run_length(a.tok, n0, runs, k);
+        if (len <= RS * a.steps)
+            write_run<D, F32, MIX, ROT, 1>(a, hd, n0 + runs.first[k], len, runs.page[k], 0, nullptr);
     }
-    __syncthreads();
-    const int total = n_longs;
-    for (int i = 0; i < total; ++i)
-        write_run<D, F32, MIX, kWarps>(a, hd, n0 + longs[i][0], longs[i][1], longs[i][2], warp, red);
+    for (int k = part; k < total; k += a.parts) {
+        if (runs.page[k] < 0) continue;
+        const int32_t len = run_length(a.tok, n0, runs, k);
+        if (len > RS * a.steps)
+            write_run<D, F32, MIX, ROT, kWarps>(a, hd, n0 + runs.first[k], len, runs.page[k], warp, red);
+    }
 }
 
-template <int D, bool F32, bool MIX>
-__global__ void __launch_bounds__(kWarps * 32, 3) q8_write_kernel(const Q8WriteArgs a) {
+// CTAs: per SM.  Three leave a thread 80 registers, fewer than the rotation of long runs
+// takes without spilling: 17 K prefill rows of 16 / 8 heads with pages of 256 took 73 us
+// with three and 56 with two, pages of 64 89 and 69, pages of 16 55 and 63.
+template <int D, bool F32, bool MIX, int CTAS>
+__global__ void __launch_bounds__(kWarps * 32, CTAS) q8_write_kernel(const Q8WriteArgs a) {
     PKV_DEPENDENT_PROLOGUE();
     // CTAs of K and V lie among those of the queries, which fill the GPU behind them
     const uint32_t kv = (uint32_t)min((blockIdx.x * a.kv_step) >> 32, (uint64_t)a.kv_ctas);
     if (kv < a.kv_ctas && ((blockIdx.x + 1ull) * a.kv_step) >> 32 > kv) {
-        write_runs<D, F32, MIX>(a, kv);
+        if (a.table.rot && !(kv & 1)) write_runs<D, F32, MIX, true>(a, kv);
+        else write_runs<D, F32, MIX, false>(a, kv);
         return;
     }
     const int64_t id = (int64_t)(blockIdx.x - kv) * kWarps + (threadIdx.x >> 5);
@@ -556,10 +576,10 @@ __global__ void __launch_bounds__(kReadWarps * 32) q8_read_kernel(const Q8ReadAr
     }
 }
 
-template <int D, bool F32, bool MIX>
+template <int D, bool F32, bool MIX, int CTAS>
 cudaError_t launch_write(const DeviceInfo& dev, const Q8WriteArgs& a, int64_t ctas, size_t smem,
                          cudaStream_t stream) {
-    auto kern = q8_write_kernel<D, F32, MIX>;
+    auto kern = q8_write_kernel<D, F32, MIX, CTAS>;
     // the most shared memory a CTA may have, set once per device
     static std::atomic<uint64_t> set{0};
     const uint64_t bit = 1ull << dev.device;
@@ -597,7 +617,6 @@ cudaError_t launch_q8_write(const DeviceInfo& dev, const RopeWriteLaunch& r, flo
     a.steps = (int32_t)std::min<int64_t>(most, ((int64_t)r.block_size + rows - 1) / rows);
     const size_t smem = (size_t)a.steps * (f32 ? step_bytes<true>() : step_bytes<false>());
     // CTAs that share a window: as many as fill the GPU, but no fewer tokens than warps
-    constexpr int kWindow = kWarps * 32;
     const int64_t windows = (r.num_tokens + kWindow - 1) / kWindow;
     const int64_t fill = 3 * dev.num_sms / (windows * r.hkv * 2);
     a.parts = (int32_t)std::max<int64_t>(
@@ -616,7 +635,9 @@ cudaError_t launch_q8_write(const DeviceInfo& dev, const RopeWriteLaunch& r, flo
     a.err = r.err;
     cudaError_t e = cudaErrorInvalidValue;
 #define PKV_Q8_CASE(DD, FF, MM) \
-    if (r.d == DD && f32 == FF && mix == MM) e = launch_write<DD, FF, MM>(dev, a, ctas, smem, stream);
+    if (r.d == DD && f32 == FF && mix == MM) \
+        e = r.block_size <= kFewRows ? launch_write<DD, FF, MM, 3>(dev, a, ctas, smem, stream) \
+                                     : launch_write<DD, FF, MM, 2>(dev, a, ctas, smem, stream);
     PKV_Q8_CASE(64, false, false) PKV_Q8_CASE(64, false, true)
     PKV_Q8_CASE(64, true, false) PKV_Q8_CASE(64, true, true)
     PKV_Q8_CASE(128, false, false) PKV_Q8_CASE(128, false, true)
