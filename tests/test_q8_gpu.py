@@ -524,6 +524,106 @@ def test_decode_workspace_and_refusals():
             pkv.paged_decode_q8(**{**ok, **bad})
 
 
+def test_decode_of_the_largest_batch():
+    """4096 sequences, the shortest empty; the table keeps them from being taken whole."""
+    rng = np.random.default_rng(13)
+    lens = [int(n) for n in rng.integers(0, 40, 4096)]
+    q, qt, (kc, ks, vc, vs), table = decode_inputs(rng, lens, 4, 2, 64, 8, "bf16")
+    got = pkv.paged_decode_q8(qt, pool(kc), pool(vc), to_dev(ks), to_dev(vs), to_dev(table),
+                              to_dev(np.array(lens, np.int32)))
+    want, mass, reach = decode_want(q, kc, ks, vc, vs, table, lens, 0.125, 8)
+    assert np.all(np.abs(widen(got) - want) <= decode_bound(want, mass, reach, lens, "bf16"))
+    assert pkv.paged_error_flags() == 0
+
+
+@pytest.mark.parametrize("seed", range(30))
+def test_decode_of_random_shapes(seed):
+    rng = np.random.default_rng(1000 + seed)
+    d = int(rng.choice([64, 128]))
+    hkv = int(rng.integers(1, 13))
+    hq = hkv * int(rng.integers(1, 18))
+    block = int(rng.integers(1, 70)) * (2 if d == 64 else 1)
+    batch = int(rng.integers(1, 9))
+    top = int(np.exp(rng.uniform(0, np.log(3000))))
+    lens = [int(n) for n in rng.integers(0, top + 1, batch)]
+    dtype = ["bf16", "f32"][int(rng.integers(2))]
+    wide = int(rng.integers(0, 2)) * 200  # a table that reaches further than any sequence
+    q, qt, (kc, ks, vc, vs), table = decode_inputs(rng, lens, hq, hkv, d, block, dtype)
+    table = np.concatenate((table, np.full((batch, wide), -1, np.int32)), 1)
+    scale = float(rng.uniform(0.02, 0.2))
+    got = pkv.paged_decode_q8(qt, pool(kc), pool(vc), to_dev(ks), to_dev(vs), to_dev(table),
+                              to_dev(np.array(lens, np.int32)), scale=scale)
+    want, mass, reach = decode_want(q, kc, ks, vc, vs, table, lens, scale, block)
+    err = np.abs(widen(got) - want)
+    bound = decode_bound(want, mass, reach, lens, dtype)
+    assert np.all(err <= bound), (err / bound).max()
+    assert pkv.paged_error_flags() == 0
+
+
+def test_pages_past_four_gigabytes():
+    """Pages at the end of pools whose byte offsets pass 32 bits: write, read, decode and copy;
+    the write with the rotation into bf16 pools as well."""
+    rng = np.random.default_rng(14)
+    hq, hkv, d, block, lens = 16, 8, 128, 16, [300, 41]
+    page = hkv * block * d
+    total = (5 << 30) // page
+    if torch.cuda.mem_get_info()[0] < 6 * total * page:
+        pytest.skip("needs 30 GB of device memory")
+    used = sum(-(-n // block) for n in lens)
+    ids = rng.permutation(used)
+    near = np.full((2, 19), -1, np.int32)
+    near[0], near[1, :3] = ids[:19], ids[19:]
+    far = np.where(near < 0, -1, total - 1 - near).astype(np.int32)
+    kc, vc = (torch.empty(pkv.q8_cache_shape(total, block, hkv, d), dtype=F8, device="cuda")
+              for _ in range(2))
+    ks, vs = (torch.empty(total, hkv, device="cuda") for _ in range(2))
+    seq = np.concatenate([np.full(n, i) for i, n in enumerate(lens)]).astype(np.int32)
+    pos = np.concatenate([np.arange(n) for n in lens]).astype(np.int32)
+    (k, kt), (v, vt) = (rows(rng, len(seq), hkv, d, "bf16") for _ in range(2))
+    q, qt = rows(rng, 2, hq, d, "bf16")
+    cs = Q.cos_sin(300, d)
+    pkv.paged_kv_write_q8(kt, vt, to_dev(far), to_dev(seq), to_dev(pos), kc, vc, ks, vs,
+                          cos_sin=to_dev(cs))
+    model = []
+    kr = Q.rotate(k, cs, pos, False)
+    for x in (kr, v):
+        c, s = np.zeros((used, hkv, block, d), np.uint8), np.zeros((used, hkv), np.float32)
+        Q.write(x, near, seq, pos, c, s, np.ones(len(seq), bool))
+        model += [c, s]
+    slots = (far[seq, pos // block] * block + pos % block).astype(np.int32)
+    got = pkv.paged_kv_read_q8(kc, vc, ks, vs, to_dev(slots), torch.float32)
+    for g, c, s in zip(got, model[::2], model[1::2]):
+        assert np.array_equal(to_host(g), Q.values(c, s)[near[seq, pos // block], :, pos % block]
+                              .astype(np.float32))
+    out = pkv.paged_decode_q8(qt, kc, vc, ks, vs, to_dev(far), to_dev(np.array(lens, np.int32)))
+    kcm, ksm, vcm, vsm = model
+    want, mass, reach = decode_want(q, kcm, ksm, vcm, vsm, near, lens, d ** -0.5, block)
+    assert np.all(np.abs(widen(out) - want) <= decode_bound(want, mass, reach, lens, "bf16"))
+    src, dst = to_dev(far[0, :1]), torch.tensor([3], dtype=torch.int32, device="cuda")
+    pkv.paged_copy_blocks(kc, vc, src, dst, ks, vs)
+    for t in (kc.view(torch.uint8), vc.view(torch.uint8), ks, vs):
+        assert torch.equal(t[int(far[0, 0])], t[3])
+    del kc, vc, got, out
+    kb, vb = (torch.empty(total, block, hkv, d, dtype=torch.bfloat16, device="cuda")
+              for _ in range(2))
+    pkv.paged_kv_write_rope(kt, vt, to_dev(cs), to_dev(far), to_dev(seq), to_dev(pos), kb, vb)
+    at = torch.from_numpy(slots.astype(np.int64)).cuda()
+    for p, x in ((kb, kr), (vb, v)):
+        assert np.array_equal(to_host(p.view(-1, hkv, d)[at]), Q4.bf16_bits(x))
+    assert pkv.paged_error_flags() == 0
+
+
+def test_copy_blocks_of_8_bit_pools_needs_their_scales():
+    kc = torch.zeros(4, 2, 8, 64, device="cuda").to(F8)
+    s = torch.zeros(4, 2, device="cuda")
+    i = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for ks, vs in ((None, None), (s, None), (s[:2], s), (s, s[:, :1])):
+        with pytest.raises(ValueError):
+            pkv.paged_copy_blocks(kc, kc.clone(), i, i + 1, ks, vs)
+    with pytest.raises(TypeError):
+        pkv.paged_copy_blocks(kc, kc.clone(), i, i + 1, s.double(), s)
+
+
 # ---------------------------------------------------------------------------
 # together
 # ---------------------------------------------------------------------------
