@@ -679,7 +679,8 @@ int paged_kv_write_rope(const void* k, int64_t k_stride, const void* v, int64_t 
  * differs from the old scale the codes of the rows in front of them become
  * e4m3(code * (old / s)).  The new codes are e4m3(x / s), rounded to nearest even.
  * Every value is then within 2^-4 of itself or 2^-10 s of what was written (the larger),
- * and 2^-10 s more for each time that the scale grew afterwards.  Rows behind the tokens
+ * and 2^-10 s more for each time that the scale grew afterwards; sizes from 2^128 - 2^123
+ * on round to 2^128, which reads as infinite.  Rows behind the tokens
  * keep their codes.  A NaN or an infinity is stored as a NaN of its own.  An old scale
  * below 0, above 2^126 or NaN makes the page's scale NaN.  The pages written must
  * belong to one sequence only (copy shared ones first, paged_copy_blocks).
@@ -692,11 +693,13 @@ int paged_kv_write_q8(const void* k, int64_t k_stride, const void* v, int64_t v_
 
 /*
  * paged_kv_read_q8 -- rows of 8-bit pools as values: row n of k_out and v_out
- * ([num_tokens, Hkv, d] of kv_dtype, rounded once) holds what slot_mapping[n] stores; a
- * negative slot gives a row of zeros, and so does a slot past the pool
- * (PKV_FLAG_BAD_SLOT).  The same slot may appear more than once.  With the slots of all
- * keys of a step's requests (paged_build_slot_mapping) this yields the packed K/V that
- * paged_varlen_prefill takes with block_table == NULL: prompts over an 8-bit cache.
+ * ([num_tokens, Hkv, d] of kv_dtype) holds what slot_mapping[n] stores, code times scale
+ * in fp32 and rounded to kv_dtype (exact in both for scales that are powers of two, but
+ * for what lies below the type's range); a negative slot gives a row of zeros, and so does
+ * a slot past the pool (PKV_FLAG_BAD_SLOT).  The same slot may appear more than once.
+ * With the slots of all keys of a step's requests (paged_build_slot_mapping) this yields
+ * the packed K/V that paged_varlen_prefill takes with block_table == NULL: prompts over an
+ * 8-bit cache.
  * k_out, v_out and the pools 16-byte aligned; Hkv * d and num_tokens up to 2^30.
  */
 int paged_kv_read_q8(const void* k_cache, const void* v_cache, const float* k_scale,
@@ -715,7 +718,8 @@ int paged_kv_read_q8(const void* k_cache, const void* v_cache, const float* k_sc
  * Rounding: bf16 queries enter the scores exactly (down to 2^-31 of the largest value of
  * the query); each weight is multiplied by its V scale and rounded to fp16 (11 bits; those
  * below 2^-20 of the largest of a head's to 2^-31 of it), below the output's own
- * rounding.  With fp32 queries, queries and weights keep 22 bits.  A NaN or infinite
+ * rounding.  With fp32 queries, queries and weights keep 22 bits.  Scores and values have
+ * fp32's range; V scales may lie as far apart as that allows.  A NaN or infinite
  * query, or a NaN key, makes its own heads' output NaN, and so does a V scale that is no
  * number; a NaN code of V makes its own dim NaN.
  * workspace: paged_decode_q8_workspace_size(batch, q_dtype, geom) bytes, 256-byte

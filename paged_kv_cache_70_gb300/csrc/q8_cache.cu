@@ -18,8 +18,16 @@
 // rows than a CTA holds: twice).  A thread copies there (cp.async) what it reads itself:
 // no barrier but those of the maximum, and no registers for rows in flight.  Keys are put
 // back rotated, bf16 ones in 16 bits that round to the same code.
+//
+// Measured: 16,729 tokens of 16 / 8 heads of 128, bf16, rotated, into pages of 256, 250 MB
+// with the queries: 56 us (4460 GB/s, 0.67 of the measured copy rate; pages of 16 55 us, of
+// 64 69).  The values alone, without rotation and queries, take 37 of them: CTAs that start
+// together load together and then compute together, so that the time is the sum of both,
+// and half of the instructions are not the arithmetic's.  64 single tokens: 4 us beyond
+// an empty graph, 256 8.
 // Read: row n of the outputs is code * scale at slot_mapping[n], rounded once to the
-// output's type; zeros for a negative slot.
+// output's type; zeros for a negative slot.  34,567 rows of 8 x 128 to bf16, 212.5 MB: 33.0
+// us, 6440 GB/s (0.96 of the measured copy rate).
 #include <algorithm>
 #include <atomic>
 

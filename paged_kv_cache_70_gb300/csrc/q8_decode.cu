@@ -35,6 +35,16 @@
 //  * Keys of a page outside the pool are skipped and flagged; rows past the length
 //    never enter: scores of -inf, V codes and scales of 0, whatever the page holds
 //    there.  Every wait is time-limited.
+//
+// Measured (bf16 queries, a call among others; of the measured copy rate, 6696 GB/s):
+//   8 sequences of 16 K - 41 K keys, 16 / 8 heads, d = 128, 485 MB     77.5 us  0.93
+//   the same with 64 / 8 heads                                          78.8 us  0.92
+//   64 sequences of 128 - 4096 keys, 16 / 8 heads, B = 16, 278 MB       51.1 us  0.81
+//   one of 7777 keys, 32 / 4 heads, d = 64                               9.1 us
+// From one to four times the long contexts the time grows by 6980 GB/s, above the copy
+// rate.  What stands around the stream: ~5 us to the first copy (wait for the launch, plan,
+// table), ~4 us that the SMs' last tiles lie apart, by chance, and ~4 us from the last tile
+// to the end (merges, partial states, the second kernel).
 #include <algorithm>
 #include <atomic>
 #include <numeric>

@@ -8,7 +8,12 @@
 // Alone, a rotation would read and write q and K once more: 1.5 times the bytes of
 // the whole call at 16 / 8 heads.  One warp moves up to 16 heads (fp32: 8) of 128 dims
 // of one token's q, K or V, every load of it in flight before the first is needed and
-// before the slot is known; a small batch then spreads over 4 warps per token.
+// before the slot is known; a small batch then spreads over 3 to 4 warps per token.
+//
+// Measured: 16,729 tokens of 16 / 8 heads of 128, bf16, the columns of one projection, into
+// pages of 256, 282.8 MB: 45.6 us, 6205 GB/s (0.93 of the measured copy rate).  2430 tokens
+// of 16 / 8 heads of 64 in fp32 into bf16 pools, 36.2 MB: 7.8 us.  64 tokens: 4.5 us a
+// call among others, what the host takes to make it.
 #include "common.cuh"
 #include "launch.h"
 #include "rope.cuh"
