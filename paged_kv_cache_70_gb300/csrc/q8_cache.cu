@@ -13,19 +13,19 @@
 // What bounds it: bytes for long runs, the chain token -> page -> rows -> angles for
 // single tokens.  A CTA looks at 256 tokens at once, one per thread, for one head of K or
 // V, and takes every `parts`-th of the runs that begin among them: a warp each, or, runs
-// of more rows than a warp holds, all its warps together.  Rows stay in shared memory
+// of more rows than a warp holds, a team of two or of all.  Rows stay in shared memory
 // from the load over the maximum to the store, so that they are read once (runs of more
 // rows than a CTA holds: twice).  A thread copies there (cp.async) what it reads itself:
 // no barrier but those of the maximum, and no registers for rows in flight.  Keys are put
 // back rotated, bf16 ones in 16 bits that round to the same code.
 //
 // Measured: 16,729 tokens of 16 / 8 heads of 128, bf16, rotated, into pages of 256, 250 MB
-// with the queries: 56 us (4460 GB/s, 0.67 of the measured copy rate; pages of 16 55 us, of
-// 64 69).  The values alone, without rotation and queries, take 37 of them: CTAs that start
+// with the queries: 54 us (4630 GB/s, 0.69 of the measured copy rate; pages of 16 48 us, of
+// 64 57).  The values alone, without rotation and queries, take 36 of them: CTAs that start
 // together load together and then compute together, so that the time is the sum of both,
-// and half of the instructions are not the arithmetic's.  64 single tokens: 4 us beyond
-// an empty graph, 256 8.
-// Read: row n of the outputs is code * scale at slot_mapping[n], rounded once to the
+// and much of the instructions is not the arithmetic's.  64 single tokens: 4 us beyond an
+// empty graph, 256 7.
+// Read: row n of the outputs is code * scale at slot_mapping[n], in fp32 and then in the
 // output's type; zeros for a negative slot.  34,567 rows of 8 x 128 to bf16, 212.5 MB: 33.0
 // us, 6440 GB/s (0.96 of the measured copy rate).
 #include <algorithm>
@@ -39,8 +39,7 @@ namespace pkv {
 
 namespace {
 
-constexpr int kWarps = 8;      // per CTA of the write
-constexpr int kFewRows = 32;  // of a page: its runs take a warp each
+constexpr int kWarps = 8;  // per CTA of the write
 // row steps that a CTA holds in shared memory, 8 KiB each (fp32: 16): 64 KiB, so that
 // three CTAs share an SM
 template <bool F32>
@@ -129,18 +128,94 @@ __device__ __forceinline__ RawUnit<F32> staged_unit(uint32_t slot) {
     return x;
 }
 template <bool F32>
-__device__ __forceinline__ void restage_unit(uint32_t slot, const float* x) {
-    constexpr int C = F32 ? 4 : 2, E = 16 / C;
+__device__ __forceinline__ void restage_unit(uint32_t slot, const RawUnit<F32>& x) {
+    constexpr int C = F32 ? 4 : 2;
 #pragma unroll
-    for (int j = 0; j < C; ++j) {
-        const float* y = x + E * j;
-        if constexpr (F32)
-            sts16(slot + j * kPiece, make_uint4(__float_as_uint(y[0]), __float_as_uint(y[1]),
-                                                __float_as_uint(y[2]), __float_as_uint(y[3])));
-        else
-            sts16(slot + j * kPiece, make_uint4(odd_bf16x2(y[0], y[1]), odd_bf16x2(y[2], y[3]),
-                                                odd_bf16x2(y[4], y[5]), odd_bf16x2(y[6], y[7])));
+    for (int j = 0; j < C; ++j) sts16(slot + j * kPiece, j < C / 2 ? x.a[j % (C / 2)] : x.b[j % (C / 2)]);
+}
+
+// four pairs, rotated; the largest magnitude
+__device__ __forceinline__ float rotate4(float* a, float* b, const float4& c, const float4& s) {
+    const float cc[4] = {c.x, c.y, c.z, c.w}, ss[4] = {s.x, s.y, s.z, s.w};
+    float m = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float r = __fsub_rn(__fmul_rn(a[i], cc[i]), __fmul_rn(b[i], ss[i]));
+        b[i] = __fadd_rn(__fmul_rn(b[i], cc[i]), __fmul_rn(a[i], ss[i]));
+        a[i] = r;
+        m = fmax3(m, fabsf(a[i]), fabsf(b[i]));
     }
+    return m;
+}
+// Half j of a unit's pairs, rotated in place (as rotate_unit does, in half the registers;
+// bf16: to odd); the largest magnitude
+template <bool F32, bool MIX>
+__device__ __forceinline__ float rotate_half(RawUnit<F32>& x, int j, const float4& c,
+                                             const float4& s) {
+    float a[4], b[4], m;
+    if constexpr (F32 && MIX) {  // pairs are neighbours, in chunk a (j = 0) or b
+        uint4* const w = j ? x.b : x.a;
+        float f[8];
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            f[4 * i] = __uint_as_float(w[i].x);
+            f[4 * i + 1] = __uint_as_float(w[i].y);
+            f[4 * i + 2] = __uint_as_float(w[i].z);
+            f[4 * i + 3] = __uint_as_float(w[i].w);
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            a[i] = f[2 * i];
+            b[i] = f[2 * i + 1];
+        }
+        m = rotate4(a, b, c, s);
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+            w[i] = make_uint4(__float_as_uint(a[2 * i]), __float_as_uint(b[2 * i]),
+                              __float_as_uint(a[2 * i + 1]), __float_as_uint(b[2 * i + 1]));
+    } else if constexpr (F32) {  // piece j of chunk a with piece j of chunk b
+        uint4 &u = x.a[j], &v = x.b[j];
+        a[0] = __uint_as_float(u.x); a[1] = __uint_as_float(u.y);
+        a[2] = __uint_as_float(u.z); a[3] = __uint_as_float(u.w);
+        b[0] = __uint_as_float(v.x); b[1] = __uint_as_float(v.y);
+        b[2] = __uint_as_float(v.z); b[3] = __uint_as_float(v.w);
+        m = rotate4(a, b, c, s);
+        u = make_uint4(__float_as_uint(a[0]), __float_as_uint(a[1]), __float_as_uint(a[2]),
+                       __float_as_uint(a[3]));
+        v = make_uint4(__float_as_uint(b[0]), __float_as_uint(b[1]), __float_as_uint(b[2]),
+                       __float_as_uint(b[3]));
+    } else if constexpr (MIX) {
+        uint4& u = j ? x.b[0] : x.a[0];
+        a[0] = bf16lo(u.x); b[0] = bf16hi(u.x);
+        a[1] = bf16lo(u.y); b[1] = bf16hi(u.y);
+        a[2] = bf16lo(u.z); b[2] = bf16hi(u.z);
+        a[3] = bf16lo(u.w); b[3] = bf16hi(u.w);
+        m = rotate4(a, b, c, s);
+        u = make_uint4(odd_bf16x2(a[0], b[0]), odd_bf16x2(a[1], b[1]), odd_bf16x2(a[2], b[2]),
+                       odd_bf16x2(a[3], b[3]));
+    } else {
+        uint32_t &u0 = j ? x.a[0].z : x.a[0].x, &u1 = j ? x.a[0].w : x.a[0].y;
+        uint32_t &v0 = j ? x.b[0].z : x.b[0].x, &v1 = j ? x.b[0].w : x.b[0].y;
+        a[0] = bf16lo(u0); a[1] = bf16hi(u0); a[2] = bf16lo(u1); a[3] = bf16hi(u1);
+        b[0] = bf16lo(v0); b[1] = bf16hi(v0); b[2] = bf16lo(v1); b[3] = bf16hi(v1);
+        m = rotate4(a, b, c, s);
+        u0 = odd_bf16x2(a[0], a[1]);
+        u1 = odd_bf16x2(a[2], a[3]);
+        v0 = odd_bf16x2(b[0], b[1]);
+        v1 = odd_bf16x2(b[2], b[3]);
+    }
+    return m;
+}
+// the largest magnitude of a unit, NaNs aside
+__device__ __forceinline__ float largest(const RawUnit<false>& x) {
+    return largest_bf16(x.a[0], x.b[0]);
+}
+__device__ __forceinline__ float largest(const RawUnit<true>& r) {
+    float x[16], m = 0.f;
+    widen_unit<true>(r, x);
+#pragma unroll
+    for (int e = 0; e < 16; e += 2) m = fmax3(m, fabsf(x[e]), fabsf(x[e + 1]));
+    return m;
 }
 
 // The runs (the tokens of one sequence on one page) that begin at tokens n0 .. n0 + 255,
@@ -149,24 +224,38 @@ constexpr int kWindow = kWarps * 32;
 struct Runs {
     uint32_t starts[kWarps], goes_on[kWarps];  // tokens that begin a run, and that continue one
     uint32_t behind[kWarps];                   // tokens behind the window that continue its last
-    int32_t seq, block;                        // that the last token lies in
     int32_t first[kWindow], page[kWindow], len[kWindow];  // of each (page below 0: not in the pool)
 };
+
+// how many of a window's tokens from `at` on have their bit set without a gap
+__device__ __forceinline__ int bits_from(const uint32_t* words, int at) {
+    int end = at;
+    while (end < kWindow) {
+        const uint32_t rest = ~words[end >> 5] >> (end & 31);
+        if (rest) return end + __ffs(rest) - 1 - at;
+        end = (end | 31) + 1;
+    }
+    return kWindow - at;
+}
 
 // One thread looks at each token and at one behind the window; returns how many runs.
 __device__ __forceinline__ int find_runs(const NewTokens& t, const RopeTable& table, int64_t n0,
                                          unsigned int* err, Runs* w) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t n = n0 + tid;
-    int32_t s = -1, p = -1, rp = 0, s2 = -1, p2 = -1;
+    int32_t s = -1, p = -1, rp = 0, s2 = -1, p2 = -1, sl = -1, pl = -1;
     if (n < t.num) {
         s = __ldg(t.seq + n);
         p = __ldg(t.pos + n);
         rp = __ldg(t.rope_pos + n);
     }
-    if (n + kWindow < t.num) {
-        s2 = __ldg(t.seq + n + kWindow);
-        p2 = __ldg(t.pos + n + kWindow);
+    if (n0 + kWindow < t.num) {  // the window's last token, and one behind it
+        sl = __ldg(t.seq + n0 + kWindow - 1);
+        pl = __ldg(t.pos + n0 + kWindow - 1);
+        if (n + kWindow < t.num) {
+            s2 = __ldg(t.seq + n + kWindow);
+            p2 = __ldg(t.pos + n + kWindow);
+        }
     }
     int32_t s1 = __shfl_up_sync(0xffffffffu, s, 1), p1 = __shfl_up_sync(0xffffffffu, p, 1);
     if (lane == 0) {
@@ -174,26 +263,21 @@ __device__ __forceinline__ int find_runs(const NewTokens& t, const RopeTable& ta
         p1 = n > 0 && n <= t.num ? __ldg(t.pos + n - 1) : -1;
     }
     if (n < t.num) token_ok(t, table, s, p, rp, err);
-    const int32_t block = (int32_t)t.block.quot((uint32_t)max(p, 0));
-    const bool placed = s >= 0 && s < t.num_seqs && p >= 0 && block < t.max_blocks;
-    const bool on = placed && s1 == s && p1 >= 0 && (int32_t)t.block.quot((uint32_t)p1) == block;
+    auto block = [&](int32_t x) { return (int32_t)t.block.quot((uint32_t)max(x, 0)); };
+    const bool placed = s >= 0 && s < t.num_seqs && p >= 0 && block(p) < t.max_blocks;
+    const bool on = placed && s1 == s && p1 >= 0 && block(p1) == block(p);
     const bool begins = placed && !on;
     const int32_t page = begins ? token_page(t, s, p, err) : -1;
     const uint32_t starts = __ballot_sync(0xffffffffu, begins);
     const uint32_t goes_on = __ballot_sync(0xffffffffu, on);
+    const uint32_t behind = __ballot_sync(0xffffffffu, s2 >= 0 && s2 == sl && p2 >= 0 && pl >= 0 &&
+                                                           block(p2) == block(pl));
     if (lane == 0) {
         w->starts[warp] = starts;
         w->goes_on[warp] = goes_on;
-    }
-    if (tid == kWindow - 1) {
-        w->seq = placed ? s : -1;
-        w->block = block;
+        w->behind[warp] = behind;
     }
     __syncthreads();
-    const bool same = s2 >= 0 && s2 == w->seq && p2 >= 0 &&
-                      (int32_t)t.block.quot((uint32_t)p2) == w->block;
-    const uint32_t behind = __ballot_sync(0xffffffffu, same);
-    if (lane == 0) w->behind[warp] = behind;
     int k = __popc(starts & ((1u << lane) - 1)), total = 0;
 #pragma unroll
     for (int i = 0; i < kWarps; ++i) {
@@ -202,44 +286,23 @@ __device__ __forceinline__ int find_runs(const NewTokens& t, const RopeTable& ta
         k += i < warp ? m : 0;
     }
     if (begins) {
-        int end = tid + 1;  // the first token behind it
-        while (end < kWindow) {
-            const uint32_t rest = ~w->goes_on[end >> 5] >> (end & 31);
-            if (rest) {
-                end += __ffs(rest) - 1;
-                break;
+        int len = 1 + bits_from(w->goes_on, tid + 1);
+        if (tid + len == kWindow) {
+            int more = bits_from(w->behind, 0);
+            if (more == kWindow) {  // (pages of more than 256: one by one)
+                for (int64_t m = n0 + 2 * kWindow; m < t.num && __ldg(t.seq + m) == s; ++m, ++more) {
+                    const int32_t q = __ldg(t.pos + m);
+                    if (q < 0 || block(q) != block(p)) break;
+                }
             }
-            end = (end | 31) + 1;
+            len += more;
         }
         w->first[k] = tid;
         w->page[k] = page;
-        w->len[k] = end - tid;
+        w->len[k] = len;
     }
     __syncthreads();
     return total;
-}
-
-// the length of run k, with what lies behind the window
-__device__ __forceinline__ int32_t run_length(const NewTokens& t, int64_t n0, const Runs& w,
-                                              int k) {
-    int32_t len = w.len[k];
-    if (w.first[k] + len < kWindow) return len;
-#pragma unroll 1
-    for (int i = 0; i < kWarps; ++i) {
-        const uint32_t rest = ~w.behind[i];
-        if (rest) return len + __ffs(rest) - 1;
-        len += 32;
-    }
-    for (int64_t n = n0 + w.first[k] + len;; n += 32, len += 32) {  // (pages of more than 256)
-        const int64_t at = n + (threadIdx.x & 31);
-        bool same = false;
-        if (at < t.num) {
-            const int32_t s = __ldg(t.seq + at), p = __ldg(t.pos + at);
-            same = s == w.seq && p >= 0 && (int32_t)t.block.quot((uint32_t)p) == w.block;
-        }
-        const uint32_t rest = ~__ballot_sync(0xffffffffu, same);
-        if (rest) return len + __ffs(rest) - 1;
-    }
 }
 
 // `count` times 16 codes times `ratio`, every step-th from `first` on (rare: kept out of
@@ -306,9 +369,17 @@ __device__ __forceinline__ void write_run(const Q8WriteArgs& a, const Head& hd, 
     auto run_max = [&](uint32_t m) {
         m = __reduce_max_sync(0xffffffffu, m);
         if constexpr (W > 1) {
-            __syncthreads();
+            auto meet = [&]() {
+                if constexpr (W == kWarps) {
+                    __syncthreads();
+                } else {  // (barrier 0 is the CTA's)
+                    const int bar = 1 + (threadIdx.x >> 5) / W;
+                    asm volatile("bar.sync %0, %1;" ::"r"(bar), "n"(W * 32) : "memory");
+                }
+            };
+            meet();
             if (lane == 0) red[rank] = m;
-            __syncthreads();
+            meet();
 #pragma unroll
             for (int i = 0; i < W; ++i) m = max(m, red[i]);
         }
@@ -346,20 +417,17 @@ __device__ __forceinline__ void write_run(const Q8WriteArgs& a, const Head& hd, 
         for (int32_t r = base + r0; r < min(len, base + cap); r += step, slot += kNext) {
             const int32_t rp = turn_of(r);
             if (rp < 0) continue;
-            UnitAngles ang;
-            if (spins) load_angles(a.table, rp, hd.u, ang);
-            const RawUnit<F32> raw = staged_unit<F32>(slot);
-            float x[16], m = 0.f;  // (the maximum takes no notice of a NaN)
-            if (!F32 && !ROT) {
-                m = largest_bf16(raw.a[0], raw.b[0]);
+            RawUnit<F32> x = staged_unit<F32>(slot);
+            float m;  // (no maximum here takes notice of a NaN)
+            if (spins) {
+                const float4* const c =
+                    reinterpret_cast<const float4*>(a.table.cos_sin + (int64_t)rp * a.table.rot + 8 * hd.u);
+                const float4* const q = c + a.table.rot / 8;
+                m = rotate_half<F32, MIX>(x, 0, __ldg(c), __ldg(q));
+                m = fmaxf(m, rotate_half<F32, MIX>(x, 1, __ldg(c + 1), __ldg(q + 1)));
+                restage_unit<F32>(slot, x);
             } else {
-                widen_unit<F32>(raw, x);
-                if (spins) {
-                    rotate_unit<MIX>(x, ang);
-                    restage_unit<F32>(slot, x);
-                }
-#pragma unroll
-                for (int e = 0; e < 16; e += 2) m = fmax3(m, fabsf(x[e]), fabsf(x[e + 1]));
+                m = largest(x);
             }
             top = max(top, __float_as_uint(m) + 1);
         }
@@ -451,7 +519,7 @@ __device__ __forceinline__ void write_run(const Q8WriteArgs& a, const Head& hd, 
     }
 }
 
-template <int D, bool F32, bool MIX, bool ROT>
+template <int D, bool F32, bool MIX, bool ROT, int TEAM>
 __device__ __forceinline__ void write_runs(const Q8WriteArgs& a, uint32_t cta) {
     constexpr int U = D / 16, RS = 32 / U;
     extern __shared__ __align__(16) unsigned char stage[];
@@ -476,32 +544,29 @@ __device__ __forceinline__ void write_runs(const Q8WriteArgs& a, uint32_t cta) {
     // (one CTA of a window flags what is wrong with its tokens)
     const int total = find_runs(a.tok, a.table, n0, h == 0 && part == 0 && !is_v ? a.err : nullptr,
                                 &runs);
-    // every parts-th run, one per warp, then those of more rows than a warp holds, by all
-    for (int k = part + warp * a.parts; k < total; k += kWarps * a.parts) {
-        if (runs.page[k] < 0) continue;
-        const int32_t len = run_length(a.tok, n0, runs, k);
-        if (len <= RS * a.steps)
-            write_run<D, F32, MIX, ROT, 1>(a, hd, n0 + runs.first[k], len, runs.page[k], 0, nullptr);
-    }
-    for (int k = part; k < total; k += a.parts) {
-        if (runs.page[k] < 0) continue;
-        const int32_t len = run_length(a.tok, n0, runs, k);
-        if (len > RS * a.steps)
-            write_run<D, F32, MIX, ROT, kWarps>(a, hd, n0 + runs.first[k], len, runs.page[k], warp, red);
+    // every parts-th run, one per warp, then those of more rows than a warp holds, by teams
+    for (int k = part + warp * a.parts; k < total; k += kWarps * a.parts)
+        if (runs.page[k] >= 0 && (TEAM == 1 || runs.len[k] <= RS * a.steps))
+            write_run<D, F32, MIX, ROT, 1>(a, hd, n0 + runs.first[k], runs.len[k], runs.page[k], 0,
+                                           nullptr);
+    if constexpr (TEAM > 1) {
+        const int team = TEAM == kWarps ? 0 : warp / TEAM, rank = TEAM == kWarps ? warp : warp % TEAM;
+        for (int k = part + team * a.parts; k < total; k += kWarps / TEAM * a.parts)
+            if (runs.page[k] >= 0 && runs.len[k] > RS * a.steps)
+                write_run<D, F32, MIX, ROT, TEAM>(a, hd, n0 + runs.first[k], runs.len[k],
+                                                  runs.page[k], rank, red + team * TEAM);
     }
 }
 
-// CTAs: per SM.  Three leave a thread 80 registers, fewer than the rotation of long runs
-// takes without spilling: 17 K prefill rows of 16 / 8 heads with pages of 256 took 73 us
-// with three and 56 with two, pages of 64 89 and 69, pages of 16 55 and 63.
-template <int D, bool F32, bool MIX, int CTAS>
-__global__ void __launch_bounds__(kWarps * 32, CTAS) q8_write_kernel(const Q8WriteArgs a) {
+// TEAM: warps that take a run of more rows than one holds
+template <int D, bool F32, bool MIX, int TEAM>
+__global__ void __launch_bounds__(kWarps * 32, 3) q8_write_kernel(const Q8WriteArgs a) {
     PKV_DEPENDENT_PROLOGUE();
     // CTAs of K and V lie among those of the queries, which fill the GPU behind them
     const uint32_t kv = (uint32_t)min((blockIdx.x * a.kv_step) >> 32, (uint64_t)a.kv_ctas);
     if (kv < a.kv_ctas && ((blockIdx.x + 1ull) * a.kv_step) >> 32 > kv) {
-        if (a.table.rot && !(kv & 1)) write_runs<D, F32, MIX, true>(a, kv);
-        else write_runs<D, F32, MIX, false>(a, kv);
+        if (a.table.rot && !(kv & 1)) write_runs<D, F32, MIX, true, TEAM>(a, kv);
+        else write_runs<D, F32, MIX, false, TEAM>(a, kv);
         return;
     }
     const int64_t id = (int64_t)(blockIdx.x - kv) * kWarps + (threadIdx.x >> 5);
@@ -584,10 +649,10 @@ __global__ void __launch_bounds__(kReadWarps * 32) q8_read_kernel(const Q8ReadAr
     }
 }
 
-template <int D, bool F32, bool MIX, int CTAS>
+template <int D, bool F32, bool MIX, int TEAM>
 cudaError_t launch_write(const DeviceInfo& dev, const Q8WriteArgs& a, int64_t ctas, size_t smem,
                          cudaStream_t stream) {
-    auto kern = q8_write_kernel<D, F32, MIX, CTAS>;
+    auto kern = q8_write_kernel<D, F32, MIX, TEAM>;
     // the most shared memory a CTA may have, set once per device
     static std::atomic<uint64_t> set{0};
     const uint64_t bit = 1ull << dev.device;
@@ -641,11 +706,16 @@ cudaError_t launch_q8_write(const DeviceInfo& dev, const RopeWriteLaunch& r, flo
     const uint64_t even = (((uint64_t)kv_ctas << 32) + ctas - 1) / ctas;
     a.kv_step = std::min(2 * even, (uint64_t)1 << 32);
     a.err = r.err;
+    // a page's rows are a warp's, two warps', or all warps' (16,729 tokens of 16 / 8 heads in
+    // pages of 64: 56 us by twos, 65 by all; of 128: 77 by twos, 57 by all)
+    const int64_t held = (int64_t)a.steps * rows;
+    const int team = r.block_size <= held ? 1 : (r.block_size <= 2 * held ? 2 : 8);
     cudaError_t e = cudaErrorInvalidValue;
 #define PKV_Q8_CASE(DD, FF, MM) \
     if (r.d == DD && f32 == FF && mix == MM) \
-        e = r.block_size <= kFewRows ? launch_write<DD, FF, MM, 3>(dev, a, ctas, smem, stream) \
-                                     : launch_write<DD, FF, MM, 2>(dev, a, ctas, smem, stream);
+        e = team == 1 ? launch_write<DD, FF, MM, 1>(dev, a, ctas, smem, stream) \
+            : team == 2 ? launch_write<DD, FF, MM, 2>(dev, a, ctas, smem, stream) \
+                        : launch_write<DD, FF, MM, 8>(dev, a, ctas, smem, stream);
     PKV_Q8_CASE(64, false, false) PKV_Q8_CASE(64, false, true)
     PKV_Q8_CASE(64, true, false) PKV_Q8_CASE(64, true, true)
     PKV_Q8_CASE(128, false, false) PKV_Q8_CASE(128, false, true)
