@@ -587,7 +587,8 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                 const float x = p[h][i];
                 const float e = ex2(x - mr[i]);
                 w[h][i] = e * (ss[h].y * wm[i]);
-                grow |= x > lim[i] || fabsf(w[h][i]) > kLimit;
+                // (no number either: a weight of 0 times a scale that overflows here)
+                grow |= x > lim[i] || !(fabsf(w[h][i]) <= kLimit);
                 acc[h][i] = e;  // (scores stay in p: they are needed if the references move)
             }
         if (__builtin_expect(__any_sync(0xffffffffu, grow), 0)) {
@@ -626,7 +627,8 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                     o[x][2 + i] *= fo;
                 }
 #pragma unroll
-                for (int h = 0; h < 2; ++h) w[h][i] = acc[h][i] * (ss[h].y * wm[i]);
+                // (in this order: scale and reference by themselves may pass fp32's range)
+                for (int h = 0; h < 2; ++h) w[h][i] = acc[h][i] * ss[h].y * wm[i];
             }
         }
 #pragma unroll

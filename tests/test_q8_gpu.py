@@ -396,6 +396,33 @@ def test_decode_large_scales_before_keys_that_outweigh_them(dtype):
     assert np.all(err <= decode_bound(want, mass, reach, lens, dtype))
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("n", [64, 1024])
+@pytest.mark.parametrize("first,then", [(0.0, 8.0), (0.0, 2.0 ** 100), (2.0 ** -100, 2.0 ** 40),
+                                        (-(2.0 ** -100), -(2.0 ** 90)), (2.0 ** 40, 2.0 ** 90)])
+def test_decode_larger_scales_behind_keys_that_outweigh_them(dtype, n, first, then):
+    """The second half's keys have no weight (their scores are hundreds below the others'), whatever
+    their V scales are: a weight of zero times a scale past the range of the reference is nothing,
+    and no NaN.  (Also where a sequence begins with V scales of zero.)"""
+    rng = np.random.default_rng(n)
+    lens, hq, hkv, d, block = [n], 4, 2, 128, 16
+    q, qt, (kc, ks, vc, vs), table = decode_inputs(rng, lens, hq, hkv, d, block, dtype, spread=0)
+    q[:] = 1.0
+    qt.copy_(to_dev(q.astype(np.float32)))
+    early, late = table[0, : n // 32], table[0, n // 32:]
+    kc[early] = Q.encode(np.abs(Q.VALUES[kc[early] & 0x77]) + 32)
+    kc[late] = Q.encode(-np.abs(Q.VALUES[kc[late] & 0x77]) - 32)
+    vs[early], vs[late] = first, then
+    got = pkv.paged_decode_q8(qt, pool(kc), pool(vc), to_dev(ks), to_dev(vs), to_dev(table),
+                              to_dev(np.array(lens, np.int32)), scale=2.0)
+    # (in 64 bits the late keys would weigh 2^-700 and less)
+    late_v = vs.copy()
+    late_v[late] = 0.0
+    want, mass, reach = decode_want(q, kc, ks, vc, late_v, table, lens, 2.0, block)
+    err = np.abs(widen(got) - want)
+    assert np.all(err <= decode_bound(want, mass, reach, lens, dtype))
+
+
 def test_decode_nans_stay_with_their_own():
     rng = np.random.default_rng(3)
     lens, hq, hkv, d, block = [100, 64, 40], 8, 4, 128, 16
