@@ -620,7 +620,7 @@ int paged_kv_compact(void* k_cache, void* v_cache, const int32_t* block_table,
  *              may be q itself with q's stride, receives them rotated.  The row of a
  *              padding token, or of one whose position is outside the table, is passed on
  *              as it is.
- *   q_stride, q_out_stride   elements from token to token
+ *   q_stride, q_out_stride   elements from token to token; equal where q_out is q
  */
 typedef struct pkv_rope {
     const float* cos_sin;

@@ -80,6 +80,9 @@ int fill(pkv::RopeWriteLaunch* r, const void* k, int64_t k_stride, const void* v
                 !rows_ok(rope->q_out, rope->q_out_stride, elt) ||
                 rope->q_out_stride < (int64_t)g->num_heads * g->head_dim)
                 return PKV_ERR_INVALID;
+            // in place: a row must not land on another token's
+            if (rope->q == rope->q_out && rope->q_stride != rope->q_out_stride && num_tokens > 1)
+                return PKV_ERR_INVALID;
             r->q = rope->q;
             r->q_out = rope->q_out;
             r->q_stride = rope->q_stride;

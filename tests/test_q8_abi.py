@@ -74,6 +74,13 @@ def test_write_refusals(lib, func):
     assert f(n=0, r=rope(rotary_dim=256)) == -1
 
 
+@pytest.mark.parametrize("func", ["paged_kv_write_rope", "paged_kv_write_q8"])
+def test_queries_in_place_keep_their_stride(lib, func):
+    for q_stride, out_stride in ((4096, 2048), (2048, 4096), (0, 2048)):
+        r = rope(q=P, q_out=P, q_stride=q_stride, q_out_stride=out_stride)
+        assert write(lib, func, r=r, n=3) == -1
+
+
 def test_write_rope_needs_a_rotation_and_write_q8_its_scales(lib):
     assert write(lib, "paged_kv_write_rope", r=None) == -1
     assert write(lib, "paged_kv_write_q8", k_scale=None) == -1
