@@ -288,20 +288,26 @@ __device__ __forceinline__ int find_runs(const NewTokens& t, const RopeTable& ta
     if (begins) {
         int len = 1 + bits_from(w->goes_on, tid + 1);
         if (tid + len == kWindow) {
-            int more = bits_from(w->behind, 0);
-            if (more == kWindow) {  // (pages of more than 256: one by one)
-                for (int64_t m = n0 + 2 * kWindow; m < t.num && __ldg(t.seq + m) == s; ++m, ++more) {
-                    const int32_t q = __ldg(t.pos + m);
-                    if (q < 0 || block(q) != block(p)) break;
-                }
-            }
-            len += more;
+            len += bits_from(w->behind, 0);
         }
         w->first[k] = tid;
         w->page[k] = page;
         w->len[k] = len;
     }
     __syncthreads();
+    if (t.block.d <= kWindow || total == 0) return total;
+    // larger pages: the last run may go on for windows
+    int more = w->first[total - 1] + w->len[total - 1] == 2 * kWindow ? kWindow : 0;
+    for (int64_t m = n + 2 * kWindow; more == kWindow; m += kWindow) {
+        const bool same = m < t.num && __ldg(t.seq + m) == sl && __ldg(t.pos + m) >= 0 &&
+                          block(__ldg(t.pos + m)) == block(pl);
+        const uint32_t words = __ballot_sync(0xffffffffu, same);
+        if (lane == 0) w->behind[warp] = words;
+        __syncthreads();
+        more = bits_from(w->behind, 0);
+        if (tid == 0) w->len[total - 1] += more;
+        __syncthreads();
+    }
     return total;
 }
 

@@ -55,6 +55,10 @@ WRITES = [  # (cached, new), Hq, Hkv, d, rot (0: none), interleaved, B, type, pa
     ([(7, 3000), (0, 2000)], 2, 1, 64, 64, False, 16, "bf16", 0, 0),
     ([(0, 64)] * 3, 4, 4, 128, 128, False, 64, "bf16", 0, 0),
     ([(2, 130)], 4, 4, 128, 128, True, 128, "f32", 0, 0),
+    # runs that go on for windows of 256 tokens, and end with one, behind one or before one
+    ([(0, 768), (4090, 1), (1, 511), (40, 257)], 2, 1, 64, 64, False, 4096, "bf16", 0, 0),
+    ([(3, 2500), (1900, 700)], 2, 2, 128, 0, False, 2048, "f32", 0, 0),
+    ([(200, 1), (0, 255), (5, 513), (0, 1025)], 1, 1, 64, 32, True, 600, "bf16", 7, 0),
 ]
 
 
