@@ -4,7 +4,7 @@
 // into libpagedkv.so, whose entry points _binding.py hands over.  A small call takes the
 // GPU 4 us; marshalled in Python it took the host 17 to 20.  Like the rest of the
 // binding it computes nothing.
-#include <ATen/ops/empty.h>
+#include <ATen/cuda/EmptyTensor.h>
 #include <c10/cuda/CUDAGuard.h>
 #include <c10/cuda/CUDAStream.h>
 #include <torch/csrc/Dtype.h>
@@ -71,6 +71,12 @@ int32_t* int32s_or_null(PyObject* o, const char* name, int index, int64_t n) {
     const at::Tensor& t = tensor(o, name);
     if (t.numel() != n) value_error(std::string(name) + " must have one entry per token row");
     return int32s(t, name, index);
+}
+
+// (straight from the allocator: the dispatcher's way there takes as long again)
+at::Tensor new_tensor(at::IntArrayRef sizes, at::ScalarType dtype, int index) {
+    return at::Tensor(at::detail::empty_cuda(
+        sizes, dtype, c10::Device(c10::kCUDA, (c10::DeviceIndex)index), std::nullopt));
 }
 
 int32_t dtype_code(at::ScalarType t) {
@@ -198,7 +204,7 @@ PyObject* write_impl(PyObject* const* a) {
             g.num_heads = (int32_t)q.size(1);
             rope.q = row_address(q, "q", index, dtype, &rope.q_stride);
             if (a[11] == Py_None) {
-                made = at::empty(q.sizes(), q.options());
+                made = new_tensor(q.sizes(), dtype, index);
                 rope.q_out = row_address(made, "q_out", index, dtype, &rope.q_out_stride);
             } else {
                 const at::Tensor& out = tensor(a[11], "q_out");
@@ -250,7 +256,7 @@ PyObject* read_q8_impl(PyObject* const* a) {
     const int32_t code = dtype_code(dtype);
     if (a[7] != Py_None) out[1] = tensor(a[7], "v_out");
     for (at::Tensor& t : out)
-        if (!t.defined()) t = at::empty(at::IntArrayRef(shape, 3), kc.options().dtype(dtype));
+        if (!t.defined()) t = new_tensor(at::IntArrayRef(shape, 3), dtype, index);
     for (const at::Tensor& t : out)
         if (t.sizes() != at::IntArrayRef(shape, 3)) value_error("k_out / v_out must be [N, Hkv, d]");
     void* kp = address(out[0], "k_out", index, dtype);
@@ -300,15 +306,14 @@ PyObject* decode_q8_impl(PyObject* const* a) {
         out = tensor(a[8], "out");
         if (out.sizes() != q.sizes()) value_error("out must have q's shape");
     } else {
-        out = at::empty(q.sizes(), q.options());
+        out = new_tensor(q.sizes(), dtype, index);
     }
     void* op = address(out, "out", index, dtype);
     if (a[9] != Py_None) {
         workspace = tensor(a[9], "workspace");
         address(workspace, "workspace", index, workspace.scalar_type());
     } else {
-        workspace = at::empty({(int64_t)g_decode_q8_size(batch, code, &g)},
-                              q.options().dtype(at::kByte));
+        workspace = new_tensor({(int64_t)g_decode_q8_size(batch, code, &g)}, at::kByte, index);
     }
     if (!ok("paged_decode_q8",
             g_decode_q8(qp, code, p.k, p.v, p.k_scale, p.v_scale, tp, (int32_t)table.size(1), lp,

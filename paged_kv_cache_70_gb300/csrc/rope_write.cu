@@ -12,7 +12,7 @@
 //
 // Measured: 16,729 tokens of 16 / 8 heads of 128, bf16, the columns of one projection, into
 // pages of 256, 282.8 MB: 45.6 us, 6205 GB/s (0.93 of the measured copy rate).  2430 tokens
-// of 16 / 8 heads of 64 in fp32 into bf16 pools, 36.2 MB: 7.8 us.  64 tokens: 4.5 us a
+// of 16 / 8 heads of 64 in fp32 into bf16 pools, 36.2 MB: 7.8 us.  64 tokens: 4.1 us a
 // call among others, what the host takes to make it.
 #include "common.cuh"
 #include "launch.h"
