@@ -15,6 +15,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "divide.cuh"
 
 namespace pkv {
 

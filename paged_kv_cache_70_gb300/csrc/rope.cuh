@@ -16,6 +16,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "divide.cuh"
 
 namespace pkv {
 
