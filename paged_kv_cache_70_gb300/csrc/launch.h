@@ -32,6 +32,25 @@ cudaError_t launch_dependent(void (*kern)(Params...), dim3 grid, dim3 block, siz
     return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
 }
 
+// The same with `cluster` CTAs (along x) in a cluster.
+template <typename... Params, typename... Args>
+cudaError_t launch_clusters(void (*kern)(Params...), int cluster, dim3 grid, dim3 block,
+                            size_t smem, cudaStream_t stream, Args&&... args) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = block;
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim = {(unsigned)cluster, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, static_cast<Args&&>(args)...);
+}
+
 // First statement of such kernels: let the next kernel launch early, then wait
 // for this one's inputs.
 #define PKV_DEPENDENT_PROLOGUE()                                  \
@@ -303,7 +322,8 @@ struct Q8DecodePlan {
     int ctas;         // grid.x (CTAs along the keys)
     int tile;         // keys per stage
     int piece;        // keys per copy (divides the tile and the page)
-    bool whole;       // a CTA per sequence and head group, no partial states
+    int cluster;      // CTAs that take a sequence and head group, 0: the tiles of all
+                      // sequences are split, and a second kernel merges partial states
     int stages;
     size_t smem_bytes;
     size_t ws_bytes;  // workspace bytes needed (the same for every max_blocks)

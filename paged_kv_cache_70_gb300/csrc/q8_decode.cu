@@ -30,8 +30,8 @@
 //    swizzle (d = 64: 64-byte) so that a fragment's loads touch all banks once; the
 //    other warps own a (head, 8 queries) and 16 of the tile's keys each and hold a
 //    stage for their loads only.
-//    Short sequences that need no splitting (plan_q8_decode) are a CTA's each, which
-//    writes the output itself.
+//    Short sequences (plan_q8_decode) need no second kernel: a CTA takes one, or a
+//    cluster shares one and its CTAs read each other's states.
 //  * Keys of a page outside the pool are skipped and flagged; rows past the length
 //    never enter: scores of -inf, V codes and scales of 0, whatever the page holds
 //    there.  Every wait is time-limited.
@@ -40,7 +40,7 @@
 //   8 sequences of 16 K - 41 K keys, 16 / 8 heads, d = 128, 485 MB     77.5 us  0.93
 //   the same with 64 / 8 heads                                          78.8 us  0.92
 //   64 sequences of 128 - 4096 keys, 16 / 8 heads, B = 16, 278 MB       51.1 us  0.81
-//   one of 7777 keys, 32 / 4 heads, d = 64                               9.1 us
+//   one of 7777 keys, 32 / 4 heads, d = 64                               8.4 us
 // From one to four times the long contexts the time grows by 6980 GB/s, above the copy
 // rate.  What stands around the stream: ~5 us to the first copy (wait for the launch, plan,
 // table), ~4 us that the SMs' last tiles lie apart, by chance, and ~4 us from the last tile
@@ -71,6 +71,7 @@ template <bool F32>
 __host__ __device__ constexpr float grow_by() { return F32 ? 2.f : 8.f; }
 constexpr int kProducers = 4;
 constexpr int kMaxStages = 8;
+constexpr int kMaxCluster = 16;  // (more than 8 have to be asked for)
 constexpr int kHeader = 512;  // barriers and stage tags
 constexpr size_t kStaticSmem = 1024;  // left for static shared memory
 constexpr int kAlign = 1024;  // of the ring: the swizzle's period
@@ -91,7 +92,7 @@ struct Q8DecodeArgs {
     float* part_o;     // [ctas + batch][hq][D]
     float* part_ml;    // [ctas + batch][hq][2]
     int32_t* tstart;   // [batch + 1]
-    void* out;         // WHOLE
+    void* out;         // WHOLE, CLUSTER
     unsigned int* err;
     int64_t num_blocks;
     float qscale;  // scale * log2(e)
@@ -101,6 +102,7 @@ struct Q8DecodeArgs {
     int32_t wh;      // warps that share a head and its queries (16 of a tile's keys each)
     int32_t piece;   // keys per copy
     int32_t stages;
+    int32_t cluster;  // CTAs that share a sequence (CLUSTER)
     FastDiv block, tile;  // by the page size, and by a tile's keys
 };
 
@@ -153,14 +155,38 @@ __device__ __forceinline__ uint32_t swizzle(uint32_t off) {
     return D == 128 ? (off >> 3) & 0x70u : (off >> 3) & 0x30u;
 }
 
-template <int D, bool F32, bool WHOLE>
+// the word of shared memory that lies at `at` in CTA `cta` of the cluster
+__device__ __forceinline__ uint32_t at_cta(uint32_t at, int cta) {
+    uint32_t y;
+    asm("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(y) : "r"(at), "r"(cta));
+    return y;
+}
+__device__ __forceinline__ float4 load_cluster(uint32_t at) {
+    float4 y;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(y.x), "=f"(y.y), "=f"(y.z), "=f"(y.w) : "r"(at) : "memory");
+    return y;
+}
+// all threads of the cluster that have not ended
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// What a CTA takes: its share of the line of all tiles, a sequence (and its heads), or
+// its part of one that its cluster shares
+enum Mode { SPLIT, WHOLE, CLUSTER };
+
+template <int D, bool F32, Mode MODE>
 __global__ void __launch_bounds__(threads<F32>(), 1)
 q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
                 const __grid_constant__ CUtensorMap vmap) {
-    // WHOLE: the CTA's only sequence is blockIdx.x
-    const int batch = WHOLE ? 1 : a.batch;
-    const int32_t* const seqlens = a.seqlens + (WHOLE ? blockIdx.x : 0);
-    const int32_t* const table = a.table + (WHOLE ? (int64_t)blockIdx.x * a.max_blocks : 0);
+    // one sequence, `own`, unless the tiles are SPLIT; part `part` of it
+    constexpr bool ONE = MODE != SPLIT;
+    const int own = MODE == CLUSTER ? blockIdx.x / a.cluster : ONE ? blockIdx.x : 0;
+    const int part = MODE == CLUSTER ? blockIdx.x - own * a.cluster : 0;
+    const int batch = ONE ? 1 : a.batch;
+    const int32_t* const seqlens = a.seqlens + own;
+    const int32_t* const table = a.table + (int64_t)own * a.max_blocks;
     constexpr int WC = consumers<F32>();
     constexpr int PARTS = F32 ? 2 : 1;
     constexpr int KW = D / 16;   // words of K codes per lane and row: 16-dim steps
@@ -177,7 +203,8 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
     const int S = a.stages, T = 16 * a.wh, P = a.piece;
     const int pieces = T / P;
     // scales [stage][piece][head]: K's and V's
-    float* scales = reinterpret_cast<float*>(scratch + (size_t)units * (a.wh - 1) * state_bytes(D));
+    float* scales = reinterpret_cast<float*>(
+        scratch + (size_t)units * (a.wh - (MODE == CLUSTER ? 0 : 1)) * state_bytes(D));
     unsigned char* ring = reinterpret_cast<unsigned char*>(scales) + (size_t)S * pieces * a.hc * 8;
     ring += (0u - smem_u32(ring)) % kAlign;
     __shared__ int32_t warp_sum[threads<F32>() / 32];
@@ -201,7 +228,7 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
 
     // ---- plan: tile starts of the sequences (an exclusive scan of their tiles)
     const int64_t cap = (int64_t)a.max_blocks * a.block_size;
-    const bool first_cta = (WHOLE || blockIdx.x == 0) && blockIdx.y == 0;
+    const bool first_cta = (ONE ? part == 0 : blockIdx.x == 0) && blockIdx.y == 0;
     {
         // (what comes next, the table, is on its way meanwhile: 64 KB of it at most)
         const int64_t line = (int64_t)tid * 128;
@@ -222,7 +249,7 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
             }
             return x;
         };
-        if (WHOLE || batch <= 32) {  // one warp's work
+        if (ONE || batch <= 32) {  // one warp's work
             if (warp == 0) {
                 const int32_t x = scan(lane < batch ? tiles(lane) : 0);
                 if (lane < batch) tstart[lane + 1] = x;
@@ -255,12 +282,17 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int head0 = blockIdx.y * a.hc;
     int32_t t0 = 0, t1 = total;
-    if constexpr (WHOLE) {
+    if constexpr (ONE) {
         if (total == 0) {  // no keys
-            const int64_t at = ((int64_t)blockIdx.x * a.hq + head0 * (a.hq / a.hkv)) * D;
+            const int64_t at = ((int64_t)own * a.hq + head0 * (a.hq / a.hkv)) * D;
             uint32_t* const o = static_cast<uint32_t*>(a.out) + (F32 ? at : at / 2);
-            for (int i = tid; i < a.hc * (a.hq / a.hkv) * D / (F32 ? 1 : 2); i += blockDim.x) o[i] = 0u;
+            const int words = part == 0 ? a.hc * (a.hq / a.hkv) * D / (F32 ? 1 : 2) : 0;
+            for (int i = tid; i < words; i += blockDim.x) o[i] = 0u;
             return;
+        }
+        if constexpr (MODE == CLUSTER) {
+            t0 = (int32_t)((int64_t)total * part / a.cluster);
+            t1 = (int32_t)((int64_t)total * (part + 1) / a.cluster);
         }
     } else {
         if (first_cta)  // for the combine, which reads them behind its wait
@@ -446,7 +478,7 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
         if (r < nq) {
 #pragma unroll
             for (int w = 0; w < KW; w += F32 ? 1 : 2) {
-                const int64_t at = ((int64_t)(WHOLE ? blockIdx.x : seq) * a.hq + qh0 + r) * D + 16 * c + (w & 3) * 4 +
+                const int64_t at = ((int64_t)(ONE ? own : seq) * a.hq + qh0 + r) * D + 16 * c + (w & 3) * 4 +
                                    (w >= 4 ? 64 : 0);
                 if constexpr (F32) {
                     const float4 u =
@@ -490,6 +522,19 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
     };
 
     int merges = 0;
+    // CLUSTER: where this head's and these queries' state of the CTA is left for the others
+    float4* const left = reinterpret_cast<float4*>(
+        scratch + (size_t)((a.wh - 1) * units + unit) * state_bytes(D));
+    bool none = true;
+    // (a store of 4 outputs of query 2c + i, D / 8 r + x first)
+    auto store4 = [&](int i, int x, float4 y) {
+        const int64_t at = ((int64_t)own * a.hq + qh0 + 2 * c + i) * D + D / 8 * r + x;
+        if constexpr (F32)
+            *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at) = y;
+        else
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at) =
+                make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
+    };
     const int32_t n_tiles = t1 - t0;
     uint32_t full_bar = smem_u32(full), empty_bar = smem_u32(empty);
     asm volatile("" : "+r"(full_bar), "+r"(empty_bar));  // (keep them)
@@ -728,23 +773,27 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
             ++merges;
         }
         if (rank != 0) continue;
-        if constexpr (WHOLE) {
+        if constexpr (MODE == WHOLE) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 if (2 * c + i >= nq) continue;
                 const float inv = l2[i] == 0.f ? 0.f : 1.f / l2[i];
-                const int64_t at = ((int64_t)blockIdx.x * a.hq + qh0 + 2 * c + i) * D + D / 8 * r;
 #pragma unroll
-                for (int x = 0; x < D / 8; x += 4) {
-                    const float4 y = make_float4(val[i][x] * inv, val[i][x + 1] * inv,
-                                                 val[i][x + 2] * inv, val[i][x + 3] * inv);
-                    if constexpr (F32)
-                        *reinterpret_cast<float4*>(static_cast<float*>(a.out) + at + x) = y;
-                    else
-                        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + at + x) =
-                            make_uint2(pack_bf16x2(y.x, y.y), pack_bf16x2(y.z, y.w));
-                }
+                for (int x = 0; x < D / 8; x += 4)
+                    store4(i, x, make_float4(val[i][x] * inv, val[i][x + 1] * inv,
+                                             val[i][x + 2] * inv, val[i][x + 3] * inv));
             }
+            continue;
+        }
+        if constexpr (MODE == CLUSTER) {
+            left[lane] = make_float4(m2[0], m2[1], l2[0], l2[1]);
+#pragma unroll
+            for (int i = 0; i < 2; ++i)
+#pragma unroll
+                for (int x = 0; x < D / 8; x += 4)
+                    left[(1 + i * (D / 32) + x / 4) * 32 + lane] =
+                        make_float4(val[i][x], val[i][x + 1], val[i][x + 2], val[i][x + 3]);
+            none = false;
             continue;
         }
         const int64_t slot = (int64_t)blockIdx.x + seq;
@@ -759,12 +808,93 @@ q8_split_kernel(const Q8DecodeArgs a, const __grid_constant__ CUtensorMap kmap,
             if (r == 0) *reinterpret_cast<float2*>(a.part_ml + at * 2) = make_float2(m2[i], l2[i]);
         }
     }
+    if constexpr (MODE == CLUSTER) {
+        // The parts' states, merged: piece q (4 values per lane) of a head and its queries by
+        // the q-th CTA of the cluster.  Every warp that has work comes here, after a wait that
+        // ran out too.
+        if (rank == 0 && none) {  // no tile was this CTA's
+            left[lane] = make_float4(-INFINITY, -INFINITY, 0.f, 0.f);
+            for (int q = 0; q < D / 16; ++q) left[(1 + q) * 32 + lane] = make_float4(0.f, 0.f, 0.f, 0.f);
+        }
+        cluster_sync();
+        const uint32_t here = smem_u32(left + lane);
+        for (int q = part + a.cluster * rank; q < D / 16; q += a.cluster * a.wh) {
+            const int i = q / (D / 32);
+            float M = -INFINITY, L = 0.f;
+            float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+            for (int j0 = 0; j0 < a.cluster; j0 += 8) {
+                float4 y[8];
+                float mj[8], lj[8], top = M;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    mj[j] = -INFINITY;
+                    if (j0 + j >= a.cluster) continue;
+                    const uint32_t there = at_cta(here, j0 + j);
+                    const float4 st = load_cluster(there);
+                    mj[j] = i ? st.y : st.x;
+                    lj[j] = i ? st.w : st.z;
+                    y[j] = load_cluster(there + (1 + q) * 512);
+                }
+#pragma unroll
+                for (int j = 0; j < 8; ++j) top = fmaxf(top, mj[j]);
+                const float f0 = M == -INFINITY ? 0.f : ex2(M - top);
+                M = top;
+                L *= f0;
+                sum = make_float4(sum.x * f0, sum.y * f0, sum.z * f0, sum.w * f0);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    if (mj[j] == -INFINITY) continue;  // (no key)
+                    const float f = ex2(mj[j] - M);
+                    L += lj[j] * f;
+                    sum.x += y[j].x * f;
+                    sum.y += y[j].y * f;
+                    sum.z += y[j].z * f;
+                    sum.w += y[j].w * f;
+                }
+            }
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            if (2 * c + i < nq)
+                store4(i, 4 * (q % (D / 32)),
+                       make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv));
+        }
+        cluster_sync();  // (no CTA ends while its state is read)
+    }
 }
 
-template <int D, bool F32, bool WHOLE>
+// How many clusters of n CTAs, each with an SM to itself, fit on the GPU (its SMs lie in
+// groups of unequal size that no cluster spans).  Asked once per device and n.
+int clusters_that_fit(const DeviceInfo& dev, int n) {
+    static std::atomic<int> known[64][kMaxCluster + 1];  // 1 more than the answer
+    std::atomic<int>& fit = known[dev.device & 63][n];
+    if (const int k = fit.load(std::memory_order_relaxed)) return k - 1;
+    auto kern = q8_split_kernel<128, false, CLUSTER>;
+    const int smem = (int)(dev.max_smem_optin - kStaticSmem);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(n);
+    cfg.blockDim = dim3(threads<false>());
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim = {(unsigned)n, 1, 1};
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    int k = 0;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) !=
+            cudaSuccess ||
+        cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) !=
+            cudaSuccess ||
+        cudaOccupancyMaxActiveClusters(&k, kern, &cfg) != cudaSuccess) {
+        cudaGetLastError();
+        return 0;
+    }
+    fit.store(k + 1, std::memory_order_relaxed);
+    return k;
+}
+
+template <int D, bool F32, Mode MODE>
 cudaError_t launch_split(const DeviceInfo& dev, const Q8DecodePlan& p, const Q8DecodeArgs& a,
                          const CUtensorMap& kmap, const CUtensorMap& vmap, cudaStream_t stream) {
-    auto kern = q8_split_kernel<D, F32, WHOLE>;
+    auto kern = q8_split_kernel<D, F32, MODE>;
     // the most shared memory a CTA may have, set once per device
     static std::atomic<uint64_t> set{0};
     const uint64_t bit = 1ull << dev.device;
@@ -773,9 +903,17 @@ cudaError_t launch_split(const DeviceInfo& dev, const Q8DecodePlan& p, const Q8D
             kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
             (int)(dev.max_smem_optin - kStaticSmem));
         if (e != cudaSuccess) return e;
+        if (MODE == CLUSTER) {
+            const cudaError_t f =
+                cudaFuncSetAttribute(kern, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+            if (f != cudaSuccess) return f;
+        }
         set.fetch_or(bit, std::memory_order_relaxed);
     }
-    return launch_dependent(kern, dim3(WHOLE ? a.batch : p.ctas, p.head_groups),
+    if (MODE == CLUSTER)
+        return launch_clusters(kern, p.cluster, dim3(a.batch * p.cluster, p.head_groups),
+                               dim3(threads<F32>()), p.smem_bytes, stream, a, kmap, vmap);
+    return launch_dependent(kern, dim3(MODE == WHOLE ? a.batch : p.ctas, p.head_groups),
                             dim3(threads<F32>()), p.smem_bytes, stream, a, kmap, vmap);
 }
 
@@ -816,35 +954,73 @@ bool plan_q8_decode(const DeviceInfo& dev, int32_t batch, int32_t max_blocks, in
     auto at_work = [&](int h) { return wc / (h * p->no) * (h * p->no); };
     for (int h = 1; h <= hkv && h * p->no <= std::max(6, p->no); ++h)
         if (hkv % h == 0 && (5 * at_work(h) >= 4 * wc || at_work(h) > at_work(p->hc))) p->hc = h;
-    p->head_groups = hkv / p->hc;
-    if (p->head_groups > 65535) return false;
-    const int units = p->hc * p->no;
-    p->wh = wc / units;
-    p->tile = 16 * p->wh;
-    p->piece = std::gcd(p->tile, block_size);
-    const size_t stage = (size_t)2 * p->hc * p->tile * d;
-    const size_t stage_scales = (size_t)p->tile / p->piece * p->hc * 8;
-    const size_t fixed = kHeader + up((size_t)(batch + 1) * 4, 128) +
-                         (size_t)units * (p->wh - 1) * state_bytes(d);
+    // what follows from the heads of a CTA and from the CTAs of a cluster
     const size_t room = dev.max_smem_optin - kStaticSmem - kAlign;
-    if (room < fixed + 2 * (stage + stage_scales)) return false;
-    p->stages = (int)std::min<size_t>(kMaxStages, (room - fixed) / (stage + stage_scales));
-    p->smem_bytes = fixed + p->stages * (stage + stage_scales) + kAlign;
+    auto shape = [&](int hc, int cluster) {
+        const int units = hc * p->no;
+        p->hc = hc;
+        p->cluster = cluster;
+        p->head_groups = hkv / hc;
+        p->wh = wc / units;
+        p->tile = 16 * p->wh;
+        p->piece = std::gcd(p->tile, block_size);
+        const size_t stage = (size_t)2 * hc * p->tile * d;
+        const size_t stage_scales = (size_t)p->tile / p->piece * hc * 8;
+        const size_t fixed = kHeader + up((size_t)(batch + 1) * 4, 128) +
+                             (size_t)units * (p->wh - (cluster > 1 ? 0 : 1)) * state_bytes(d);
+        if (room < fixed + 2 * (stage + stage_scales)) return false;
+        p->stages = (int)std::min<size_t>(kMaxStages, (room - fixed) / (stage + stage_scales));
+        p->smem_bytes = fixed + p->stages * (stage + stage_scales) + kAlign;
+        return true;
+    };
+    if (hkv / p->hc > 65535 || !shape(p->hc, 0)) return false;
     // one CTA per SM, no more than there can be tiles
     const int64_t tiles = ((int64_t)max_blocks * block_size + p->tile - 1) / p->tile * batch;
     const int64_t most = std::max(1, dev.num_sms / p->head_groups);
     if (tiles + batch > 0x7fffffffLL - most) return false;  // the line of tiles is 32 bits long
     p->ctas = (int)std::max<int64_t>(1, std::min(most, tiles));
-    // Sequences that the table keeps short, no more than there are SMs: a CTA takes all of
-    // one (and its heads), and no second kernel is needed.  At 16 / 8 heads, d = 128, 48 keys
-    // per tile, whole and split: one sequence of 40 keys 8.2 and 10.3 us, 180 keys 10.0 and
-    // 10.3, 380 keys 12.3 and 10.3; 64 sequences of 90 keys 8.6 and 14.7, 760 keys 22.6 and
-    // 25.6, 1500 keys 35.5 and 35.5.
-    const int64_t whole = (int64_t)batch * p->head_groups;
-    p->whole = tiles <= (4 + 12 * whole / dev.num_sms) * batch && whole <= dev.num_sms;
     const size_t slots = (size_t)most + batch;  // whatever the table's width is
     p->ws_bytes = up((size_t)(batch + 1) * 4, 256) + up(slots * hq * 2 * 4, 256) +
                   up(slots * hq * d * 4, 256);
+    // Sequences that the table keeps short enough need no second kernel: a cluster shares each
+    // (and its heads), or one CTA takes it.
+    const Q8DecodePlan split = *p;
+    const double head_bytes = (double)max_blocks * block_size * 2 * d;  // a sequence's of one head
+    // The clusters that put most SMs to work, all of them at once; 16 CTAs where 8 would have 40 KB
+    // each or more (32 / 4 heads of 64, 8 and 16: 1000 keys 6.3 and 6.8 us, 6000 8.3 and 7.4).
+    int hc = 1, cluster = 0;
+    int64_t ctas = 0;
+    for (int n = 2; n <= kMaxCluster; n *= 2) {
+        const int64_t fit = clusters_that_fit(dev, n);
+        for (int h = 1; h <= split.hc; ++h) {
+            const int64_t m = (int64_t)batch * (hkv / h);
+            if (hkv % h == 0 && m <= fit && m * n > ctas && (n <= 8 || head_bytes * h >= 320e3)) {
+                hc = h;
+                cluster = n;
+                ctas = m * n;
+            }
+        }
+    }
+    // One CTA: up to 4 tiles, more where that puts most SMs to work, and no more than 150 KB where
+    // there are SMs to share them.  At 16 / 8 heads, d = 128, 48 keys per tile, one CTA and a
+    // cluster of 8 (4): one sequence of 20 keys 4.8 and 7.1 us, 140 6.6 and 7.3, 190 7.5 and 7.4;
+    // 16 of 190 keys 7.7 and 7.2, 60 of 190 9.0 and (split) 14.1, of 700 23.5 and 23.7; at 4 / 1
+    // heads one of 250 keys 7.0 and 7.0, 700 8.5 and 6.8.
+    const int64_t whole = (int64_t)batch * split.head_groups;
+    if (tiles <= (4 + 12 * whole / dev.num_sms) * batch && whole <= dev.num_sms &&
+        (ctas < 4 * whole || head_bytes * split.hc <= 150e3)) {
+        p->cluster = 1;
+        return true;
+    }
+    // A cluster: where the second kernel costs more (1.6 us and the longer the more sequences it
+    // has, or 70 KB and 3 KB each of what an SM streams) than SMs without work do.  At 16 / 8 heads, d = 128, cluster and split: one sequence of 1000 keys
+    // 7.3 and 8.5 us, 4000 9.1 and 9.1, 8000 12.1 and 10.4; 4 of 2000 9.5 and 10.9, of 16000 29.2
+    // and 29.4; 16 of 300 7.9 and 10.0, of 2000 18.0 and 20.0; at 32 / 4 heads of 64 one of 12000
+    // 8.8 and 9.8, of 16000 10.4 and 9.8, 16 of 1000 7.9 and 11.5.
+    if (ctas == 0 ||
+        head_bytes * hc / cluster * (1 - (double)ctas / dev.num_sms) > 70e3 + 3e3 * batch ||
+        !shape(hc, cluster))
+        *p = split;
     return true;
 }
 
@@ -882,6 +1058,7 @@ cudaError_t launch_q8_decode(const DeviceInfo& dev, const Q8DecodePlan& p, const
     a.wh = p.wh;
     a.piece = p.piece;
     a.stages = p.stages;
+    a.cluster = p.cluster;
     a.block = FastDiv((uint32_t)block_size);
     a.tile = FastDiv((uint32_t)p.tile);
     CUtensorMap kmap, vmap;
@@ -893,11 +1070,12 @@ cudaError_t launch_q8_decode(const DeviceInfo& dev, const Q8DecodePlan& p, const
     cudaError_t e = cudaErrorInvalidValue;
 #define PKV_Q8_CASE(DD, FF)                                                         \
     if (d == DD && f32 == FF)                                                       \
-        e = p.whole ? launch_split<DD, FF, true>(dev, p, a, kmap, vmap, stream)     \
-                    : launch_split<DD, FF, false>(dev, p, a, kmap, vmap, stream);
+        e = p.cluster > 1 ? launch_split<DD, FF, CLUSTER>(dev, p, a, kmap, vmap, stream) \
+            : p.cluster   ? launch_split<DD, FF, WHOLE>(dev, p, a, kmap, vmap, stream)   \
+                          : launch_split<DD, FF, SPLIT>(dev, p, a, kmap, vmap, stream);
     PKV_Q8_CASE(128, false) PKV_Q8_CASE(128, true) PKV_Q8_CASE(64, false) PKV_Q8_CASE(64, true)
 #undef PKV_Q8_CASE
-    if (e != cudaSuccess || p.whole) return e;
+    if (e != cudaSuccess || p.cluster) return e;
     return launch_combine(d, f32, a.part_o, a.part_ml, a.tstart, out, batch, hq, p.ctas, stream);
 }
 

@@ -361,6 +361,51 @@ def test_decode(lens, hq, hkv, d, block, dtype):
     assert np.all(np.isfinite(err)) and np.all(err <= bound), (err / bound).max()
 
 
+@pytest.mark.parametrize("lens,hq,hkv,d,block,dtype", DECODE)
+def test_decode_with_a_table_for_longer_contexts(lens, hq, hkv, d, block, dtype):
+    """The same sequences where the table could hold 400,000 keys of each: what is a CTA's or a
+    cluster's there is split here."""
+    rng = np.random.default_rng(len(lens) + hq * 3 + d + block)
+    q, qt, (kc, ks, vc, vs), table = decode_inputs(rng, lens, hq, hkv, d, block, dtype)
+    wide = np.full((len(lens), 400000 // block), -1, np.int32)
+    wide[:, :table.shape[1]] = table
+    got = pkv.paged_decode_q8(qt, pool(kc), pool(vc), to_dev(ks), to_dev(vs), to_dev(wide),
+                              to_dev(np.array(lens, np.int32)))
+    assert pkv.paged_error_flags() == 0
+    want, mass, reach = decode_want(q, kc, ks, vc, vs, table, lens, 1 / math.sqrt(d), block)
+    err = np.abs(widen(got) - want)
+    assert np.all(err <= decode_bound(want, mass, reach, lens, dtype))
+
+
+CLUSTERS = [  # lens, Hq, Hkv, d, B, type, keys that the table holds
+    ([0, 1, 191, 192, 193, 1536, 1537, 2000], 4, 1, 128, 16, "bf16", 2000),  # fewer tiles than CTAs
+    ([0, 5, 3000], 32, 4, 64, 16, "bf16", 4096),
+    ([0], 16, 8, 128, 16, "f32", 4096),
+    ([1, 4096], 40, 2, 128, 32, "bf16", 4096),   # 20 queries per KV head: three warps' worth
+    ([700, 0, 33, 1500] * 4, 16, 8, 128, 16, "f32", 1500),
+    ([1000] * 30, 16, 8, 128, 64, "bf16", 1024),
+    ([990, 77] * 30, 8, 4, 64, 2, "bf16", 1000),
+    ([64, 900] * 9, 6, 6, 128, 1, "bf16", 900),
+    ([800, 31], 64, 1, 64, 8, "f32", 800),
+]
+
+
+@pytest.mark.parametrize("lens,hq,hkv,d,block,dtype,keys", CLUSTERS)
+def test_decode_of_sequences_that_clusters_share(lens, hq, hkv, d, block, dtype, keys):
+    rng = np.random.default_rng(keys + hq)
+    q, qt, (kc, ks, vc, vs), table = decode_inputs(rng, lens, hq, hkv, d, block, dtype)
+    wide = np.full((len(lens), -(-keys // block)), -1, np.int32)
+    wide[:, :table.shape[1]] = table
+    args = (qt, pool(kc), pool(vc), to_dev(ks), to_dev(vs), to_dev(wide),
+            to_dev(np.array(lens, np.int32)))
+    got = pkv.paged_decode_q8(*args)
+    assert pkv.paged_error_flags() == 0
+    want, mass, reach = decode_want(q, kc, ks, vc, vs, table, lens, 1 / math.sqrt(d), block)
+    err = np.abs(widen(got) - want)
+    assert np.all(err <= decode_bound(want, mass, reach, lens, dtype))
+    assert torch.equal(got, pkv.paged_decode_q8(*args))
+
+
 @pytest.mark.parametrize("dtype", ["bf16", "f32"])
 @pytest.mark.parametrize("spread", [20, 60])
 def test_decode_scales_far_apart(dtype, spread):

@@ -27,7 +27,7 @@ def _flags(lib):
     return v.value
 
 
-@pytest.mark.parametrize("width", [125, 7])
+@pytest.mark.parametrize("width", [25000, 125, 7])
 @pytest.mark.parametrize("hq,hkv,dtype", [(16, 8, torch.bfloat16), (4, 2, torch.bfloat16),
                                           (8, 1, torch.bfloat16), (4, 2, torch.float32)])
 def test_decode_wait_timeout_sets_flag_and_returns(timeout_lib, hq, hkv, dtype, width):
