@@ -672,7 +672,9 @@ int paged_kv_write_rope(const void* k, int64_t k_stride, const void* v, int64_t 
  * rotated first where rope is not NULL (then also the queries, as above).  Arguments and
  * flags as in paged_kv_write_rope.
  * The tokens of a call that lie in one page of one sequence follow one another, in
- * ascending positions.  With a the largest finite magnitude among their values of a head
+ * ascending positions; rows that are not written (padding, a sequence or position past the
+ * table) may stand between them, a token of another sequence or page may not.
+ * With a the largest finite magnitude among their values of a head
  * they need the least power of two n >= 2^-100 with a <= 448 n.  If they begin the page
  * (the first of them is at a multiple of block_size) its scale becomes s = n, whatever
  * it was.  Else s = max(n, the least power of two >= the old scale), and where that

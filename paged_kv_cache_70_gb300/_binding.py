@@ -1024,7 +1024,7 @@ def paged_kv_write_q8(k: torch.Tensor, v: torch.Tensor, block_table: torch.Tenso
                       interleaved: bool = False) -> torch.Tensor | None:
     """In-place write of k/v [N, Hkv, d] rows (fp32 or bf16) into 8-bit pools
     (q8_cache_shape) at their positions, with the pages' scales; the tokens of one
-    page follow one another.  With cos_sin, k and q are rotated first, as in
+    page follow one another, padding between them or not.  With cos_sin, k and q are rotated first, as in
     paged_kv_write_rope."""
     return (_native_module or _native()).write(
         k, v, cos_sin, block_table, token_seq, token_pos, k_cache, v_cache, k_scale, v_scale, q,

@@ -7,8 +7,9 @@
 // front of them become e4m3(code * (old / s)): a shift of the exponent, which is exact
 // until a code gets below 2^-6.  New codes are e4m3(x / s).  A power of two makes both
 // divisions exact, so that a value is rounded once.  Tokens of one page follow one
-// another in the list (a run); a run is found by its first token, which differs from
-// the token before it in sequence or page.
+// another in the list (a run), with rows that are not written between them or not; a run is
+// found by its first token, which differs in sequence or page from the last one before it
+// that has a place.
 //
 // What bounds it: bytes for long runs, the chain token -> page -> rows -> angles for
 // single tokens.  A CTA looks at 256 tokens at once, one per thread, for one head of K or
@@ -23,13 +24,15 @@
 // with the queries: 54 us (4630 GB/s, 0.69 of the measured copy rate; pages of 16 48 us, of
 // 64 57).  The values alone, without rotation and queries, take 36 of them: CTAs that start
 // together load together and then compute together, so that the time is the sum of both,
-// and much of the instructions is not the arithmetic's.  64 single tokens: 4 us beyond an
-// empty graph, 256 7.
+// and much of the instructions is not the arithmetic's.  A run that tokens without a place
+// stand within is looked up row by row: with 5 % of them anywhere among these rows 97 us.
+// 64 single tokens: 4 us beyond an empty graph, 256 8; 64 and 448 padding rows behind them 6.
 // Read: row n of the outputs is code * scale at slot_mapping[n], in fp32 and then in the
 // output's type; zeros for a negative slot.  34,567 rows of 8 x 128 to bf16, 212.5 MB: 33.0
 // us, 6440 GB/s (0.96 of the measured copy rate).
 #include <algorithm>
 #include <atomic>
+#include <type_traits>
 
 #include "launch.h"
 #include "q8.cuh"
@@ -218,24 +221,203 @@ __device__ __forceinline__ float largest(const RawUnit<true>& r) {
     return m;
 }
 
-// The runs (the tokens of one sequence on one page) that begin at tokens n0 .. n0 + 255,
-// a CTA's window
+// The runs (the tokens of one sequence on one page) that begin at tokens n0 .. n0 + 255, a
+// CTA's window.  Tokens without a place (padding, a sequence or position past the table) are
+// passed over: those in front of and behind them are one run, since two that had a page
+// between them would both set its scale and shift its codes, at the same time.
 constexpr int kWindow = kWarps * 32;
+constexpr int kFar = 8 * kWindow;  // tokens that are looked at at once behind it
 struct Runs {
-    uint32_t starts[kWarps], goes_on[kWarps];  // tokens that begin a run, and that continue one
-    uint32_t behind[kWarps];                   // tokens behind the window that continue its last
-    int32_t first[kWindow], page[kWindow], len[kWindow];  // of each (page below 0: not in the pool)
+    // tokens that begin a run, and that go on with the run of the one directly before them
+    uint32_t starts[kWarps], goes_on[kWarps];
+    // tokens behind the window: those that go on with its last run; others that have a place
+    uint32_t behind[kFar / 32], other[kFar / 32];
+    int32_t first[kWindow], page[kWindow];  // of each run (page below 0: not in the pool)
+    int32_t len[kWindow];                   // tokens to its last, those passed over as well
+    bool gaps[kWindow];                     // some were passed over
+    bool open;                              // the last run may go on farther behind
+    // where tokens are passed over: the window's, and which of them have a place
+    int32_t seq[kWindow], pos[kWindow];
+    uint32_t placed[kWarps];
 };
 
-// how many of a window's tokens from `at` on have their bit set without a gap
+// of `words`: how many bits from `at` on are set without a gap; the first one set from `at`
+// on (N: none); the last one set below `end` (-1: none)
+template <int N>
 __device__ __forceinline__ int bits_from(const uint32_t* words, int at) {
     int end = at;
-    while (end < kWindow) {
+    while (end < N) {
         const uint32_t rest = ~words[end >> 5] >> (end & 31);
         if (rest) return end + __ffs(rest) - 1 - at;
         end = (end | 31) + 1;
     }
-    return kWindow - at;
+    return N - at;
+}
+template <int N>
+__device__ __forceinline__ int first_from(const uint32_t* words, int at) {
+    while (at < N) {
+        const uint32_t rest = words[at >> 5] >> (at & 31);
+        if (rest) return at + __ffs(rest) - 1;
+        at = (at | 31) + 1;
+    }
+    return N;
+}
+__device__ __forceinline__ int last_below(const uint32_t* words, int end) {
+    while (end > 0) {
+        const uint32_t rest = words[(end - 1) >> 5] << (31 - ((end - 1) & 31));
+        if (rest) return end - 1 - __clz(rest);
+        end = (end - 1) & ~31;
+    }
+    return -1;
+}
+
+__device__ __forceinline__ int32_t block_of(const NewTokens& t, int32_t p) {
+    return (int32_t)t.block.quot((uint32_t)max(p, 0));
+}
+__device__ __forceinline__ bool has_place(const NewTokens& t, int32_t s, int32_t p) {
+    return s >= 0 && s < t.num_seqs && p >= 0 && block_of(t, p) < t.max_blocks;
+}
+// sequence and position of token m, -1 where there is none
+__device__ __forceinline__ void load_token(const NewTokens& t, int64_t m, int32_t& s, int32_t& p) {
+    s = p = -1;
+    if (m >= 0 && m < t.num) {
+        s = __ldg(t.seq + m);
+        p = __ldg(t.pos + m);
+    }
+}
+// how many runs begin in the window, and the number of the one that this thread's token would
+// begin
+__device__ __forceinline__ int count_runs(const Runs* w, int* k) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    int total = 0;
+    *k = __popc(w->starts[warp] & ((1u << lane) - 1));
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        const int m = __popc(w->starts[i]);
+        total += m;
+        *k += i < warp ? m : 0;
+    }
+    return total;
+}
+
+// The same over the words of kFar tokens, by a warp: the first bit set of words ^ flip, and the
+// last one set below `end`
+__device__ __forceinline__ int first_of_far(const uint32_t* words, uint32_t flip) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = 0; i < kFar / 1024; ++i) {
+        const uint32_t x = words[32 * i + lane] ^ flip;
+        const uint32_t some = __ballot_sync(0xffffffffu, x != 0);
+        if (some) {
+            const int at = __ffs(some) - 1;
+            return 1024 * i + 32 * at + __ffs(__shfl_sync(0xffffffffu, x, at)) - 1;
+        }
+    }
+    return kFar;
+}
+__device__ __forceinline__ int last_of_far(const uint32_t* words, int end) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int i = kFar / 1024 - 1; i >= 0; --i) {
+        const int left = end - 1024 * i - 32 * lane;  // bits of this lane's word below `end`
+        uint32_t x = left > 0 ? words[32 * i + lane] : 0;
+        if (left > 0 && left < 32) x &= (1u << left) - 1;
+        const uint32_t some = __ballot_sync(0xffffffffu, x != 0);
+        if (some) {
+            const int at = 31 - __clz(some);
+            return 1024 * i + 32 * at + 31 - __clz(__shfl_sync(0xffffffffu, x, at));
+        }
+    }
+    return -1;
+}
+
+// Length and gaps of the window's last run, number `run`, that may go on behind the window.
+// (Rare, as what follows: kept out of the registers of what runs every time.)
+__device__ __noinline__ void follow_run(const NewTokens& t, int64_t n0, int run, Runs* w) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t from = n0 + w->first[run];
+    const int32_t sl = __ldg(t.seq + from), bl = block_of(t, __ldg(t.pos + from));
+    bool open = true;
+    for (int64_t m = n0 + kWindow; open && m < t.num; m += kFar) {
+        int32_t s[kFar / kWindow], p[kFar / kWindow];
+#pragma unroll
+        for (int i = 0; i < kFar / kWindow; ++i)
+            load_token(t, m + i * kWindow + tid, s[i], p[i]);
+#pragma unroll
+        for (int i = 0; i < kFar / kWindow; ++i) {
+            const bool has = has_place(t, s[i], p[i]);
+            const bool on = has && s[i] == sl && block_of(t, p[i]) == bl;
+            const uint32_t ons = __ballot_sync(0xffffffffu, on);
+            const uint32_t others = __ballot_sync(0xffffffffu, has && !on);
+            if (lane == 0) {
+                w->behind[i * kWarps + warp] = ons;
+                w->other[i * kWarps + warp] = others;
+            }
+        }
+        __syncthreads();
+        const int stop = first_of_far(w->other, 0u);
+        open = stop == kFar;
+        const int more = last_of_far(w->behind, stop) + 1;
+        const bool gaps = first_of_far(w->behind, ~0u) < more;
+        if (tid == 0 && more > 0) {
+            if (from + w->len[run] < m || gaps) w->gaps[run] = true;
+            w->len[run] = (int32_t)(m + more - from);
+        }
+        __syncthreads();
+    }
+}
+
+// find_runs where a token with a place stands behind one without: a run goes on from the last
+// token before that has one, however far that is.
+__device__ __noinline__ int find_runs_over(const NewTokens& t, int64_t n0, unsigned int* err,
+                                           Runs* w) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int32_t s, p, s1, p1;  // this token, and the last before it
+    load_token(t, n0 + tid, s, p);
+    load_token(t, n0 - 1, s1, p1);
+    const bool placed = has_place(t, s, p);
+    w->seq[tid] = s;
+    w->pos[tid] = p;
+    const uint32_t mine = __ballot_sync(0xffffffffu, placed);
+    if (lane == 0) w->placed[warp] = mine;
+    __syncthreads();
+    // (in front of the window: every warp for itself, 128 tokens at once)
+    for (int64_t end = n0 - 1; end > 0 && !has_place(t, s1, p1); end -= 128) {
+        int32_t ss[4], pp[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) load_token(t, end - 1 - 32 * i - lane, ss[i], pp[i]);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t some = __ballot_sync(0xffffffffu, has_place(t, ss[i], pp[i]));
+            if (some && !has_place(t, s1, p1)) {
+                s1 = __shfl_sync(0xffffffffu, ss[i], __ffs(some) - 1);
+                p1 = __shfl_sync(0xffffffffu, pp[i], __ffs(some) - 1);
+            }
+        }
+    }
+    const int at = last_below(w->placed, tid);
+    if (at >= 0) {
+        s1 = w->seq[at];
+        p1 = w->pos[at];
+    }
+    const bool begins = placed && !(has_place(t, s1, p1) && s1 == s &&
+                                    block_of(t, p1) == block_of(t, p));
+    const int32_t page = begins ? token_page(t, s, p, err) : -1;
+    const uint32_t starts = __ballot_sync(0xffffffffu, begins);
+    if (lane == 0) w->starts[warp] = starts;
+    __syncthreads();
+    int k;
+    const int total = count_runs(w, &k);
+    if (begins) {
+        const int end = last_below(w->placed, first_from<kWindow>(w->starts, tid + 1)) + 1;
+        w->first[k] = tid;
+        w->page[k] = page;
+        w->len[k] = end - tid;
+        w->gaps[k] = bits_from<kWindow>(w->placed, tid) < end - tid;
+    }
+    __syncthreads();
+    if (total > 0) follow_run(t, n0, total - 1, w);
+    return total;
 }
 
 // One thread looks at each token and at one behind the window; returns how many runs.
@@ -263,51 +445,43 @@ __device__ __forceinline__ int find_runs(const NewTokens& t, const RopeTable& ta
         p1 = n > 0 && n <= t.num ? __ldg(t.pos + n - 1) : -1;
     }
     if (n < t.num) token_ok(t, table, s, p, rp, err);
-    auto block = [&](int32_t x) { return (int32_t)t.block.quot((uint32_t)max(x, 0)); };
-    const bool placed = s >= 0 && s < t.num_seqs && p >= 0 && block(p) < t.max_blocks;
-    const bool on = placed && s1 == s && p1 >= 0 && block(p1) == block(p);
+    const bool placed = has_place(t, s, p);
+    const bool on = placed && s1 == s && p1 >= 0 && block_of(t, p1) == block_of(t, p);
     const bool begins = placed && !on;
-    const int32_t page = begins ? token_page(t, s, p, err) : -1;
+    int32_t page = -1;
+    bool over = false;
+    if (begins) {
+        page = token_page(t, s, p, err);
+        over = n > 0 && !has_place(t, s1, p1);
+    }
     const uint32_t starts = __ballot_sync(0xffffffffu, begins);
     const uint32_t goes_on = __ballot_sync(0xffffffffu, on);
     const uint32_t behind = __ballot_sync(0xffffffffu, s2 >= 0 && s2 == sl && p2 >= 0 && pl >= 0 &&
-                                                           block(p2) == block(pl));
+                                                           block_of(t, p2) == block_of(t, pl));
     if (lane == 0) {
         w->starts[warp] = starts;
         w->goes_on[warp] = goes_on;
         w->behind[warp] = behind;
     }
-    __syncthreads();
-    int k = __popc(starts & ((1u << lane) - 1)), total = 0;
-#pragma unroll
-    for (int i = 0; i < kWarps; ++i) {
-        const int m = __popc(w->starts[i]);
-        total += m;
-        k += i < warp ? m : 0;
-    }
+    if (__syncthreads_or(over)) return find_runs_over(t, n0, err, w);
+    int k;
+    const int total = count_runs(w, &k);
     if (begins) {
-        int len = 1 + bits_from(w->goes_on, tid + 1);
-        if (tid + len == kWindow) {
-            len += bits_from(w->behind, 0);
-        }
+        int len = 1 + bits_from<kWindow>(w->goes_on, tid + 1);
+        if (tid + len == kWindow) len += bits_from<kWindow>(w->behind, 0);
         w->first[k] = tid;
         w->page[k] = page;
         w->len[k] = len;
+        w->gaps[k] = false;
+        if (k == total - 1) {  // does it end behind the window, with a token that has a place?
+            const int end = tid + len;
+            w->open = n0 + kWindow < t.num && n0 + end < t.num &&
+                      (end < kWindow || end == 2 * kWindow ||
+                       !has_place(t, __ldg(t.seq + n0 + end), __ldg(t.pos + n0 + end)));
+        }
     }
     __syncthreads();
-    if (t.block.d <= kWindow || total == 0) return total;
-    // larger pages: the last run may go on for windows
-    int more = w->first[total - 1] + w->len[total - 1] == 2 * kWindow ? kWindow : 0;
-    for (int64_t m = n + 2 * kWindow; more == kWindow; m += kWindow) {
-        const bool same = m < t.num && __ldg(t.seq + m) == sl && __ldg(t.pos + m) >= 0 &&
-                          block(__ldg(t.pos + m)) == block(pl);
-        const uint32_t words = __ballot_sync(0xffffffffu, same);
-        if (lane == 0) w->behind[warp] = words;
-        __syncthreads();
-        more = bits_from(w->behind, 0);
-        if (tid == 0) w->len[total - 1] += more;
-        __syncthreads();
-    }
+    if (total > 0 && w->open) follow_run(t, n0, total - 1, w);
     return total;
 }
 
@@ -350,11 +524,12 @@ struct Head {
     int u, da, db;              // this lane's unit and its chunks
 };
 
-// The run of `len` tokens from n on, in `page`, written by W warps of which this is
-// the rank-th; W is 1 or all of the CTA's.
+// The run of `len` tokens from n on, in `page`, written by W warps of which this is the
+// rank-th (W is 1, 2 or all of the CTA's); `gaps`: some of the tokens are passed over.
 template <int D, bool F32, bool MIX, bool ROT, int W>
 __device__ __forceinline__ void write_run(const Q8WriteArgs& a, const Head& hd, int64_t n,
-                                          int32_t len, int32_t page, int rank, uint32_t* red) {
+                                          int32_t len, bool gaps, int32_t page, int rank,
+                                          uint32_t* red) {
     constexpr int U = D / 16, RS = 32 / U;  // lanes per row, rows per step
     constexpr int step = W * RS;
     constexpr uint32_t kNext = (F32 ? 4 : 2) * kPiece;  // a thread's next slot
@@ -402,135 +577,143 @@ __device__ __forceinline__ void write_run(const Q8WriteArgs& a, const Head& hd, 
         }
         asm volatile("cp.async.commit_group;" ::: "memory");
     };
-    // The usual run is one of consecutive positions, all of them in the table: then
-    // nothing is looked up row by row.
     const int32_t rp0 = a.table.rot ? __ldg(rope_pos) : 0;
-    bool plain = true;
-    // the position that row r is rotated by (0 without a rotation), below 0: none, the
-    // row is not written
-    auto turn_of = [&](int32_t r) {
-        if (!a.table.rot) return 0;
-        const int32_t rp = plain ? rp0 + r : __ldg(rope_pos + r);
-        return plain || rp < a.table.positions ? rp : -1;
-    };
-    // rotates the rows from base on in place (to odd where bf16 holds them: a further
-    // rounding to 4 bits then gives what one rounding gives); the largest magnitude's
-    // bits + 1
-    auto rotate_rows = [&](int32_t base) {
-        uint32_t top = 0, slot = hd.slot;
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        #pragma unroll 1
-        for (int32_t r = base + r0; r < min(len, base + cap); r += step, slot += kNext) {
-            const int32_t rp = turn_of(r);
-            if (rp < 0) continue;
-            RawUnit<F32> x = staged_unit<F32>(slot);
-            float m;  // (no maximum here takes notice of a NaN)
-            if (spins) {
-                const float4* const c =
-                    reinterpret_cast<const float4*>(a.table.cos_sin + (int64_t)rp * a.table.rot + 8 * hd.u);
-                const float4* const q = c + a.table.rot / 8;
-                m = rotate_half<F32, MIX>(x, 0, __ldg(c), __ldg(q));
-                m = fmaxf(m, rotate_half<F32, MIX>(x, 1, __ldg(c + 1), __ldg(q + 1)));
-                restage_unit<F32>(slot, x);
-            } else {
-                m = largest(x);
-            }
-            top = max(top, __float_as_uint(m) + 1);
+    fetch(0);
+    // The usual run is one of consecutive positions, all of them in the table: then
+    // nothing is looked up row by row.  (What follows is compiled for each kind by itself:
+    // together, in the same registers, the usual ones took 3 to 6 us more of 60.)
+    bool plain = !gaps && rp0 >= 0;
+    for (int32_t r = r0; r < len; r += step) {
+        plain &= __ldg(pos + r) - p == r;
+        if (a.table.rot) {
+            const int32_t rp = __ldg(rope_pos + r);
+            plain &= rp - rp0 == r && rp < a.table.positions;
         }
-        return top;
-    };
-    uint32_t top = 0;
-    for (int32_t base = 0; base < len; base += cap) {
-        fetch(base);
-        if (base == 0) {
-            for (int32_t r = r0; r < len; r += step) {
-                plain &= __ldg(pos + r) - p == r;
-                if (a.table.rot) {
-                    const int32_t rp = __ldg(rope_pos + r);
-                    plain &= rp - rp0 == r && rp < a.table.positions;
+    }
+    auto rest = [&](auto by_row) {
+        constexpr bool PLAIN = !decltype(by_row)::value;
+        // the position that row r is rotated by (0 without a rotation), below 0: none, the
+        // row is not written
+        auto turn_of = [&](int32_t r) {
+            if (PLAIN) return a.table.rot ? rp0 + r : 0;
+            const int32_t pr = __ldg(pos + r);
+            // (a token that is passed over)
+            if (__ldg(a.tok.seq + n + r) != __ldg(a.tok.seq + n) || pr < p0 || pr - p0 >= B)
+                return -1;
+            if (!a.table.rot) return 0;
+            const int32_t rp = __ldg(rope_pos + r);
+            return rp < a.table.positions ? rp : -1;
+        };
+        // rotates the rows from base on in place (to odd where bf16 holds them: a further
+        // rounding to 4 bits then gives what one rounding gives); the largest magnitude's
+        // bits + 1
+        auto rotate_rows = [&](int32_t base) {
+            uint32_t top = 0, slot = hd.slot;
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            #pragma unroll 1
+            for (int32_t r = base + r0; r < min(len, base + cap); r += step, slot += kNext) {
+                const int32_t rp = turn_of(r);
+                if (rp < 0) continue;
+                RawUnit<F32> x = staged_unit<F32>(slot);
+                float m;  // (no maximum here takes notice of a NaN)
+                if (spins) {
+                    const float4* const c = reinterpret_cast<const float4*>(
+                        a.table.cos_sin + (int64_t)rp * a.table.rot + 8 * hd.u);
+                    const float4* const q = c + a.table.rot / 8;
+                    m = rotate_half<F32, MIX>(x, 0, __ldg(c), __ldg(q));
+                    m = fmaxf(m, rotate_half<F32, MIX>(x, 1, __ldg(c + 1), __ldg(q + 1)));
+                    restage_unit<F32>(slot, x);
+                } else {
+                    m = largest(x);
+                }
+                top = max(top, __float_as_uint(m) + 1);
+            }
+            return top;
+        };
+        uint32_t top = 0;
+        for (int32_t base = 0; base < len; base += cap) {
+            if (base > 0) fetch(base);
+            top = max(top, rotate_rows(base));
+        }
+        top = run_max(top);
+        if (top == 0) return;  // no row to write
+        const bool inf = top - 1 == 0x7f800000u;
+        if (inf) {  // once more over the finite ones
+            top = 1;
+            for (int32_t base = 0; base < len; base += cap) {
+                if (len > cap) {
+                    fetch(base);
+                    rotate_rows(base);
+                }
+                uint32_t slot = hd.slot;
+#pragma unroll 1
+                for (int32_t r = base + r0; r < min(len, base + cap); r += step, slot += kNext) {
+                    float x[16];
+                    if (turn_of(r) < 0) continue;
+                    widen_unit<F32>(staged_unit<F32>(slot), x);
+#pragma unroll
+                    for (int e = 0; e < 16; ++e)
+                        if (fabsf(x[e]) < INFINITY) top = max(top, __float_as_uint(fabsf(x[e])) + 1);
                 }
             }
-            plain = __all_sync(0xffffffffu, plain && rp0 >= 0);
+            top = run_max(top);
         }
-        top = max(top, rotate_rows(base));
-    }
-    top = run_max(top);
-    if (top == 0) return;  // no row to write
-    const bool inf = top - 1 == 0x7f800000u;
-    if (inf) {  // once more over the finite ones
-        top = 1;
+        float s = scale_for(__uint_as_float(top - 1));
+        unsigned char* const head = hd.pool + page * hd.page_bytes;
+        if (front > 0) {
+            const float was = scale_up(old);
+            s = was <= s ? s : was;  // (NaN stays)
+            if (s != old) {
+                const float ratio = old * __frcp_rn(s);
+                rescale(head, (int64_t)front * (D / 16), ratio, rank * 32 + lane, W * 32);
+            }
+        }
+        // (all warps of the run have read the old scale: they met in run_max)
+        if (rank == 0 && lane == 0) *sp = s;
+        const float inv = __frcp_rn(s);
         for (int32_t base = 0; base < len; base += cap) {
             if (len > cap) {
                 fetch(base);
                 rotate_rows(base);
             }
             uint32_t slot = hd.slot;
-#pragma unroll 1
+            #pragma unroll 1
             for (int32_t r = base + r0; r < min(len, base + cap); r += step, slot += kNext) {
-                float x[16];
                 if (turn_of(r) < 0) continue;
+                const int32_t at = PLAIN ? front + r : __ldg(pos + r) - p0;
+                float x[16];
                 widen_unit<F32>(staged_unit<F32>(slot), x);
+                if (inf) {
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
-                    if (fabsf(x[e]) < INFINITY) top = max(top, __float_as_uint(fabsf(x[e])) + 1);
-            }
-        }
-        top = run_max(top);
-    }
-    float s = scale_for(__uint_as_float(top - 1));
-    unsigned char* const head = hd.pool + page * hd.page_bytes;
-    if (front > 0) {
-        const float was = scale_up(old);
-        s = was <= s ? s : was;  // (NaN stays)
-        if (s != old) {
-            const float ratio = old * __frcp_rn(s);
-            rescale(head, (int64_t)front * (D / 16), ratio, rank * 32 + lane, W * 32);
-        }
-    }
-    // (all warps of the run have read the old scale: they met in run_max)
-    if (rank == 0 && lane == 0) *sp = s;
-    const float inv = __frcp_rn(s);
-    for (int32_t base = 0; base < len; base += cap) {
-        if (len > cap) {
-            fetch(base);
-            rotate_rows(base);
-        }
-        uint32_t slot = hd.slot;
-        #pragma unroll 1
-        for (int32_t r = base + r0; r < min(len, base + cap); r += step, slot += kNext) {
-            if (turn_of(r) < 0) continue;
-            const int32_t at = plain ? front + r : __ldg(pos + r) - p0;
-            float x[16];
-            widen_unit<F32>(staged_unit<F32>(slot), x);
-            if (inf) {
+                    for (int e = 0; e < 16; ++e) x[e] = fmaf(x[e], 0.f, x[e]);  // to NaN
+                }
+                uint32_t w[4];
 #pragma unroll
-                for (int e = 0; e < 16; ++e) x[e] = fmaf(x[e], 0.f, x[e]);  // to NaN
-            }
-            uint32_t w[4];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const float2 y = fmul2(make_float2(x[4 * e], x[4 * e + 1]), make_float2(inv, inv));
-                const float2 z = fmul2(make_float2(x[4 * e + 2], x[4 * e + 3]),
-                                       make_float2(inv, inv));
-                w[e] = e4m3x2(y.x, y.y) | e4m3x2(z.x, z.y) << 16;
-            }
-            unsigned char* const to = head + (int64_t)at * D;
-            if (hd.db == hd.da + 8) {
-                *reinterpret_cast<uint4*>(to + hd.da) = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-                *reinterpret_cast<uint2*>(to + hd.da) = make_uint2(w[0], w[1]);
-                *reinterpret_cast<uint2*>(to + hd.db) = make_uint2(w[2], w[3]);
+                for (int e = 0; e < 4; ++e) {
+                    const float2 y = fmul2(make_float2(x[4 * e], x[4 * e + 1]), make_float2(inv, inv));
+                    const float2 z = fmul2(make_float2(x[4 * e + 2], x[4 * e + 3]),
+                                           make_float2(inv, inv));
+                    w[e] = e4m3x2(y.x, y.y) | e4m3x2(z.x, z.y) << 16;
+                }
+                unsigned char* const to = head + (int64_t)at * D;
+                if (hd.db == hd.da + 8) {
+                    *reinterpret_cast<uint4*>(to + hd.da) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+                    *reinterpret_cast<uint2*>(to + hd.da) = make_uint2(w[0], w[1]);
+                    *reinterpret_cast<uint2*>(to + hd.db) = make_uint2(w[2], w[3]);
+                }
             }
         }
-    }
+    };
+    if (__all_sync(0xffffffffu, plain)) rest(std::false_type{});
+    else rest(std::true_type{});
 }
 
 template <int D, bool F32, bool MIX, bool ROT, int TEAM>
-__device__ __forceinline__ void write_runs(const Q8WriteArgs& a, uint32_t cta) {
+__device__ __forceinline__ void write_runs(const Q8WriteArgs& a, uint32_t cta, Runs& runs,
+                                           uint32_t* red) {
     constexpr int U = D / 16, RS = 32 / U;
     extern __shared__ __align__(16) unsigned char stage[];
-    __shared__ uint32_t red[kWarps];
-    __shared__ Runs runs;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const bool is_v = cta & 1;
     const int h = (int)((cta >> 1) % (uint32_t)a.tok.hkv);
@@ -553,26 +736,29 @@ __device__ __forceinline__ void write_runs(const Q8WriteArgs& a, uint32_t cta) {
     // every parts-th run, one per warp, then those of more rows than a warp holds, by teams
     for (int k = part + warp * a.parts; k < total; k += kWarps * a.parts)
         if (runs.page[k] >= 0 && (TEAM == 1 || runs.len[k] <= RS * a.steps))
-            write_run<D, F32, MIX, ROT, 1>(a, hd, n0 + runs.first[k], runs.len[k], runs.page[k], 0,
-                                           nullptr);
+            write_run<D, F32, MIX, ROT, 1>(a, hd, n0 + runs.first[k], runs.len[k], runs.gaps[k],
+                                           runs.page[k], 0, nullptr);
     if constexpr (TEAM > 1) {
         const int team = TEAM == kWarps ? 0 : warp / TEAM, rank = TEAM == kWarps ? warp : warp % TEAM;
         for (int k = part + team * a.parts; k < total; k += kWarps / TEAM * a.parts)
             if (runs.page[k] >= 0 && runs.len[k] > RS * a.steps)
                 write_run<D, F32, MIX, ROT, TEAM>(a, hd, n0 + runs.first[k], runs.len[k],
-                                                  runs.page[k], rank, red + team * TEAM);
+                                                  runs.gaps[k], runs.page[k], rank,
+                                                  red + team * TEAM);
     }
 }
 
 // TEAM: warps that take a run of more rows than one holds
 template <int D, bool F32, bool MIX, int TEAM>
-__global__ void __launch_bounds__(kWarps * 32, 3) q8_write_kernel(const Q8WriteArgs a) {
+__global__ void __launch_bounds__(kWarps * 32, 3) q8_write_kernel(const __grid_constant__ Q8WriteArgs a) {
     PKV_DEPENDENT_PROLOGUE();
     // CTAs of K and V lie among those of the queries, which fill the GPU behind them
     const uint32_t kv = (uint32_t)min((blockIdx.x * a.kv_step) >> 32, (uint64_t)a.kv_ctas);
     if (kv < a.kv_ctas && ((blockIdx.x + 1ull) * a.kv_step) >> 32 > kv) {
-        if (a.table.rot && !(kv & 1)) write_runs<D, F32, MIX, true, TEAM>(a, kv);
-        else write_runs<D, F32, MIX, false, TEAM>(a, kv);
+        __shared__ Runs runs;
+        __shared__ uint32_t red[kWarps];
+        if (a.table.rot && !(kv & 1)) write_runs<D, F32, MIX, true, TEAM>(a, kv, runs, red);
+        else write_runs<D, F32, MIX, false, TEAM>(a, kv, runs, red);
         return;
     }
     const int64_t id = (int64_t)(blockIdx.x - kv) * kWarps + (threadIdx.x >> 5);
