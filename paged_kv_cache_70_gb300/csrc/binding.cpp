@@ -107,20 +107,35 @@ pkv_geom q8_geom(const at::Tensor& pool) {
     return pkv_geom{(int32_t)pool.size(1), (int32_t)pool.size(1), (int32_t)pool.size(3),
                     (int32_t)pool.size(2), pool.size(0), PKV_Q8};
 }
-struct Q8Pools {
+struct Pools {
     void *k, *v;
-    float *k_scale, *v_scale;
+    float *k_scale, *v_scale;  // of 8-bit pools
 };
-Q8Pools q8_pools(const at::Tensor& k, const at::Tensor& v, const at::Tensor& ks,
+Pools q8_pools(const at::Tensor& k, const at::Tensor& v, const at::Tensor& ks,
                  const at::Tensor& vs, int index) {
     const bool same = v.sizes() == k.sizes() && ks.dim() == 2 && vs.sizes() == ks.sizes() &&
                       ks.size(0) == k.size(0) && ks.size(1) == k.size(1);
     if (!same) value_error("the pools have one shape and the scales are [num_blocks, Hkv]");
-    return Q8Pools{address(k, "k_cache", index, at::kFloat8_e4m3fn),
+    return Pools{address(k, "k_cache", index, at::kFloat8_e4m3fn),
                    address(v, "v_cache", index, at::kFloat8_e4m3fn),
                    static_cast<float*>(address(ks, "k_scale", index, at::kFloat)),
                    static_cast<float*>(address(vs, "v_scale", index, at::kFloat))};
 }
+
+// Other Python threads run while one of these lives: around allocations and launches, which
+// wait where the launch queue is full or memory has to be freed, perhaps for a host function
+// of the stream that needs Python.  (No Python object is touched meanwhile; the caller holds
+// the arguments.)
+class OthersRun {
+public:
+    OthersRun() : state_(PyEval_SaveThread()) {}
+    ~OthersRun() { PyEval_RestoreThread(state_); }
+    OthersRun(const OthersRun&) = delete;
+    OthersRun& operator=(const OthersRun&) = delete;
+
+private:
+    PyThreadState* state_;
+};
 
 // raises (returns false) for a status
 bool ok(const char* func, int status) {
@@ -181,6 +196,7 @@ PyObject* write_impl(PyObject* const* a) {
     pkv_rope rope{};
     PyObject* result = Py_None;
     at::Tensor made;
+    const at::Tensor* q_like = nullptr;  // q, where q_out is to be made
     if (a[2] == Py_None) {
         if (!q8) value_error("cos_sin is needed (paged_kv_write_positions writes without it)");
         if (a[10] != Py_None || a[11] != Py_None || a[12] != Py_None)
@@ -204,8 +220,7 @@ PyObject* write_impl(PyObject* const* a) {
             g.num_heads = (int32_t)q.size(1);
             rope.q = row_address(q, "q", index, dtype, &rope.q_stride);
             if (a[11] == Py_None) {
-                made = new_tensor(q.sizes(), dtype, index);
-                rope.q_out = row_address(made, "q_out", index, dtype, &rope.q_out_stride);
+                q_like = &q;
             } else {
                 const at::Tensor& out = tensor(a[11], "q_out");
                 if (out.sizes() != q.sizes()) value_error("q_out must have q's shape");
@@ -215,23 +230,28 @@ PyObject* write_impl(PyObject* const* a) {
         }
     }
     const pkv_rope* r = a[2] == Py_None ? nullptr : &rope;
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
-    cudaStream_t stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index);
-    if (q8) {
-        const Q8Pools p = q8_pools(kc, vc, tensor(a[8], "k_scale"), tensor(a[9], "v_scale"), index);
-        if (!ok("paged_kv_write_q8",
-                g_write_q8(kp, k_stride, vp, v_stride, code, r, tp, (int32_t)table.size(1),
-                           (int32_t)table.size(0), sp, pp, n, p.k, p.v, p.k_scale, p.v_scale, &g,
-                           stream)))
-            return nullptr;
-    } else {
-        void* kcp = address(kc, "k_cache", index, kc.scalar_type());
-        void* vcp = address(vc, "v_cache", index, kc.scalar_type());
-        if (!ok("paged_kv_write_rope",
-                g_write_rope(kp, k_stride, vp, v_stride, code, r, tp, (int32_t)table.size(1),
-                             (int32_t)table.size(0), sp, pp, n, slots, kcp, vcp, &g, stream)))
-            return nullptr;
+    Pools p;
+    if (q8)
+        p = q8_pools(kc, vc, tensor(a[8], "k_scale"), tensor(a[9], "v_scale"), index);
+    else
+        p = Pools{address(kc, "k_cache", index, kc.scalar_type()),
+                    address(vc, "v_cache", index, kc.scalar_type()), nullptr, nullptr};
+    const int32_t rows = (int32_t)table.size(0), width = (int32_t)table.size(1);
+    int status;
+    {
+        const OthersRun others;
+        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
+        cudaStream_t stream = c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index);
+        if (q_like) {
+            made = new_tensor(q_like->sizes(), dtype, index);
+            rope.q_out = row_address(made, "q_out", index, dtype, &rope.q_out_stride);
+        }
+        status = q8 ? g_write_q8(kp, k_stride, vp, v_stride, code, r, tp, width, rows, sp, pp, n,
+                                 p.k, p.v, p.k_scale, p.v_scale, &g, stream)
+                    : g_write_rope(kp, k_stride, vp, v_stride, code, r, tp, width, rows, sp, pp, n,
+                                   slots, p.k, p.v, &g, stream);
     }
+    if (!ok(q8 ? "paged_kv_write_q8" : "paged_kv_write_rope", status)) return nullptr;
     return made.defined() ? THPVariable_Wrap(std::move(made)) : same(result);
 }
 
@@ -241,7 +261,7 @@ PyObject* read_q8_impl(PyObject* const* a) {
     const at::Tensor& slots = tensor(a[4], "slot_mapping");
     const int index = device_of(kc, "k_cache");
     const pkv_geom g = q8_geom(kc);
-    const Q8Pools p = q8_pools(kc, vc, tensor(a[2], "k_scale"), tensor(a[3], "v_scale"), index);
+    const Pools p = q8_pools(kc, vc, tensor(a[2], "k_scale"), tensor(a[3], "v_scale"), index);
     const int64_t n = slots.numel();
     const int64_t shape[3] = {n, g.num_kv_heads, g.head_dim};
     at::ScalarType dtype;
@@ -255,18 +275,22 @@ PyObject* read_q8_impl(PyObject* const* a) {
     }
     const int32_t code = dtype_code(dtype);
     if (a[7] != Py_None) out[1] = tensor(a[7], "v_out");
-    for (at::Tensor& t : out)
-        if (!t.defined()) t = new_tensor(at::IntArrayRef(shape, 3), dtype, index);
     for (const at::Tensor& t : out)
-        if (t.sizes() != at::IntArrayRef(shape, 3)) value_error("k_out / v_out must be [N, Hkv, d]");
-    void* kp = address(out[0], "k_out", index, dtype);
-    void* vp = address(out[1], "v_out", index, dtype);
+        if (t.defined() && t.sizes() != at::IntArrayRef(shape, 3))
+            value_error("k_out / v_out must be [N, Hkv, d]");
     const int32_t* sp = int32s(slots, "slot_mapping", index);
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
-    if (!ok("paged_kv_read_q8",
-            g_read_q8(p.k, p.v, p.k_scale, p.v_scale, sp, n, kp, vp, code, &g,
-                      c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index))))
-        return nullptr;
+    int status;
+    {
+        const OthersRun others;
+        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
+        for (at::Tensor& t : out)
+            if (!t.defined()) t = new_tensor(at::IntArrayRef(shape, 3), dtype, index);
+        void* kp = address(out[0], "k_out", index, dtype);
+        void* vp = address(out[1], "v_out", index, dtype);
+        status = g_read_q8(p.k, p.v, p.k_scale, p.v_scale, sp, n, kp, vp, code, &g,
+                           c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index));
+    }
+    if (!ok("paged_kv_read_q8", status)) return nullptr;
     PyObject* pair = PyTuple_New(2);
     if (!pair) return nullptr;
     for (int i = 0; i < 2; ++i)
@@ -296,31 +320,33 @@ PyObject* decode_q8_impl(PyObject* const* a) {
         scale = PyFloat_AsDouble(a[7]);
         if (scale == -1.0 && PyErr_Occurred()) return nullptr;
     }
-    const Q8Pools p = q8_pools(kc, vc, tensor(a[3], "k_scale"), tensor(a[4], "v_scale"), index);
+    const Pools p = q8_pools(kc, vc, tensor(a[3], "k_scale"), tensor(a[4], "v_scale"), index);
     const void* qp = address(q, "q", index, dtype);
     const int32_t* tp = int32s(table, "block_table", index);
     const int32_t* lp = int32s(lens, "cache_seqlens", index);
-    const c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
     at::Tensor out, workspace;
     if (a[8] != Py_None) {
         out = tensor(a[8], "out");
         if (out.sizes() != q.sizes()) value_error("out must have q's shape");
-    } else {
-        out = new_tensor(q.sizes(), dtype, index);
     }
-    void* op = address(out, "out", index, dtype);
     if (a[9] != Py_None) {
         workspace = tensor(a[9], "workspace");
         address(workspace, "workspace", index, workspace.scalar_type());
-    } else {
-        workspace = new_tensor({(int64_t)g_decode_q8_size(batch, code, &g)}, at::kByte, index);
     }
-    if (!ok("paged_decode_q8",
-            g_decode_q8(qp, code, p.k, p.v, p.k_scale, p.v_scale, tp, (int32_t)table.size(1), lp,
-                        batch, (float)scale, op, workspace.data_ptr(),
-                        (size_t)workspace.numel() * workspace.element_size(), &g,
-                        c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index))))
-        return nullptr;
+    int status;
+    {
+        const OthersRun others;
+        const c10::cuda::CUDAGuard guard((c10::DeviceIndex)index);
+        if (!out.defined()) out = new_tensor(q.sizes(), dtype, index);
+        void* op = address(out, "out", index, dtype);
+        if (!workspace.defined())
+            workspace = new_tensor({(int64_t)g_decode_q8_size(batch, code, &g)}, at::kByte, index);
+        status = g_decode_q8(qp, code, p.k, p.v, p.k_scale, p.v_scale, tp, (int32_t)table.size(1),
+                             lp, batch, (float)scale, op, workspace.data_ptr(),
+                             (size_t)workspace.numel() * workspace.element_size(), &g,
+                             c10::cuda::getCurrentCUDAStream((c10::DeviceIndex)index));
+    }
+    if (!ok("paged_decode_q8", status)) return nullptr;
     return a[8] != Py_None ? same(a[8]) : THPVariable_Wrap(std::move(out));
 }
 
