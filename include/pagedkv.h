@@ -712,7 +712,8 @@ int paged_kv_read_q8(const void* k_cache, const void* v_cache, const float* k_sc
 /*
  * paged_decode_q8 -- paged_decode over 8-bit pools: one query per sequence (q, out
  * [batch, Hq, d] of q_dtype, PKV_F32 or PKV_BF16), cache_seqlens[b] keys each, read
- * through block_table row b; 0 when cache_seqlens[b] == 0.  Codes and scales are used
+ * through block_table row b; 0 when cache_seqlens[b] == 0.  block_table may be NULL where
+ * max_blocks_per_seq is 0.  Codes and scales are used
  * as stored; scores, softmax statistics and sums are fp32.
  * Supported: any Hq / Hkv up to 64; head_dim 128 with any block_size (multiples of 8
  * are fastest), 64 with an even one; batch <= 4096; num_blocks * Hkv below 2^31;

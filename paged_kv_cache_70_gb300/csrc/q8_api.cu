@@ -183,8 +183,8 @@ int paged_decode_q8(const void* q, int32_t q_dtype, const void* k_cache, const v
     if (st != PKV_OK) return st;
     if (!elt_size(q_dtype) || batch < 0 || max_blocks_per_seq < 0) return PKV_ERR_INVALID;
     if (batch == 0) return PKV_OK;
-    if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !block_table || !cache_seqlens ||
-        !out)
+    if (!q || !k_cache || !v_cache || !k_scale || !v_scale || !cache_seqlens || !out ||
+        (max_blocks_per_seq > 0 && !block_table))
         return PKV_ERR_INVALID;
     if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
         return PKV_ERR_INVALID;
