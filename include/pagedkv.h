@@ -663,8 +663,9 @@ int paged_kv_write_rope(const void* k, int64_t k_stride, const void* v, int64_t 
  *          of two; the read and the decode take any finite ones.
  * A page is copied by paged_copy_blocks with a geom whose pages have the same number of
  * bytes (e.g. one head, block_size 1, head_dim Hkv * B * d / 2, bf16), its scales by a
- * second call (one head, block_size 1, head_dim Hkv, fp32).  Tokens cannot be moved
- * from page to page (paged_kv_compact): their codes belong to their page's scale.
+ * second call (one head, block_size 1, head_dim Hkv, fp32).  paged_kv_compact does not
+ * take these pools: it moves bytes, and a token's codes would have to be shifted to the
+ * scale of the page that it comes to.
  */
 
 /*

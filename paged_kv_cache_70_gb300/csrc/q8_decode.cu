@@ -39,7 +39,7 @@
 // Measured (bf16 queries, a call among others; of the measured copy rate, 6696 GB/s):
 //   8 sequences of 16 K - 41 K keys, 16 / 8 heads, d = 128, 485 MB     77.5 us  0.93
 //   the same with 64 / 8 heads                                          78.8 us  0.92
-//   64 sequences of 128 - 4096 keys, 16 / 8 heads, B = 16, 278 MB       51.1 us  0.81
+//   64 sequences of 128 - 4096 keys, 16 / 8 heads, B = 16, 278 MB       50.8 us  0.82
 //   one of 7777 keys, 32 / 4 heads, d = 64                               8.4 us
 // From one to four times the long contexts the time grows by 6980 GB/s, above the copy
 // rate.  What stands around the stream: ~5 us to the first copy (wait for the launch, plan,
@@ -1013,7 +1013,10 @@ bool plan_q8_decode(const DeviceInfo& dev, int32_t batch, int32_t max_blocks, in
         return true;
     }
     // A cluster: where the second kernel costs more (1.6 us and the longer the more sequences it
-    // has, or 70 KB and 3 KB each of what an SM streams) than SMs without work do.  At 16 / 8 heads, d = 128, cluster and split: one sequence of 1000 keys
+    // has, or 70 KB and 3 KB each of what an SM streams) than SMs without work do.  The lengths
+    // are not known here, and the figures are of sequences that fill the table; one long among
+    // short ones is better split (one of 8000 and three of 100 keys 15.4 us, split 13.2).  At
+    // 16 / 8 heads, d = 128, cluster and split: one sequence of 1000 keys
     // 7.3 and 8.5 us, 4000 9.1 and 9.1, 8000 12.1 and 10.4; 4 of 2000 9.5 and 10.9, of 16000 29.2
     // and 29.4; 16 of 300 7.9 and 10.0, of 2000 18.0 and 20.0; at 32 / 4 heads of 64 one of 12000
     // 8.8 and 9.8, of 16000 10.4 and 9.8, 16 of 1000 7.9 and 11.5.
